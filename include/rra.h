@@ -41,11 +41,12 @@
  *    RRA_ERR_UNSUPPORTED; a failed launch returns RRA_ERR_CUDA.  Errors the
  *    device detects while running (a wait that ran out of time) are latched
  *    in the communicator and reported by rra_comm_status().
- *  - Inputs must be finite: NaN or infinity in an input is outside the
- *    contract (results unspecified, no fault).
+ *  - Inputs of the collectives and codecs must be finite: NaN or infinity in
+ *    an input is outside the contract (results unspecified, no fault).
  *  - Nothing on these paths allocates memory except rra_comm_create, and
- *    rra_sparse_encode / rra_sparse_decode when a stream's scratch is
- *    smaller than the call needs (its first call, or a larger n; see there).
+ *    rra_sparse_encode / rra_sparse_decode and the training-step operators
+ *    when a stream's scratch is smaller than the call needs (its first call,
+ *    or a larger one; see there).
  */
 #ifndef RRA_H
 #define RRA_H
@@ -582,6 +583,134 @@ rra_status rra_codec_advise_op(rra_comm *comm, int op, int root, const void *con
  * which it has a child (L = ceil(log2 N)); the compressed broadcast at any
  * step >= 1.  rank < 0 disables.  The setting applies to one call only. */
 rra_status rra_debug_withhold(rra_comm *comm, int rank, int step);
+
+/*
+ * Training-step operators around the ring: the layers whose gradients the
+ * codecs are made for (a row-sparse embedding gradient, the small gradients
+ * of layer norm's weights) and the clipping of the reduced gradients.  The
+ * pages have no counterpart; the formulas are the usual ones and stand at
+ * each function.
+ *
+ * Conventions beside those above:
+ *  - Buffers need only the alignment of their elements; 16-byte aligned
+ *    buffers and row lengths run fastest.
+ *  - An empty call (no tensors, tokens or rows) is valid: pointers of empty
+ *    arrays may be NULL, and sums over nothing are zero.
+ *  - All sums and statistics are held in fp32 or more; every result is
+ *    rounded to its type once, to nearest even.  Equal calls give equal bits.
+ *  - Infinities and NaN are carried through as the formulas have it.
+ *  - rra_grad_norm, rra_grad_clip, rra_embedding_grad and
+ *    rra_layer_norm_grad use scratch memory that the library keeps per device
+ *    and stream, allocates with cudaMalloc when a call needs more than it
+ *    holds, and frees never (it at least doubles when it grows).  A call
+ *    that would have to allocate while its stream is being captured returns
+ *    RRA_ERR_INVALID: make one call of that size before the capture.  Graphs
+ *    captured on one stream share its scratch: do not replay two of them, or
+ *    one and a call on that stream, at the same time.
+ */
+
+/* Norms of a list of gradients taken as one vector. */
+typedef enum { RRA_NORM_L2 = 0, RRA_NORM_L1 = 1, RRA_NORM_INF = 2 } rra_norm;
+
+/* Types of token numbers. */
+typedef enum { RRA_I32 = 0, RRA_I64 = 1 } rra_index;
+
+/*
+ * Norm of all elements of ntensors gradients: sqrt(sum g^2), sum |g| or
+ * max |g|.
+ *  grads    HOST array of device pointers; counts and dtypes: HOST arrays of
+ *           the tensors' element counts and types.  Read during the call.
+ *  norm     device fp32[1].
+ * The sum of squares neither overflows nor loses small values: the norm is
+ * finite and exact to fp32 whenever it is an fp32 number.  A NaN anywhere
+ * gives NaN, else an infinity gives infinity.
+ * Errors: RRA_ERR_INVALID (NULL, a bad enum, ntensors < 0, a count above
+ * 2^40), RRA_ERR_NOMEM, RRA_ERR_CUDA.
+ */
+rra_status rra_grad_norm(const void *const *grads, const size_t *counts, const rra_dtype *dtypes,
+                         int ntensors, rra_norm kind, float *norm, void *stream);
+
+/*
+ * Clip gradients to a largest norm: with n the norm above,
+ * c = min(1, max_norm / (n + eps)) (1 when n = 0), out[k] = grads[k] * c.
+ *  out   HOST array of device pointers; out[k] is grads[k] (in place; a c of
+ *        1 then writes nothing) or apart from every gradient and other
+ *        output.  Tensors have their gradient's type.
+ *  norm  device fp32[1], receives n (before clipping).
+ * n is never read on the host.  NaN: n, c and every output are NaN.
+ * An infinite n: c is 0.  Errors: as rra_grad_norm; RRA_ERR_INVALID for a
+ * max_norm or eps that is negative or NaN, an infinite eps, and an output
+ * that overlaps its own gradient in part.
+ */
+rra_status rra_grad_clip(const void *const *grads, void *const *out, const size_t *counts,
+                         const rra_dtype *dtypes, int ntensors, rra_norm kind, float max_norm,
+                         float eps, float *norm, void *stream);
+
+/*
+ * Embedding lookup: out[t, :] = scale * weight[tokens[t], :], in fp32,
+ * rounded to dtype.  weight: vocab rows of dim elements; tokens: ntokens
+ * numbers of type index; out: ntokens rows of dim elements.  A token outside
+ * [0, vocab) gives a row of zeros.
+ * Errors: RRA_ERR_INVALID (NULL, bad enums, vocab or dim 0, ntokens or vocab
+ * above 2^31 - 1, dim above 2^32, out overlapping weight or tokens),
+ * RRA_ERR_CUDA.
+ */
+rra_status rra_embedding(const void *weight, const void *tokens, size_t ntokens, size_t vocab,
+                         size_t dim, rra_dtype dtype, rra_index index, float scale, void *out,
+                         void *stream);
+
+/*
+ * Gradient of the embedding lookup:
+ *   dweight[v, :] = scale * (sum over t with tokens[t] = v of dout[t, :])
+ * for every row v of the table; rows of no token are zero.
+ *  dout        ntokens rows of dim elements of type dout_t.
+ *  padding     a token that gets no gradient (negative: none).  Tokens outside
+ *              [0, vocab) get none either.
+ *  dweight     vocab rows of dim elements of type dweight_t: dout_t or
+ *              RRA_F32 (else RRA_ERR_UNSUPPORTED).
+ *  accumulate  nonzero: the sum is added to dweight's value in fp32; rows
+ *              of no token are left as they are.
+ * The tokens are sorted, and a row's terms are added in a fixed order, so
+ * equal inputs give equal bits.  Errors: as rra_embedding (dweight
+ * overlapping dout or tokens), RRA_ERR_NOMEM.
+ */
+rra_status rra_embedding_grad(const void *dout, const void *tokens, size_t ntokens, size_t vocab,
+                              size_t dim, rra_dtype dout_t, rra_index index, float scale,
+                              int64_t padding, void *dweight, rra_dtype dweight_t, int accumulate,
+                              void *stream);
+
+/*
+ * Layer norm over rows of dim elements: mean = sum x / dim,
+ * var = sum (x - mean)^2 / dim, rstd = 1 / sqrt(var + eps),
+ * y = (x - mean) * rstd * gamma + beta.
+ *  x, y         rows * dim elements of dtype; y may be x.
+ *  gamma, beta  dim elements of weight_t (dtype or RRA_F32, else
+ *               RRA_ERR_UNSUPPORTED); NULL: 1 and 0.
+ *  mean, rstd   device fp32[rows], for rra_layer_norm_grad; NULL: not stored.
+ * Errors: RRA_ERR_INVALID (NULL, bad enums, dim 0 or above 2^31, rows above
+ * 2^40, a negative or NaN eps, outputs that overlap an input or each other
+ * otherwise), RRA_ERR_CUDA.
+ */
+rra_status rra_layer_norm(const void *x, const void *gamma, const void *beta, size_t rows,
+                          size_t dim, rra_dtype dtype, rra_dtype weight_t, float eps, void *y,
+                          float *mean, float *rstd, void *stream);
+
+/*
+ * Gradients of layer norm: with xh = (x - mean) * rstd and w = dy * gamma,
+ *   dx = rstd * (w - mean(w) - xh * mean(w * xh))   (means over the row)
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ *  dy, x        rows * dim elements of dtype; mean, rstd: fp32[rows] as
+ *               rra_layer_norm stored them; gamma NULL: 1.
+ *  dx           rows * dim elements of dtype; may be dy or x.
+ *  dgamma, dbeta  dim elements of weight_t; accumulate nonzero: added to
+ *               what they hold, in fp32.  dx, dgamma and dbeta may be NULL
+ *               (not computed), not all three.
+ * Errors: as rra_layer_norm, RRA_ERR_NOMEM.
+ */
+rra_status rra_layer_norm_grad(const void *dy, const void *x, const void *gamma,
+                               const float *mean, const float *rstd, size_t rows, size_t dim,
+                               rra_dtype dtype, rra_dtype weight_t, void *dx, void *dgamma,
+                               void *dbeta, int accumulate, void *stream);
 
 /* Human-readable name of a status code (static string). */
 const char *rra_status_string(rra_status s);

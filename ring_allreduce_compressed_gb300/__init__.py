@@ -10,7 +10,8 @@ call needs the built library and a CUDA device, and raises otherwise.
 Names follow the C ABI: ``Comm.ring_allreduce``, ``Comm.reduce_scatter``,
 ``Comm.allgather``, ``Comm.broadcast``, ``Comm.tree_allreduce``,
 ``bfp_encode``/``bfp_decode``, ``sparse_encode``/``sparse_decode``,
-``diff_encode``.
+``diff_encode``; the training-step operators ``grad_norm``/``grad_clip``,
+``embedding``/``embedding_grad``, ``layer_norm``/``layer_norm_grad``.
 """
 from __future__ import annotations
 
@@ -39,6 +40,8 @@ MAX_RANKS = 64
 BFP_BLOCK = 128
 RING_SLICE = 256
 SPARSE_PER_CHUNK, SPARSE_PER_SLICE = 0, 1
+RRA_NORM_L2, RRA_NORM_L1, RRA_NORM_INF = 0, 1, 2
+RRA_I32, RRA_I64 = 0, 1
 
 _lib = None
 
@@ -107,6 +110,15 @@ def lib():
                                           C.POINTER(_Codec), C.POINTER(_Stats), vp]
         L.rra_codec_advise.argtypes = [vp, vp, sz, i32, C.c_float, C.c_float,
                                        C.POINTER(_Codec), C.POINTER(_Stats), vp]
+        f32 = C.c_float
+        L.rra_grad_norm.argtypes = [vp, vp, vp, i32, i32, vp, vp]
+        L.rra_grad_clip.argtypes = [vp, vp, vp, vp, i32, i32, f32, f32, vp, vp]
+        L.rra_embedding.argtypes = [vp, vp, sz, sz, sz, i32, i32, f32, vp, vp]
+        L.rra_embedding_grad.argtypes = [vp, vp, sz, sz, sz, i32, i32, f32, C.c_int64, vp, i32,
+                                         i32, vp]
+        L.rra_layer_norm.argtypes = [vp, vp, vp, sz, sz, i32, i32, f32, vp, vp, vp, vp]
+        L.rra_layer_norm_grad.argtypes = [vp, vp, vp, vp, vp, sz, sz, i32, i32, vp, vp, vp, i32,
+                                          vp]
         L.rra_status_string.argtypes = [i32]
         L.rra_status_string.restype = C.c_char_p
         for name in ("rra_comm_create", "rra_comm_destroy", "rra_ring_allreduce",
@@ -119,7 +131,9 @@ def lib():
                      "rra_debug_withhold", "rra_comm_set_tuning", "rra_comm_last_shape",
                      "rra_autotune", "rra_allreduce_auto", "rra_set_crossover",
                      "rra_get_crossover", "rra_autotune_crossover", "rra_codec_measure",
-                     "rra_codec_advise", "rra_codec_measure_op", "rra_codec_advise_op"):
+                     "rra_codec_advise", "rra_codec_measure_op", "rra_codec_advise_op",
+                     "rra_grad_norm", "rra_grad_clip", "rra_embedding", "rra_embedding_grad",
+                     "rra_layer_norm", "rra_layer_norm_grad"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -416,3 +430,147 @@ def sparse_decode(hdr, vals, idx, n: int, acc, accumulate: bool = False, stream=
 def diff_encode(cur, prev, diff, stream=None):
     _check(lib().rra_diff_encode(_dev(cur, "cur"), _dev(prev, "prev"), _dev(diff, "diff"),
                                  cur.numel(), _stream(stream)), "rra_diff_encode")
+
+
+# ---------------------------------------------------------------- training-step operators
+#
+# Outputs are the caller's tensors, as everywhere in this module.  A call runs
+# on `stream` (default: the current one); nothing is allocated for it, so
+# tensors used on another stream than their own are the caller's to keep alive.
+
+def _op(t, name, dtype=None, shape=None):
+    """Address of a contiguous tensor on the current device, or None for None."""
+    import torch
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current device")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _grad_list(grads, name):
+    n = len(grads)
+    return ((C.c_void_p * n)(*[_op(g, name) for g in grads]),
+            (C.c_size_t * n)(*[g.numel() for g in grads]),
+            (C.c_int * n)(*[_dtype_code(g.dtype) for g in grads]))
+
+
+def _norm_code(p) -> int:
+    m = {2: RRA_NORM_L2, 1: RRA_NORM_L1, float("inf"): RRA_NORM_INF}
+    if p not in m:
+        raise ValueError(f"norm_type: expected 1, 2 or inf, got {p}")
+    return m[p]
+
+
+def grad_norm(grads: Sequence, norm, norm_type=2, stream=None):
+    """rra_grad_norm: norm[0] (fp32, on the device) = the norm of all tensors of
+    ``grads`` taken as one vector; their types may differ."""
+    import torch
+    ptrs, counts, dtypes = _grad_list(grads, "grads")
+    _check(lib().rra_grad_norm(ptrs, counts, dtypes, len(grads), _norm_code(norm_type),
+                               _op(norm, "norm", torch.float32, (1,)), _stream(stream)),
+           "rra_grad_norm")
+
+
+def grad_clip(grads: Sequence, outs: Sequence, max_norm: float, norm, norm_type=2,
+              eps: float = 1e-6, stream=None):
+    """rra_grad_clip: outs[k] = grads[k] * min(1, max_norm / (n + eps)), n the
+    norm of all of them, stored in norm[0].  outs may be grads (in place)."""
+    import torch
+    ptrs, counts, dtypes = _grad_list(grads, "grads")
+    if outs is grads:
+        optrs = ptrs
+    else:
+        if len(outs) != len(grads):
+            raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
+        optrs = (C.c_void_p * len(outs))(*[_op(o, "outs", g.dtype, g.shape)
+                                           for o, g in zip(outs, grads)])
+    _check(lib().rra_grad_clip(ptrs, optrs, counts, dtypes, len(grads), _norm_code(norm_type),
+                               float(max_norm), float(eps),
+                               _op(norm, "norm", torch.float32, (1,)), _stream(stream)),
+           "rra_grad_clip")
+
+
+def _index_code(t) -> int:
+    import torch
+    if t.dtype is torch.int64:
+        return RRA_I64
+    if t.dtype is torch.int32:
+        return RRA_I32
+    raise TypeError(f"tokens: expected int32 or int64, got {t.dtype}")
+
+
+def embedding(weight, tokens, out, scale: float = 1.0, stream=None):
+    """rra_embedding: out[..., :] = scale * weight[tokens[...], :] for a
+    (vocab, dim) weight; tokens outside the table give zeros."""
+    if weight.dim() != 2:
+        raise ValueError("weight: expected (vocab, dim)")
+    vocab, dim = weight.shape
+    _check(lib().rra_embedding(_op(weight, "weight"), _op(tokens, "tokens"), tokens.numel(),
+                               vocab, dim, _dtype_code(weight.dtype), _index_code(tokens),
+                               float(scale),
+                               _op(out, "out", weight.dtype, tokens.shape + (dim,)),
+                               _stream(stream)), "rra_embedding")
+
+
+def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optional[int] = None,
+                   accumulate: bool = False, stream=None):
+    """rra_embedding_grad: dweight[v, :] = scale * the sum of dout's rows whose
+    token is v (zero where there is none), or added to dweight."""
+    if dweight.dim() != 2:
+        raise ValueError("dweight: expected (vocab, dim)")
+    vocab, dim = dweight.shape
+    _check(lib().rra_embedding_grad(_op(dout, "dout", None, tokens.shape + (dim,)),
+                                    _op(tokens, "tokens"), tokens.numel(), vocab, dim,
+                                    _dtype_code(dout.dtype), _index_code(tokens), float(scale),
+                                    -1 if padding_idx is None else int(padding_idx),
+                                    _op(dweight, "dweight"), _dtype_code(dweight.dtype),
+                                    1 if accumulate else 0, _stream(stream)),
+           "rra_embedding_grad")
+
+
+def _rows(x, name):
+    if x.dim() < 1:
+        raise ValueError(f"{name}: expected (..., dim)")
+    dim = x.shape[-1]
+    return (x.numel() // dim if dim else 0), dim
+
+
+def layer_norm(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+    """rra_layer_norm over the last dimension of x: y = (x - mean) * rstd *
+    gamma + beta; gamma and beta may be None.  mean and rstd (fp32, one value
+    a row) are stored when given: layer_norm_grad needs them."""
+    import torch
+    rows, dim = _rows(x, "x")
+    wt = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
+    _check(lib().rra_layer_norm(_op(x, "x"), _op(gamma, "gamma", wt, (dim,)),
+                                _op(beta, "beta", wt, (dim,)), rows, dim, _dtype_code(x.dtype),
+                                _dtype_code(wt), float(eps), _op(y, "y", x.dtype, x.shape),
+                                _op(mean, "mean", torch.float32, (rows,)),
+                                _op(rstd, "rstd", torch.float32, (rows,)), _stream(stream)),
+           "rra_layer_norm")
+
+
+def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: bool = False,
+                    stream=None):
+    """rra_layer_norm_grad: the gradients of x, gamma and beta from dy and the
+    forward pass's x, mean and rstd.  dx may be dy or x; outputs that are None
+    are not computed; accumulate adds to what dgamma and dbeta hold."""
+    import torch
+    rows, dim = _rows(x, "x")
+    wt = next((t.dtype for t in (gamma, dgamma, dbeta) if t is not None), x.dtype)
+    _check(lib().rra_layer_norm_grad(_op(dy, "dy", x.dtype, x.shape), _op(x, "x"),
+                                     _op(gamma, "gamma", wt, (dim,)),
+                                     _op(mean, "mean", torch.float32, (rows,)),
+                                     _op(rstd, "rstd", torch.float32, (rows,)), rows, dim,
+                                     _dtype_code(x.dtype), _dtype_code(wt),
+                                     _op(dx, "dx", x.dtype, x.shape),
+                                     _op(dgamma, "dgamma", wt, (dim,)),
+                                     _op(dbeta, "dbeta", wt, (dim,)), 1 if accumulate else 0,
+                                     _stream(stream)), "rra_layer_norm_grad")

@@ -1,0 +1,104 @@
+// op_common.cuh -- what the training-step operators (grad_norm.cu,
+// embedding.cu, layer_norm.cu) share: packs of elements read and written by
+// one instruction, block reductions, argument checks and the scratch memory
+// of a stream.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "rra.h"
+#include "rra_device.cuh"
+
+namespace rra {
+
+int num_sms();
+
+// ---------------------------------------------------------------- device
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v)
+{
+    return __float2half_rn(v);
+}
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+
+// V consecutive elements that one load or store of V * sizeof(T) <= 16 bytes
+// moves; the address is a multiple of that size.
+template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
+    T e[V];
+};
+
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T *p)
+{
+    return *reinterpret_cast<const Pack<T, V> *>(p);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
+{
+    *reinterpret_cast<Pack<T, V> *>(p) = v;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- host
+
+inline bool valid_dt(rra_dtype t) { return t == RRA_F32 || t == RRA_F16 || t == RRA_BF16; }
+
+// Do [a, a + na) and [b, b + nb) share a byte?
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+inline bool aligned_to(const void *p, size_t n)
+{
+    return reinterpret_cast<uintptr_t>(p) % n == 0;
+}
+
+// Elements per pack: the widest of 16 bytes or less at which every address
+// (a multiple of `bytes` from the base) is aligned.
+inline bool pack_fits(const void *base, size_t row_bytes, size_t bytes)
+{
+    return aligned_to(base, bytes) && row_bytes % bytes == 0;
+}
+
+// Scratch memory of the operators, one buffer per (device, stream): calls on
+// one stream run in order and share it, calls on different streams never do.
+// Its first kScratchHead bytes are zero between calls (tickets that their
+// last user clears).  The lock in `lk` is held until the launches of the
+// call are queued.  A buffer that has become too small is kept, not freed: a
+// captured graph may still hold its address; sizes at least double, so what
+// is kept never exceeds what is in use.
+// RRA_ERR_INVALID: the buffer would have to grow while the stream is being
+// captured; RRA_ERR_NOMEM, RRA_ERR_CUDA.
+constexpr size_t kScratchHead = 256;
+rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex> &lk,
+                      unsigned char **out);
+
+inline rra_status launched(cudaError_t e) { return e == cudaSuccess ? RRA_OK : RRA_ERR_CUDA; }
+
+} // namespace rra
