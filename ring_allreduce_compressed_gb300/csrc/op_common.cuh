@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "rra.h"
 #include "rra_device.cuh"
@@ -47,6 +48,62 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
     *reinterpret_cast<Pack<T, V> *>(p) = v;
 }
 
+// A pack as the words that it was loaded in; elements are taken out where they
+// are used, so that a pack in flight costs its own size in registers.
+template <typename T, int V> struct Raw {
+    static constexpr int kWords = V * sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T *p)
+    {
+        const Pack<uint32_t, kWords> q =
+            load_pack<uint32_t, kWords>(reinterpret_cast<const uint32_t *>(p));
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[i] = q.e[i];
+    }
+    __device__ __forceinline__ float get(int j) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[j]);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+        else
+            return __half2float(__ushort_as_half((unsigned short)(w[j / 2] >> (16 * (j % 2)))));
+    }
+};
+template <typename T> struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ float get(int) const { return to_f32(v); }
+};
+
+// V elements at p in stores (loads) of at most 16 bytes; p is a multiple of
+// the lesser of V * sizeof(T) and 16 bytes.
+template <typename T, int V> __device__ __forceinline__ void store_values(T *p, const T (&v)[V])
+{
+    constexpr int W = V * sizeof(T) > 16 ? 16 / sizeof(T) : V;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        Pack<T, W> q;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            q.e[j] = v[i + j];
+        store_pack<T, W>(p + i, q);
+    }
+}
+
+template <typename T, int V> __device__ __forceinline__ void load_values(const T *p, T (&v)[V])
+{
+    constexpr int W = V * sizeof(T) > 16 ? 16 / sizeof(T) : V;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        const Pack<T, W> q = load_pack<T, W>(p + i);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            v[i + j] = q.e[j];
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -74,14 +131,14 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
-inline bool aligned_to(const void *p, size_t n)
+__host__ __device__ inline bool aligned_to(const void *p, size_t n)
 {
     return reinterpret_cast<uintptr_t>(p) % n == 0;
 }
 
 // Elements per pack: the widest of 16 bytes or less at which every address
 // (a multiple of `bytes` from the base) is aligned.
-inline bool pack_fits(const void *base, size_t row_bytes, size_t bytes)
+__host__ __device__ inline bool pack_fits(const void *base, size_t row_bytes, size_t bytes)
 {
     return aligned_to(base, bytes) && row_bytes % bytes == 0;
 }

@@ -322,6 +322,13 @@ def test_embedding_grad_lengths(n, accumulate):
                          accumulate=accumulate)
 
 
+@pytest.mark.parametrize("n", [1, 33, 70, 200, 1000])
+@pytest.mark.parametrize("dim", [1, 3, 6, 513, 1030])
+def test_embedding_grad_odd_widths(n, dim):
+    check_embedding_grad(randn((n, dim), 5), tokens(n, 50, 3), 50, "f32", 1.0)
+    check_embedding_grad(randn((n, dim), 5, dtype="bf16"), tokens(n, 50, 3), 50, "bf16", 1.0)
+
+
 @pytest.mark.parametrize("vocab", [1, 2, 255, 256, 257, 65_535, 65_536, 70_000, 1 << 18,
                                    (1 << 24) + 5])
 def test_embedding_grad_vocabularies(vocab):
