@@ -120,7 +120,36 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
+// The next kernel of the stream may start its blocks now, if it was launched
+// by launch_chained; what it reads of this one it waits for.
+__device__ __forceinline__ void dependents_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Until the kernel before this one has ended and its writes are visible.
+__device__ __forceinline__ void dependents_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- host
+
+// Launch after which the next kernel of the stream may start early.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
 
 inline bool valid_dt(rra_dtype t) { return t == RRA_F32 || t == RRA_F16 || t == RRA_BF16; }
 
