@@ -74,14 +74,16 @@ __global__ void __launch_bounds__(kThreads)
 // in the order of the tiles.  So a frequent token's terms are spread over as
 // many groups as there are tiles of it.
 //
-// Rows of no token are cleared: the last `cleared` rows of the table, where
-// tokens are fewest, while the sort runs on 16 of the SMs, the others by the
-// sums' kernel.
+// Rows of no token are cleared: the table's last rows, where tokens are
+// fewest, while the sort runs on 16 of the SMs (and written over by the sums
+// where a token has them), the others beside the joins, whose waits they hide.
 
 constexpr int kMostPlaces = 32;
+constexpr int kSumThreads = 128; // small blocks: a short last wave
 constexpr uint32_t kFew = 16; // partial sums that one warp joins
-// Rows in flight: 32 registers a lane.
-template <typename T, int V> constexpr int kBatchOf = sizeof(T) * V >= 4 ? 16 / sizeof(T) : 4;
+// Rows in flight: 16 registers a lane.  Twice as many left room for 5 blocks of
+// an SM instead of 7: 56 against 53 us at 16384 x 2048 bf16.
+template <typename T, int V> constexpr int kBatchOf = sizeof(T) * V >= 4 ? 8 / sizeof(T) : 4;
 
 struct SumArgs {
     const void *dout;
@@ -92,16 +94,17 @@ struct SumArgs {
     void *dw;
     int accumulate;
     float *part;     // [tile][2][dim]
+    uint32_t *present; // a bit for every row that a token has
     uint32_t *joins; // lengths of the two lists
     uint4 *list;     // [2][tiles]: {tile, row, partial sums} of the rows that cross
                      // edges, those of up to kFew partial sums and the others
     uint32_t places; // of a tile
     uint32_t tiles, slabs;
     int lg;
-    int zero_rows; // table rows of one group that clears what no token has
     long long cleared; // rows before which clear_kernel has left the table alone
+    int clear_lg;      // 2^clear_lg rows at a time are cleared by a warp
     long long sums;
-    unsigned sum_blocks; // blocks that add; the others clear
+    unsigned join_blocks; // blocks of the last kernel that join; the others clear
 };
 
 // V columns of a finished row of the table.
@@ -153,12 +156,22 @@ __device__ __forceinline__ void sum_tile(const SumArgs &a, uint32_t tile, uint32
         }
     };
 
+    // pairs are read one batch ahead of the rows
+    uint4 ahead[kBatch / 2];
+    const auto read_pairs = [&](uint32_t i) {
+#pragma unroll
+        for (int q = 0; q < kBatch / 2; ++q)
+            ahead[q] = reinterpret_cast<const uint4 *>(a.pair + i)[q];
+    };
+    read_pairs(lo);
     for (uint32_t i = lo; i < hi; i += kBatch) {
         uint32_t key[kBatch], pos[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch / 2; ++q) {
-            const uint4 p = reinterpret_cast<const uint4 *>(a.pair + i)[q];
-            key[2 * q] = p.x; pos[2 * q] = p.y; key[2 * q + 1] = p.z; pos[2 * q + 1] = p.w;
+            key[2 * q] = ahead[q].x;
+            pos[2 * q] = ahead[q].y;
+            key[2 * q + 1] = ahead[q].z;
+            pos[2 * q + 1] = ahead[q].w;
         }
         Raw<T, V> x[kBatch][K];
 #pragma unroll
@@ -170,6 +183,8 @@ __device__ __forceinline__ void sum_tile(const SumArgs &a, uint32_t tile, uint32
                 if (key[b] < vocab && c0 + k * stride < a.dim)
                     x[b][k].load(dout + (long long)pos[b] * a.dim + c0 + k * stride);
         }
+        if (i + kBatch < hi)
+            read_pairs(i + kBatch);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (key[b] >= vocab)
@@ -212,64 +227,71 @@ __device__ __forceinline__ void sum_tile(const SumArgs &a, uint32_t tile, uint32
     }
 }
 
-// First place whose token is not below v.
-__device__ __forceinline__ uint32_t lower_bound(const uint2 *pair, uint32_t n, uint32_t v)
-{
-    uint32_t lo = 0, len = n;
-    while (len > 0) {
-        const uint32_t h = len / 2;
-        if (pair[lo + h].x < v) {
-            lo += h + 1;
-            len -= h + 1;
-        } else {
-            len = h;
-        }
-    }
-    return lo;
-}
+// Clears the rows that no token has.  A warp takes a few rows of about 4 KB,
+// then the next ones a grid further, so that the grid goes through the table
+// in order.  Its lanes read the marks of its next 32 turns at once: a read that
+// waits behind the writes of a whole GPU at every turn cost a third of the
+// rate.
+constexpr int kClearBytes = 4096;
+constexpr int kClearPerSm = 8; // blocks
 
-// A warp clears those of its stretch of table rows that no token has.
 template <typename O>
-__device__ __forceinline__ void clear_rows(const SumArgs &a, long long v0, int lane)
+__device__ __forceinline__ void clear_rows(const SumArgs &a, unsigned block, unsigned blocks)
 {
-    const long long v = v0 + lane;
-    bool absent = false;
-    if (lane < a.zero_rows && v < a.cleared) {
-        const uint32_t at = lower_bound(a.pair, a.n, (uint32_t)v);
-        absent = at >= a.n || a.pair[at].x != (uint32_t)v;
-    }
-    unsigned left = __ballot_sync(kFull, absent);
-    const bool vec = pack_fits(a.dw, a.dim * sizeof(O), 16);
     constexpr int V = 16 / sizeof(O);
-    while (left) {
-        const int r = __ffs(left) - 1;
-        left &= left - 1;
-        O *const q = static_cast<O *>(a.dw) + (v0 + r) * a.dim;
-        if (vec) {
-            for (long long c = lane * V; c < a.dim; c += 32 * V)
-                *reinterpret_cast<uint4 *>(q + c) = make_uint4(0, 0, 0, 0);
+    const int lane = threadIdx.x % 32;
+    const bool vec = pack_fits(a.dw, a.dim * sizeof(O), 16);
+    const unsigned long long width = a.dim / (vec ? V : 1); // stores of a row
+    const int rows = 1 << a.clear_lg;
+    const long long step = (long long)blocks * kWarps << a.clear_lg;
+    long long v = (long long)(block * kWarps + threadIdx.x / 32) << a.clear_lg;
+    // (past L1, which may hold an earlier call's)
+    const auto marks = [&](long long at) {
+        return a.n && at < a.cleared ? __ldcg(a.present + at / 32) >> at % 32 : 0u;
+    };
+    uint32_t ahead = 0;
+    for (int turn = 0; v < a.cleared; v += step, ++turn) {
+        if (turn % 32 == 0)
+            ahead = marks(v + lane * step);
+        const uint32_t there = __shfl_sync(kFull, ahead, turn % 32);
+        O *const q = static_cast<O *>(a.dw) + v * a.dim;
+        if (rows == 1) {
+            if (there & 1)
+                continue;
+            if (vec) {
+#pragma unroll 4
+                for (unsigned long long u = lane; u < width; u += 32)
+                    reinterpret_cast<uint4 *>(q)[u] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (unsigned long long u = lane; u < width; u += 32)
+                    q[u] = from_f32<O>(0.0f);
+            }
         } else {
-            for (long long c = lane; c < a.dim; c += 32)
-                q[c] = from_f32<O>(0.0f);
+            const unsigned w = (unsigned)width, units = (unsigned)min(a.cleared - v, (long long)rows) * w;
+#pragma unroll 4
+            for (unsigned u = lane; u < units; u += 32) {
+                if (there >> u / w & 1)
+                    continue;
+                if (vec)
+                    reinterpret_cast<uint4 *>(q)[u] = make_uint4(0, 0, 0, 0);
+                else
+                    q[u] = from_f32<O>(0.0f);
+            }
         }
     }
 }
 
 template <typename T, typename O, int V>
-__global__ void __launch_bounds__(kThreads, 3) sum_kernel(const SumArgs a)
+__global__ void __launch_bounds__(kSumThreads, 7) sum_kernel(const SumArgs a)
 {
-    dependents_launch();
+    // in this order: when finish_kernel starts, the sort has ended
     dependents_wait();
-    if (blockIdx.x < a.sum_blocks) {
-        const long long g = ((long long)blockIdx.x * kThreads + threadIdx.x) >> a.lg;
-        if (g < a.sums) {
-            const uint32_t tile = (uint32_t)(g / a.slabs);
-            sum_tile<T, O, V>(a, tile, (uint32_t)(g - (long long)tile * a.slabs),
-                              threadIdx.x & ((1 << a.lg) - 1));
-        }
-    } else {
-        const long long w = (long long)(blockIdx.x - a.sum_blocks) * kWarps + threadIdx.x / 32;
-        clear_rows<O>(a, w * a.zero_rows, threadIdx.x % 32);
+    dependents_launch();
+    const long long g = ((long long)blockIdx.x * kSumThreads + threadIdx.x) >> a.lg;
+    if (g < a.sums) {
+        const uint32_t tile = (uint32_t)(g / a.slabs);
+        sum_tile<T, O, V>(a, tile, (uint32_t)(g - (long long)tile * a.slabs),
+                          threadIdx.x & ((1 << a.lg) - 1));
     }
 }
 
@@ -282,7 +304,10 @@ __global__ void __launch_bounds__(kThreads) clear_kernel(unsigned char *p, long 
         reinterpret_cast<uint4 *>(p)[i] = make_uint4(0, 0, 0, 0);
     if (blockIdx.x == 0 && threadIdx.x < bytes % 16)
         p[packs * 16 + threadIdx.x] = 0;
-    dependents_wait(); // when this kernel has ended, so has the sort
+    // When this kernel has ended, so has the sort.  One block waits for it: the
+    // others make room for those that found none beside the sort's.
+    if (blockIdx.x == 0)
+        dependents_wait();
 }
 
 // V * K columns of a lane, `stride` apart, of partial sums p0 .. p1 - 1 of the
@@ -311,19 +336,17 @@ __device__ __forceinline__ void add_parts(const SumArgs &a, uint32_t t, uint32_t
 // stretches of the sums at once and then their results.
 constexpr int kStretches = kThreads / 8;
 
-template <typename O, int V>
-__global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a)
+template <typename O, int V> __device__ __forceinline__ void join_rows(const SumArgs &a)
 {
     constexpr int K = 4 / V;
     __shared__ float sm[kStretches][33];
-    dependents_wait();
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     const uint32_t few_slabs = (uint32_t)((a.dim + 127) / 128),
                    many_slabs = (uint32_t)((a.dim + 31) / 32);
     const unsigned long long few = (unsigned long long)a.joins[0] * few_slabs,
                              many = (unsigned long long)a.joins[1] * many_slabs;
 
-    for (unsigned long long i = blockIdx.x; i < many; i += gridDim.x) {
+    for (unsigned long long i = blockIdx.x; i < many; i += a.join_blocks) {
         const uint4 e = a.list[a.tiles + i / many_slabs];
         const long long c0 = (long long)(i % many_slabs) * 32;
         const int s = threadIdx.x / 8, at = threadIdx.x % 8 * V;
@@ -347,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a)
         }
     }
     // from the last block down: the first ones may be at the long rows
-    for (unsigned long long i = (unsigned long long)(gridDim.x - 1 - blockIdx.x) * kWarps + w;
-         i < few; i += (unsigned long long)gridDim.x * kWarps) {
+    for (unsigned long long i = (unsigned long long)(a.join_blocks - 1 - blockIdx.x) * kWarps + w;
+         i < few; i += (unsigned long long)a.join_blocks * kWarps) {
         const uint4 e = a.list[i / few_slabs];
         const long long c = (long long)(i % few_slabs) * 128 + lane * V;
         float acc[K][V] = {};
@@ -358,6 +381,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a)
         for (int k = 0; k < K; ++k)
             if (c + k * 32 * V < a.dim)
                 put_final<O, V>(q + c + k * 32 * V, acc[k], a);
+    }
+}
+
+// The joins, for which the sums must have ended, and the clears, which need the
+// sort alone: they run beside the sums' last blocks, too.
+template <typename O, int V>
+__global__ void __launch_bounds__(kThreads) finish_kernel(const SumArgs a)
+{
+    if (blockIdx.x < a.join_blocks) {
+        dependents_wait();
+        join_rows<O, V>(a);
+    } else {
+        clear_rows<O>(a, blockIdx.x - a.join_blocks, gridDim.x - a.join_blocks);
     }
 }
 
@@ -403,13 +439,14 @@ void lookup_any(const void *w, const void *tok, long long n, long long vocab, lo
         lookup<T, 1>(w, tok, n, vocab, dim, wide, scale, out, st);
 }
 
-// Table rows that are cleared during the sort: what the other SMs write in the
-// time that it takes.
+// Table rows that are cleared during the sort: about what the other SMs write
+// in the time that it takes (none, 48 MB + 1 KB a token: 63, 56 us at 16384
+// tokens, 169, 152 us at 131072).
 long long cleared_early(const SumArgs &a, size_t row)
 {
     if (a.accumulate || a.n == 0 || a.n > kCsMost)
         return 0;
-    const unsigned long long bytes = (32ull << 20) + 1024ull * a.n;
+    const unsigned long long bytes = (48ull << 20) + 1024ull * a.n;
     return std::min((long long)(bytes / row), a.vocab);
 }
 
@@ -431,20 +468,37 @@ template <typename T, typename O, int V> cudaError_t sum_rows(SumArgs a, cudaStr
         if (e != cudaSuccess)
             return e;
     }
-    a.zero_rows = a.cleared >= 1 << 17 ? 32 : 8;
+    if (a.tiles > 0) {
+        const cudaError_t e = launch_chained(
+            sum_kernel<T, O, V>,
+            dim3((unsigned)(((a.sums << a.lg) + kSumThreads - 1) / kSumThreads)), kSumThreads, st,
+            a);
+        if (e != cudaSuccess)
+            return e;
+    }
+    a.clear_lg = 0;
+    while (a.clear_lg < 5 && (row << (a.clear_lg + 1)) <= kClearBytes)
+        ++a.clear_lg;
+    const long long at_once = (long long)kWarps << a.clear_lg;
     const long long clears =
-        a.accumulate ? 0 : (a.cleared + a.zero_rows * kWarps - 1) / (a.zero_rows * kWarps);
-    a.sum_blocks = (unsigned)(((a.sums << a.lg) + kThreads - 1) / kThreads);
-    cudaError_t e = cudaSuccess;
-    if (a.sum_blocks + clears > 0)
-        e = launch_chained(sum_kernel<T, O, V>, dim3((unsigned)(a.sum_blocks + clears)), kThreads,
-                           st, a);
-    if (e != cudaSuccess || a.tiles < 2)
-        return e;
-    const dim3 grid(grid_of((long long)a.tiles * ((a.dim + 127) / 128) / 4, 8));
-    if (a.dim % 4 == 0 && aligned_to(a.dw, 4 * sizeof(O)))
-        return launch_chained(join_kernel<O, 4>, grid, kThreads, st, a);
-    return launch_chained(join_kernel<O, 1>, grid, kThreads, st, a);
+        a.accumulate || a.cleared == 0
+            ? 0
+            : grid_of((a.cleared + at_once - 1) / at_once, kClearPerSm);
+    // joins wait more than they read: a block per SM lasts as long as the
+    // clears beside it, many are better where there are none
+    a.join_blocks = a.tiles < 2 ? 0
+                                : grid_of((long long)a.tiles * ((a.dim + 127) / 128) / 4,
+                                          clears > num_sms() ? 2 : 8);
+    const dim3 grid((unsigned)(a.join_blocks + clears));
+    if (grid.x == 0)
+        return cudaSuccess;
+    const bool wide = a.dim % 4 == 0 && aligned_to(a.dw, 4 * sizeof(O));
+    const auto fn = wide ? finish_kernel<O, 4> : finish_kernel<O, 1>;
+    if (a.tiles == 0) { // nothing of this call to be chained to
+        fn<<<grid, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    return launch_chained(fn, grid, kThreads, st, a);
 }
 
 template <typename T, typename O> cudaError_t sum_any(const SumArgs &a, cudaStream_t st)
@@ -537,11 +591,12 @@ extern "C" rra_status rra_embedding_grad(const void *dout, const void *tokens, s
     // every part is a multiple of 128 bytes, so that packs of all are aligned
     const size_t pairs = sizeof(uint2) * places * (large ? 2 : 1),
                  counts = large ? sizeof(uint32_t) * kDigits * (sort_tiles(n) + 1) : 0,
+                 marks = accumulate ? 0 : ((size_t)present_words(vocab) * 4 + 127) / 128 * 128,
                  lists = (sizeof(uint4) * (2 * (size_t)sum.tiles + 1) + 127) / 128 * 128,
                  parts = sizeof(float) * 2 * sum.tiles * dim;
     std::unique_lock<std::mutex> lk;
     unsigned char *ws = nullptr;
-    const rra_status s = op_scratch(st, kScratchHead + pairs + counts + lists + parts, lk, &ws);
+    const rra_status s = op_scratch(st, kScratchHead + pairs + counts + marks + lists + parts, lk, &ws);
     if (s != RRA_OK)
         return s;
     ws += kScratchHead;
@@ -550,20 +605,20 @@ extern "C" rra_status rra_embedding_grad(const void *dout, const void *tokens, s
     sum.scale = scale;
     sum.dw = dweight;
     sum.accumulate = accumulate;
-    sum.joins = reinterpret_cast<uint32_t *>(ws + pairs + counts);
-    sum.list = reinterpret_cast<uint4 *>(ws + pairs + counts) + 1;
-    sum.part = reinterpret_cast<float *>(ws + pairs + counts + lists);
+    unsigned char *const after = ws + pairs + counts;
+    sum.present = accumulate ? nullptr : reinterpret_cast<uint32_t *>(after);
+    sum.joins = reinterpret_cast<uint32_t *>(after + marks);
+    sum.list = reinterpret_cast<uint4 *>(after + marks) + 1;
+    sum.part = reinterpret_cast<float *>(after + marks + lists);
     const Tokens t{tokens, index == RRA_I64, (uint32_t)n, (long long)vocab, padding};
     cudaError_t e = cudaSuccess;
     if (large) {
-        sum.pair = many_sort(t, pair, reinterpret_cast<uint32_t *>(ws + pairs), st);
-        e = cudaMemsetAsync(sum.joins, 0, 2 * sizeof(uint32_t), st);
-        if (e == cudaSuccess)
-            e = cudaGetLastError();
+        e = many_sort(t, pair, reinterpret_cast<uint32_t *>(ws + pairs), sum.joins, sum.present,
+                      &sum.pair, st);
     } else {
         sum.pair = pair[0];
         if (n > 0)
-            e = cluster_sort(t, pair[0], sum.joins, st);
+            e = cluster_sort(t, pair[0], sum.joins, sum.present, st);
     }
     if (e != cudaSuccess)
         return RRA_ERR_CUDA;

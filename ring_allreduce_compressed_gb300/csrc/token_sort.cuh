@@ -26,6 +26,12 @@ __device__ __forceinline__ uint32_t token_key(const Tokens &a, uint32_t i)
     return (uint32_t)(v >= 0 && v < a.vocab && v != a.padding ? v : a.vocab);
 }
 
+// Words of a bit for every token.
+__host__ __device__ inline uint32_t present_words(long long vocab)
+{
+    return (uint32_t)((vocab + 31) / 32);
+}
+
 // Lanes of the warp with the same digit of `bits` bits; lanes that are not
 // `on` stand apart.  One vote a bit.
 __device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, bool on)
@@ -89,6 +95,7 @@ struct ClusterSortArgs {
     Tokens t;
     uint2 *pair;         // sorted
     uint32_t *joins;     // two counts that later kernels use, cleared here
+    uint32_t *present;   // a bit for every token < vocab: is it there? May be nullptr
     int bits, passes;    // of a digit; digits
 };
 
@@ -140,6 +147,11 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
     dependents_launch();
     if (me == 0 && threadIdx.x < 2)
         a.joins[threadIdx.x] = 0;
+    if (a.present) {
+        const uint32_t words = present_words(a.t.vocab);
+        for (uint32_t i = me * kCsThreads + threadIdx.x; i < words; i += blocks * kCsThreads)
+            a.present[i] = 0;
+    }
 
     // a warp holds a stretch of the block's pairs, 32 a round
     uint32_t key[R], pos[R], rank[R];
@@ -219,6 +231,9 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
             const uint32_t g = first_all[(p.x >> shift) & (digits - 1)] + j;
             if (end) {
                 a.pair[g] = p;
+                // the block's pairs are sorted here, too: one of a token's marks it
+                if (a.present && p.x < a.t.vocab && (j == 0 || stage[j - 1].x != p.x))
+                    atomicOr(a.present + p.x / 32, 1u << p.x % 32);
             } else {
                 const uint32_t to = remote(smem_u32(buf + g % kLocal), g / kLocal);
                 asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(p.x),
@@ -268,7 +283,8 @@ template <int R> cudaError_t cluster_sort(ClusterSortArgs a, int key_bits, int b
 }
 
 // Up to kCsMost tokens, at least one.
-inline cudaError_t cluster_sort(const Tokens &t, uint2 *pair, uint32_t *joins, cudaStream_t st)
+inline cudaError_t cluster_sort(const Tokens &t, uint2 *pair, uint32_t *joins, uint32_t *present,
+                                cudaStream_t st)
 {
     int key_bits = 1;
     while (((unsigned long long)t.vocab >> key_bits) != 0)
@@ -278,7 +294,7 @@ inline cudaError_t cluster_sort(const Tokens &t, uint2 *pair, uint32_t *joins, c
         blocks *= 2;
     while ((long long)blocks * kCsThreads * rounds < t.n)
         rounds *= 2;
-    const ClusterSortArgs a{t, pair, joins, 0, 0};
+    const ClusterSortArgs a{t, pair, joins, present, 0, 0};
     switch (rounds) {
     case 1: return cluster_sort<1>(a, key_bits, blocks, st);
     case 2: return cluster_sort<2>(a, key_bits, blocks, st);
@@ -392,13 +408,32 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortArgs 
             a.out[cnt[w][(pair[r].x >> a.shift) & (kDigits - 1)] + rank[r]] = pair[r];
 }
 
+// Marks the tokens of the sorted pairs.
+__global__ void __launch_bounds__(kSortThreads)
+    mark_kernel(const uint2 *__restrict__ pair, uint32_t n, long long vocab, uint32_t *present)
+{
+    const uint32_t i = blockIdx.x * kSortThreads + threadIdx.x;
+    if (i < n) {
+        const uint32_t v = pair[i].x;
+        if (v < vocab && (i == 0 || pair[i - 1].x != v))
+            atomicOr(present + v / 32, 1u << v % 32);
+    }
+}
+
 inline long long sort_tiles(long long n) { return (n + kSortTile - 1) / kSortTile; }
 
 // Any number of tokens up to 2^31 - 1; pair[0] and pair[1] hold n pairs each,
-// counts kDigits * (sort_tiles + 1) words.  Returns the sorted pairs.
-inline const uint2 *many_sort(const Tokens &t, uint2 *const pair[2], uint32_t *counts,
-                              cudaStream_t st)
+// counts kDigits * (sort_tiles + 1) words; joins and present as above.  *out
+// receives the sorted pairs.
+inline cudaError_t many_sort(const Tokens &t, uint2 *const pair[2], uint32_t *counts,
+                             uint32_t *joins, uint32_t *present, const uint2 **out,
+                             cudaStream_t st)
 {
+    cudaError_t e = cudaMemsetAsync(joins, 0, 2 * sizeof(uint32_t), st);
+    if (e == cudaSuccess && present)
+        e = cudaMemsetAsync(present, 0, sizeof(uint32_t) * present_words(t.vocab), st);
+    if (e != cudaSuccess)
+        return e;
     SortArgs a{};
     a.t = t;
     a.tiles = sort_tiles(t.n);
@@ -414,7 +449,11 @@ inline const uint2 *many_sort(const Tokens &t, uint2 *const pair[2], uint32_t *c
         sort_move_kernel<<<(unsigned)a.tiles, kSortThreads, 0, st>>>(a);
         at ^= 1;
     }
-    return pair[at];
+    if (present)
+        mark_kernel<<<(t.n + kSortThreads - 1) / kSortThreads, kSortThreads, 0, st>>>(
+            pair[at], t.n, t.vocab, present);
+    *out = pair[at];
+    return cudaGetLastError();
 }
 
 } // namespace
