@@ -25,57 +25,115 @@ struct Group {
     __host__ __device__ int lanes() const { return warps > 1 ? 32 * warps : 1 << lg; }
 };
 
-// Sums v over the group; every lane gets it.  More than a warp: `sm` holds
-// 2 * 32 * N floats of the group's own, and `turn` alternates, so that one
-// barrier a sum is enough: a warp that is a sum ahead writes elsewhere.
+// s / n for whole n, correctly rounded, where `inverse` is 1 / n correctly
+// rounded (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990).  Three instructions
+// where a division takes some twenty of every warp of a row.
+__device__ __forceinline__ float quotient(float s, float n, float inverse)
+{
+    const float q = s * inverse;
+    const float r = fmaf(fmaf(-q, n, s), inverse, q);
+    return r == r ? r : q; // (an infinite q)
+}
+
+// Sums over the lanes of a group; every lane gets them.  More than a warp:
+// `at` holds 2 * 32 * N floats of the group's own, zero behind the warps'
+// places, and `turn` alternates, so that one barrier a sum is enough: a warp
+// that is a sum ahead writes elsewhere.
 template <int N> struct Sums {
     float v[N];
 };
 
-template <bool MULTI, int N>
-__device__ __forceinline__ Sums<N> group_sum(Sums<N> s, const Group &g, float *sm, int &turn,
-                                             int barrier)
+struct GroupOf {
+    int half;    // of the lanes that a row has in a warp
+    int warps;   // of the group
+    int warp;    // this one's number
+    int barrier; // the group's
+    float *at;
+    int turn;
+};
+
+__device__ __forceinline__ GroupOf group_of(const Group &g, float *at, int barrier)
 {
-    const int lane = threadIdx.x % 32;
+    return {1 << g.lg >> 1, g.warps, (int)(threadIdx.x / 32) % g.warps, barrier, at, 0};
+}
+
+template <bool MULTI, int N>
+__device__ __forceinline__ Sums<N> group_sum(Sums<N> s, GroupOf &g)
+{
     if constexpr (!MULTI) {
-        for (int o = 1 << g.lg >> 1; o > 0; o >>= 1)
+        for (int o = g.half; o > 0; o >>= 1)
 #pragma unroll
             for (int n = 0; n < N; ++n)
                 s.v[n] += __shfl_xor_sync(kFull, s.v[n], o);
+        return s;
+    }
+    const int lane = threadIdx.x % 32;
+    float *const at = g.at + g.turn * (32 * N);
+    g.turn ^= 1;
+    if constexpr (N == 2) { // each half warp takes one of the two on
+        const float mine = lane < 16 ? s.v[0] : s.v[1], other = lane < 16 ? s.v[1] : s.v[0];
+        float t = mine + __shfl_xor_sync(kFull, other, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            t += __shfl_xor_sync(kFull, t, o);
+        if (lane % 16 == 0)
+            at[lane * 2 + g.warp] = t;
     } else {
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            s.v[n] = warp_sum(s.v[n]);
-        float *const at = sm + turn * (32 * N);
-        turn ^= 1;
-        const int w = threadIdx.x / 32 % g.warps;
+        s.v[0] = warp_sum(s.v[0]);
         if (lane == 0)
+            at[g.warp] = s.v[0];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(g.barrier), "r"(32 * g.warps) : "memory");
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-                at[n * 32 + w] = s.v[n];
-        asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * g.warps) : "memory");
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            s.v[n] = warp_sum(lane < g.warps ? at[n * 32 + lane] : 0.0f);
+    for (int n = 0; n < N; ++n) {
+        if (g.warps <= 8) {
+            const float4 a = *reinterpret_cast<const float4 *>(at + n * 32);
+            s.v[n] = (a.x + a.y) + (a.z + a.w);
+            if (g.warps > 4) {
+                const float4 b = *reinterpret_cast<const float4 *>(at + n * 32 + 4);
+                s.v[n] += (b.x + b.y) + (b.z + b.w);
+            }
+        } else {
+            s.v[n] = warp_sum(at[n * 32 + lane]);
+        }
     }
     return s;
 }
 
-// V values of type W as fp32, or `none` where there is no array.
+// V weights as fp32, or `none` where there is no array.
 template <typename W, int V>
-__device__ __forceinline__ void load_weights(const W *p, long long c, float none, float (&v)[V])
+__device__ __forceinline__ void load_weights(const W *p, int c, float none,
+                                             typename Values<V>::E (&v)[Values<V>::N])
 {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            v[j] = none;
+        for (int n = 0; n < Values<V>::N; ++n)
+            v[n] = Values<V>::all(none);
         return;
     }
-    W w[V];
-    load_values<W, V>(p + c, w);
+    constexpr int U = V * sizeof(W) > 16 ? 16 / sizeof(W) : V; // of one load
+    using P = Values<U>;
+#pragma unroll
+    for (int i = 0; i < V / U; ++i) {
+        Raw<W, U> raw;
+        raw.load(p + c + i * U);
+#pragma unroll
+        for (int n = 0; n < P::N; ++n)
+            v[i * P::N + n] = P::get(raw, n);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vals(T *p, const typename Values<V>::E (&e)[Values<V>::N])
+{
+    float f[V];
+    Values<V>::to_array(e, f);
+    T o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        v[j] = to_f32(w[j]);
+        o[j] = from_f32<T>(f[j]);
+    store_values<T, V>(p, o);
 }
 
 // ---------------------------------------------------------------- forward
@@ -94,55 +152,76 @@ constexpr int kFwdThreads = 256; // of a block, where a group is no more than th
 template <typename T, typename W, int V, int K, bool MULTI>
 __global__ void __launch_bounds__(MULTI ? 1024 : kFwdThreads, MULTI ? 1 : 4) norm_kernel(const Fwd a)
 {
-    __shared__ float sm[MULTI ? 2 * 32 : 1]; // a group of several warps is a block
+    __shared__ __align__(16) float sm[MULTI ? 2 * 32 : 4]; // a group of several warps is a block
     const T *const x = static_cast<const T *>(a.x);
     T *const y = static_cast<T *>(a.y);
     const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
                                                                 static_cast<const W *>(a.beta);
     const int lanes = a.g.lanes(), li = threadIdx.x % lanes, groups = blockDim.x / lanes;
-    const long long units = a.dim / V;
-    const float n = (float)a.dim;
-    int turn = 0;
+    using P = Values<V>;
+    using E = typename P::E;
+    const int units = (int)a.dim / V, apart = lanes * V; // (a held row is short)
+    const float n = (float)a.dim, inverse = 1.0f / n;
+    bool in[K];  // does the lane hold a k-th pack?
+    int col[K]; // its first column; that of the row's last pack if not
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        in[k] = li + k * lanes < units;
+        col[k] = min(li + k * lanes, units - 1) * V;
+    }
+    GroupOf group = group_of(a.g, sm, 1);
+    if (MULTI) {
+        if (threadIdx.x < 64)
+            sm[threadIdx.x] = 0.0f;
+        __syncthreads();
+    }
+    const int first = threadIdx.x / lanes;
     for (long long base = (long long)blockIdx.x * groups; base < a.rows;
          base += (long long)gridDim.x * groups) {
-        const long long r = base + threadIdx.x / lanes;
-        const bool on = r < a.rows; // (every lane takes part in the sums)
-        Raw<T, V> v[K];
-        Sums<1> s{};
+        // every lane takes part in the sums, some in vain: they read the last row
+        const long long r = MULTI ? base : min(base + first, a.rows - 1);
+        const bool on = MULTI || base + first < a.rows;
+        const T *const p = x + r * a.dim + li * V;
+        Raw<T, V> raw[K];
+        E sum = P::all(0.0f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            raw[k].clear();
+            if (in[k])
+                raw[k].load(p + k * apart);
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units)
-                v[k].load(x + r * a.dim + (long long)(li + k * lanes) * V);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units)
+            for (int m = 0; m < P::N; ++m)
+                sum = add(sum, P::get(raw[k], m));
+        Sums<1> s{{sum_of(sum)}};
+        const float mu = quotient(group_sum<MULTI, 1>(s, group).v[0], n, inverse);
+        sum = P::all(0.0f);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    s.v[0] += v[k].get(j);
-        const float mu = group_sum<MULTI, 1>(s, a.g, sm, turn, 1).v[0] / n;
-        s.v[0] = 0.0f;
+        for (int k = 0; k < K; ++k) {
+            const E minus = P::all(in[k] ? -mu : 0.0f); // a pack that is not there stays zero
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = v[k].get(j) - mu;
-                    s.v[0] = fmaf(d, d, s.v[0]);
-                }
-        const float rs = 1.0f / sqrtf(group_sum<MULTI, 1>(s, a.g, sm, turn, 1).v[0] / n + a.eps);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units) {
-                const long long c = (long long)(li + k * lanes) * V;
-                float g[V], b[V];
-                load_weights<W, V>(gamma, c, 1.0f, g);
-                load_weights<W, V>(beta, c, 0.0f, b);
-                T o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    o[j] = from_f32<T>(fmaf((v[k].get(j) - mu) * rs, g[j], b[j]));
-                store_values<T, V>(y + r * a.dim + c, o);
+            for (int m = 0; m < P::N; ++m) {
+                const E d = add(P::get(raw[k], m), minus);
+                sum = fma(d, d, sum);
             }
+        }
+        s.v[0] = sum_of(sum);
+        const float rs = rsqrtf(quotient(group_sum<MULTI, 1>(s, group).v[0], n, inverse) + a.eps);
+        const E minus = P::all(-mu), scale = P::all(rs);
+        T *const q = y + r * a.dim + li * V;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            E g[P::N], b[P::N];
+            load_weights<W, V>(gamma, col[k], 1.0f, g);
+            load_weights<W, V>(beta, col[k], 0.0f, b);
+#pragma unroll
+            for (int m = 0; m < P::N; ++m)
+                g[m] = fma(mul(add(P::get(raw[k], m), minus), scale), g[m], b[m]);
+            if (on && in[k])
+                store_vals<T, V>(q + k * apart, g);
+        }
         if (on && li == 0) {
             if (a.mean)
                 a.mean[r] = mu;
@@ -155,16 +234,11 @@ __global__ void __launch_bounds__(MULTI ? 1024 : kFwdThreads, MULTI ? 1 : 4) nor
 // Rows that no block holds: three passes over each, the last two from L2.
 constexpr int kLongThreads = 1024;
 
-template <int N> __device__ __forceinline__ Sums<N> block_sums(Sums<N> s, float *sm, int &turn)
-{
-    return group_sum<true, N>(s, Group{5, kLongThreads / 32}, sm, turn, 1);
-}
-
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const Fwd a)
 {
-    __shared__ float sm[2 * 32];
-    int turn = 0;
+    __shared__ __align__(16) float sm[2 * 32];
+    GroupOf block = group_of(Group{5, kLongThreads / 32}, sm, 1);
     const float n = (float)a.dim;
     for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *const p = static_cast<const T *>(a.x) + r * a.dim;
@@ -173,13 +247,13 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const Fwd a)
         Sums<1> s{};
         for (long long c = threadIdx.x; c < a.dim; c += kLongThreads)
             s.v[0] += to_f32(p[c]);
-        const float mu = block_sums<1>(s, sm, turn).v[0] / n;
+        const float mu = group_sum<true, 1>(s, block).v[0] / n;
         s.v[0] = 0.0f;
         for (long long c = threadIdx.x; c < a.dim; c += kLongThreads) {
             const float d = to_f32(p[c]) - mu;
             s.v[0] = fmaf(d, d, s.v[0]);
         }
-        const float rs = 1.0f / sqrtf(block_sums<1>(s, sm, turn).v[0] / n + a.eps);
+        const float rs = rsqrtf(group_sum<true, 1>(s, block).v[0] / n + a.eps);
         for (long long c = threadIdx.x; c < a.dim; c += kLongThreads) {
             const float g = gamma ? to_f32(gamma[c]) : 1.0f, b = beta ? to_f32(beta[c]) : 0.0f;
             static_cast<T *>(a.y)[r * a.dim + c] =
@@ -209,27 +283,28 @@ inline Group group_for(long long units, int K)
     return g;
 }
 
-constexpr int kShort = 8, kHeld = 32; // elements that a lane holds
+constexpr int kShort = 8; // elements that a lane holds: of short rows
+template <int V> constexpr int kHeld = V > 1 ? 32 : 16;
 
 template <typename T, typename W, int V> void forward_packs(Fwd a, cudaStream_t st)
 {
     const long long units = a.dim / V;
-    if (a.dim > 1024LL * kHeld) {
+    if (a.dim > 1024LL * kHeld<V>) {
         norm_long_kernel<T, W><<<grid_of(a.rows, 2), kLongThreads, 0, st>>>(a);
-    } else if (a.dim <= 32 * kHeld) {
+    } else if (a.dim <= 32 * kHeld<V>) {
         // a warp or a part of one; few elements a lane for short rows
         const bool few = a.dim <= 32 * kShort;
-        a.g = group_for(units, (few ? kShort : kHeld) / V);
+        a.g = group_for(units, (few ? kShort : kHeld<V>) / V);
         const int per_block = kFwdThreads / a.g.lanes();
         const unsigned grid = grid_of((a.rows + per_block - 1) / per_block, 16);
         if (few)
             norm_kernel<T, W, V, kShort / V, false><<<grid, kFwdThreads, 0, st>>>(a);
         else
-            norm_kernel<T, W, V, kHeld / V, false><<<grid, kFwdThreads, 0, st>>>(a);
+            norm_kernel<T, W, V, kHeld<V> / V, false><<<grid, kFwdThreads, 0, st>>>(a);
     } else {
-        a.g = group_for(units, kHeld / V);
+        a.g = group_for(units, kHeld<V> / V);
         const int threads = 32 * a.g.warps;
-        norm_kernel<T, W, V, kHeld / V, true>
+        norm_kernel<T, W, V, kHeld<V> / V, true>
             <<<grid_of(a.rows, 2048 / threads), threads, 0, st>>>(a);
     }
 }
@@ -262,7 +337,9 @@ template <typename T, typename W> void forward(const Fwd &a, cudaStream_t st)
 // A lane keeps its columns' sums of dgamma and dbeta over all rows of its
 // group in registers.  At the end the groups of a block add theirs in shared
 // memory, in order, and the block leaves one partial row of each, which
-// join_kernel adds.  The next row's packs are read while a row is worked on.
+// join_kernel adds.  The packs of the next rows are on their way to shared
+// memory while a row is worked on, each lane's to slots of its own, so that
+// nothing but the row's two sums crosses lanes.
 struct Bwd {
     const void *dy, *x, *gamma;
     const float *mean, *rstd;
@@ -274,135 +351,214 @@ struct Bwd {
     Group g;
 };
 
-constexpr int kBwdThreads = 768; // most of a block: 80 registers a thread
+constexpr int kBwdThreads = 512; // most of a block, one block an SM: 128 registers a thread
+constexpr int kMostBarriers = 15; // of groups: a block has 16, __syncthreads takes one
+constexpr int kBwdStages = 3;     // rows in shared memory
+constexpr int kBwdSums = 2 * 2 * 32; // floats of a group for its rows' sums
 
-// Elements that a lane holds: 32 bytes of x.
-template <typename T, int V> constexpr int kBwdHeld = V > 1 ? 32 / sizeof(T) : 8;
+// Elements that a lane holds: 64 bytes of x.  (32 bytes and twice the lanes
+// cost twice the instructions for a row's sums and addresses.)
+template <typename T, int V> constexpr int kBwdHeld = V > 1 ? 64 / sizeof(T) : 16;
+
+// One pack to shared memory, asynchronously where it has a size that can be.
+template <typename T, int V> __device__ __forceinline__ void stage_pack(T *to, const T *from)
+{
+    constexpr int bytes = V * sizeof(T);
+    if constexpr (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                     : "memory");
+    else if constexpr (bytes >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from),
+                     "n"(bytes)
+                     : "memory");
+    else
+        *to = *from;
+}
 
 template <typename T, typename W, int V, bool MULTI>
-__global__ void __launch_bounds__(kBwdThreads) norm_grad_kernel(const Bwd a)
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
 {
     constexpr int K = kBwdHeld<T, V> / V;
-    extern __shared__ __align__(16) float sums[];                // [2][dim], if there are several groups
-    __shared__ float sm[MULTI ? 24 * 2 * 32 : 1][2]; // of every group
+    // the groups' sums, then the stages; after the last row: [2][dim]
+    extern __shared__ __align__(16) float smem[];
     const T *const dy = static_cast<const T *>(a.dy), *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
     const W *const gamma = static_cast<const W *>(a.gamma);
     const int lanes = a.g.lanes(), li = threadIdx.x % lanes, group = threadIdx.x / lanes,
               groups = blockDim.x / lanes;
-    const long long units = a.dim / V, step = (long long)gridDim.x * groups;
-    const float n = (float)a.dim;
-    float *const own = MULTI ? sm[group * 64] : sm[0];
-    int turn = 0;
-    float dg[K][V] = {}, db[K][V] = {};
-    Raw<T, V> vx[K], vd[K], nx[K], nd[K];
-    float next_mu = 0.0f, next_rs = 0.0f;
+    using P = Values<V>;
+    using E = typename P::E;
+    const int units = (int)a.dim / V; // (a held row is short)
+    const long long step = (long long)gridDim.x * groups;
+    const float n = (float)a.dim, inverse = 1.0f / n;
+    GroupOf mine = group_of(a.g, smem + group * kBwdSums, 1 + group);
+    if (MULTI) {
+        for (int i = threadIdx.x; i < groups * kBwdSums; i += blockDim.x)
+            smem[i] = 0.0f;
+        __syncthreads();
+    }
+    T *const stages = reinterpret_cast<T *>(smem + (MULTI ? groups * kBwdSums : 0));
+    bool in[K];  // does the lane hold a k-th pack?
+    int col[K]; // its first column; that of the row's last pack if not
+    E dg[K][P::N], db[K][P::N];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        in[k] = li + k * lanes < units;
+        col[k] = min(li + k * lanes, units - 1) * V;
+#pragma unroll
+        for (int m = 0; m < P::N; ++m)
+            dg[k][m] = db[k][m] = P::all(0.0f);
+    }
 
-    long long base = (long long)blockIdx.x * groups;
-    const auto read = [&](long long r) {
-        if (r < a.rows) {
-            next_mu = a.mean[r];
-            next_rs = a.rstd[r];
-        }
+    // The lane's k-th pack of x is k slots behind the stage's first, that of dy
+    // K slots further.  Packs that are not there stay zero and add nothing.
+    constexpr int kSlot = kBwdThreads * V, kStage = 2 * K * kSlot;
+    const int apart = lanes * V;
+    T *const slots = stages + threadIdx.x * V;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (!in[k])
+#pragma unroll
+            for (int i = 0; i < kBwdStages; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    slots[i * kStage + k * kSlot + j] = slots[i * kStage + (K + k) * kSlot + j] =
+                        from_f32<T>(0.0f);
+    const auto stage_row = [&](T *to, bool there, const T *px, const T *pd) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (r < a.rows && li + k * lanes < units) {
-                const long long at = r * a.dim + (long long)(li + k * lanes) * V;
-                nx[k].load(x + at);
-                nd[k].load(dy + at);
+            if (there && in[k]) {
+                stage_pack<T, V>(to + k * kSlot, px + k * apart);
+                stage_pack<T, V>(to + (K + k) * kSlot, pd + k * apart);
             }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    read(base + group);
-    for (; base < a.rows; base += step) {
-        const long long r = base + group;
-        const bool on = r < a.rows;
+    long long r = (long long)blockIdx.x * groups + group;
+    const long long row_step = step * a.dim;
+    const T *px = x + r * a.dim + li * V, *pd = dy + r * a.dim + li * V; // staged next
+    T *q = dx + r * a.dim + li * V;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            vx[k] = nx[k];
-            vd[k] = nd[k];
+    for (int i = 0; i < kBwdStages - 1; ++i, px += row_step, pd += row_step)
+        stage_row(slots + i * kStage, r + i * step < a.rows, px, pd);
+    float next_mu = 0.0f, next_rs = 0.0f;
+    if (r < a.rows) {
+        next_mu = a.mean[r];
+        next_rs = a.rstd[r];
+    }
+    int stage = 0;
+    // a group of several warps has barriers of its own: it ends with its last
+    // row; the groups of a warp go on together
+    const long long end = MULTI ? a.rows : a.rows + group - (group & -(32 / lanes));
+    for (; r < end; r += step, px += row_step, pd += row_step, q += row_step) {
+        const bool on = MULTI || r < a.rows;
+        const T *const now = slots + stage * kStage;
+        stage = stage == kBwdStages - 1 ? 0 : stage + 1;
+        // (the stage after the next one: the one that the last row was in)
+        stage_row(slots + (stage == kBwdStages - 1 ? 0 : stage + 1) * kStage,
+                  r + (kBwdStages - 1) * step < a.rows, px, pd);
+        const E minus = P::all(-next_mu), scale = P::all(next_rs);
+        const float rs = next_rs;
+        if (r + step < a.rows) {
+            next_mu = a.mean[r + step];
+            next_rs = a.rstd[r + step];
         }
-        const float mu = next_mu, rs = next_rs;
-        read(r + step);
-        Sums<2> s{};
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+        E s0 = P::all(0.0f), s1 = s0;
+        if (on) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units) {
-                float g[V];
-                load_weights<W, V>(gamma, (long long)(li + k * lanes) * V, 1.0f, g);
+            for (int k = 0; k < K; ++k) {
+                Raw<T, V> vx, vd;
+                vx.load(now + k * kSlot);
+                vd.load(now + (K + k) * kSlot);
+                E g[P::N];
+                load_weights<W, V>(gamma, col[k], 1.0f, g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = vd[k].get(j), xh = (vx[k].get(j) - mu) * rs, w = d * g[j];
-                    s.v[0] += w;
-                    s.v[1] = fmaf(w, xh, s.v[1]);
-                    dg[k][j] = fmaf(d, xh, dg[k][j]);
-                    db[k][j] += d;
+                for (int m = 0; m < P::N; ++m) {
+                    const E d = P::get(vd, m), xh = mul(add(P::get(vx, m), minus), scale),
+                            w = mul(d, g[m]);
+                    s0 = add(s0, w);
+                    s1 = fma(w, xh, s1);
+                    dg[k][m] = fma(d, xh, dg[k][m]);
+                    db[k][m] = add(db[k][m], d);
                 }
             }
+        }
         if (!dx)
             continue;
-        s = group_sum<MULTI, 2>(s, a.g, own, turn, 1 + group);
-        const float m0 = s.v[0] / n, m1 = s.v[1] / n;
+        Sums<2> s{{sum_of(s0), sum_of(s1)}};
+        s = group_sum<MULTI, 2>(s, mine);
+        // dx = rs w - rs mean(w) - xh rs mean(w xh)
+        const E m0 = P::all(-rs * quotient(s.v[0], n, inverse)),
+                m1 = P::all(-rs * quotient(s.v[1], n, inverse));
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (on && li + k * lanes < units) {
-                const long long c = (long long)(li + k * lanes) * V;
-                float g[V];
-                load_weights<W, V>(gamma, c, 1.0f, g);
-                T o[V];
+        for (int k = 0; k < K; ++k) {
+            Raw<T, V> vx, vd;
+            vx.load(now + k * kSlot);
+            vd.load(now + (K + k) * kSlot);
+            E g[P::N];
+            load_weights<W, V>(gamma, col[k], 1.0f, g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xh = (vx[k].get(j) - mu) * rs;
-                    o[j] = from_f32<T>(rs * (fmaf(vd[k].get(j), g[j], -m0) - xh * m1));
-                }
-                store_values<T, V>(dx + r * a.dim + c, o);
+            for (int m = 0; m < P::N; ++m) {
+                const E xh = mul(add(P::get(vx, m), minus), scale);
+                const E w = mul(P::get(vd, m), g[m]);
+                g[m] = fma(xh, m1, fma(w, scale, m0));
             }
+            if (on && in[k])
+                store_vals<T, V>(q + k * apart, g);
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     dependents_launch();
     if (!a.dgamma && !a.dbeta)
         return;
 
     float *const out = a.part + 2LL * blockIdx.x * a.dim;
+    float fg[K][V], fb[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        P::to_array(dg[k], fg[k]);
+        P::to_array(db[k], fb[k]);
+    }
     if constexpr (!MULTI) { // the warp's groups first
         for (int o = lanes; o < 32; o <<= 1)
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    dg[k][j] += __shfl_xor_sync(kFull, dg[k][j], o);
-                    db[k][j] += __shfl_xor_sync(kFull, db[k][j], o);
+                    fg[k][j] += __shfl_xor_sync(kFull, fg[k][j], o);
+                    fb[k][j] += __shfl_xor_sync(kFull, fb[k][j], o);
                 }
     }
     const int holders = MULTI ? groups : blockDim.x / 32, me = MULTI ? group : threadIdx.x / 32;
     const bool holds = MULTI || threadIdx.x % 32 < lanes;
-    float *const to = holders > 1 ? sums : out;
+    float *const to = holders > 1 ? smem : out; // (the stages are done with)
+    __syncthreads();
     for (int h = 0; h < holders; ++h) {
         if (h == me && holds)
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (li + k * lanes < units) {
-                    const long long c = (long long)(li + k * lanes) * V;
+                if (in[k]) {
+                    float *const pg = to + (li + k * lanes) * V, *const pb = pg + a.dim;
                     if (h > 0) {
-                        float p[V], q[V];
-                        load_values<float, V>(to + c, p);
+                        float u[V];
+                        load_values<float, V>(pg, u);
 #pragma unroll
                         for (int j = 0; j < V; ++j)
-                            dg[k][j] += p[j];
+                            fg[k][j] += u[j];
+                        load_values<float, V>(pb, u);
 #pragma unroll
                         for (int j = 0; j < V; ++j)
-                            q[j] = to[a.dim + c + j];
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            db[k][j] += q[j];
+                            fb[k][j] += u[j];
                     }
-                    store_values<float, V>(to + c, dg[k]);
-                    store_values<float, V>(to + a.dim + c, db[k]);
+                    store_values<float, V>(pg, fg[k]);
+                    store_values<float, V>(pb, fb[k]);
                 }
         if (holders > 1)
             __syncthreads();
     }
     if (holders > 1)
         for (long long c = threadIdx.x; c < 2 * a.dim; c += blockDim.x)
-            out[c] = sums[c];
+            out[c] = smem[c];
 }
 
 constexpr int kThreads = 256;
@@ -411,10 +567,10 @@ constexpr int kThreads = 256;
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(const Bwd a)
 {
-    __shared__ float sm[2 * 2 * 32];
+    __shared__ __align__(16) float sm[2 * 2 * 32];
     const T *const dy = static_cast<const T *>(a.dy), *const x = static_cast<const T *>(a.x);
     const W *const gamma = static_cast<const W *>(a.gamma);
-    int turn = 0;
+    GroupOf block = group_of(Group{5, kLongThreads / 32}, sm, 1);
     for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const float mu = a.mean[r], rs = a.rstd[r], n = (float)a.dim;
         Sums<2> s{};
@@ -423,7 +579,7 @@ __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(const Bwd a)
             s.v[0] += w;
             s.v[1] = fmaf(w, (to_f32(x[r * a.dim + c]) - mu) * rs, s.v[1]);
         }
-        s = block_sums<2>(s, sm, turn);
+        s = group_sum<true, 2>(s, block);
         const float m0 = s.v[0] / n, m1 = s.v[1] / n;
         for (long long c = threadIdx.x; c < a.dim; c += kLongThreads) {
             const float g = gamma ? to_f32(gamma[c]) : 1.0f;
@@ -505,14 +661,15 @@ template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
     if (s.held) {
         s.g = group_for(s.packs ? a.dim / V : a.dim, held / (s.packs ? V : 1));
         // one block per SM; groups of a block only where rows are many
-        const long long most = std::max(1, (s.g.warps > 1 ? kBwdThreads : kThreads) / s.g.lanes());
+        const long long most = std::min(std::max(1, kBwdThreads / s.g.lanes()),
+                                        s.g.warps > 1 ? kMostBarriers : kBwdThreads);
         s.groups = (int)std::max(1LL, std::min(most, a.rows / num_sms()));
         if (s.g.warps == 1) { // whole warps
             const int in_warp = 32 / s.g.lanes();
             s.groups = std::max(1, s.groups / in_warp) * in_warp;
         }
         const long long blocks = (a.rows + s.groups - 1) / s.groups;
-        s.parts = (int)std::min(blocks, (long long)num_sms() * (s.g.warps == 1 ? 3 : 1));
+        s.parts = (int)std::min(blocks, (long long)num_sms());
     } else {
         const long long stretch = std::max(16LL, (a.rows + 127) / 128);
         s.groups = 1;
@@ -525,10 +682,12 @@ template <typename T, typename W, int V> cudaError_t held_rows(Bwd a, const BwdS
                                                                cudaStream_t st)
 {
     const int threads = s.groups * s.g.lanes();
-    const bool several = s.g.warps > 1 ? s.groups > 1 : threads > 32;
-    const int smem = several ? (int)(8 * a.dim) : 0;
+    // the slots of a whole block, whatever its size: their distance is a constant
+    const size_t stages = (size_t)kBwdStages * 2 * kBwdHeld<T, V> * sizeof(T) * kBwdThreads,
+                 sums = s.g.warps > 1 ? sizeof(float) * kBwdSums * s.groups : 0;
+    const int smem = (int)std::max(sums + stages, 8 * (size_t)a.dim);
     const auto fn = s.g.warps > 1 ? norm_grad_kernel<T, W, V, true> : norm_grad_kernel<T, W, V, false>;
-    if (smem > 32768) {
+    if (smem > 49152) {
         const cudaError_t e =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)

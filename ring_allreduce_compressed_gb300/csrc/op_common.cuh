@@ -53,6 +53,12 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
 template <typename T, int V> struct Raw {
     static constexpr int kWords = V * sizeof(T) / 4;
     uint32_t w[kWords];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[i] = 0;
+    }
     __device__ __forceinline__ void load(const T *p)
     {
         const Pack<uint32_t, kWords> q =
@@ -73,6 +79,7 @@ template <typename T, int V> struct Raw {
 };
 template <typename T> struct Raw<T, 1> {
     T v;
+    __device__ __forceinline__ void clear() { v = from_f32<T>(0.0f); }
     __device__ __forceinline__ void load(const T *p) { v = *p; }
     __device__ __forceinline__ float get(int) const { return to_f32(v); }
 };
@@ -103,6 +110,81 @@ template <typename T, int V> __device__ __forceinline__ void load_values(const T
             v[i + j] = q.e[j];
     }
 }
+
+// Values of a pack as the arithmetic takes them: pairs for the paired fp32
+// instructions (two IEEE operations each), or a single float.
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair_of(float lo, float hi)
+{
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves(Pair p, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum_of(float a) { return a; }
+__device__ __forceinline__ float sum_of(Pair p)
+{
+    float lo, hi;
+    halves(p, lo, hi);
+    return lo + hi;
+}
+
+// The values of a pack of V elements: N of type E.
+template <int V> struct Values {
+    using E = Pair;
+    static constexpr int N = V / 2;
+    static __device__ __forceinline__ E all(float v) { return pair_of(v, v); }
+    template <typename R> static __device__ __forceinline__ E get(const R &raw, int n)
+    {
+        return pair_of(raw.get(2 * n), raw.get(2 * n + 1));
+    }
+    static __device__ __forceinline__ void to_array(const E (&e)[N], float (&v)[V])
+    {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            halves(e[n], v[2 * n], v[2 * n + 1]);
+    }
+    static __device__ __forceinline__ E from_array(const float (&v)[V], int n)
+    {
+        return pair_of(v[2 * n], v[2 * n + 1]);
+    }
+};
+template <> struct Values<1> {
+    using E = float;
+    static constexpr int N = 1;
+    static __device__ __forceinline__ E all(float v) { return v; }
+    template <typename R> static __device__ __forceinline__ E get(const R &raw, int)
+    {
+        return raw.get(0);
+    }
+    static __device__ __forceinline__ void to_array(const E (&e)[1], float (&v)[1]) { v[0] = e[0]; }
+    static __device__ __forceinline__ E from_array(const float (&v)[1], int) { return v[0]; }
+};
 
 __device__ __forceinline__ float warp_sum(float v)
 {
