@@ -438,14 +438,35 @@ def diff_encode(cur, prev, diff, stream=None):
 # on `stream` (default: the current one); nothing is allocated for it, so
 # tensors used on another stream than their own are the caller's to keep alive.
 
-def _op(t, name, dtype=None, shape=None):
-    """Address of a contiguous tensor on the current device, or None for None."""
-    import torch
+_ops = None
+
+
+class _Ops:
+    """What every call of these operators looks up, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.lib = lib()
+        self.dtypes = {torch.float32: RRA_F32, torch.float16: RRA_F16, torch.bfloat16: RRA_BF16}
+        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
+        self.device = torch.cuda.current_device
+        self.stream = torch.cuda.current_stream
+
+
+def _setup():
+    global _ops
+    if _ops is None:
+        _ops = _Ops()
+    return _ops
+
+
+def _op(t, name, device, dtype=None, shape=None):
+    """Address of a contiguous tensor on `device`, or None for None."""
     if t is None:
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on the current device")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -454,11 +475,18 @@ def _op(t, name, dtype=None, shape=None):
     return t.data_ptr()
 
 
-def _grad_list(grads, name):
+def _op_dtype(ops, t) -> int:
+    code = ops.dtypes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _grad_list(ops, grads, name, device):
     n = len(grads)
-    return ((C.c_void_p * n)(*[_op(g, name) for g in grads]),
+    return ((C.c_void_p * n)(*[_op(g, name, device) for g in grads]),
             (C.c_size_t * n)(*[g.numel() for g in grads]),
-            (C.c_int * n)(*[_dtype_code(g.dtype) for g in grads]))
+            (C.c_int * n)(*[_op_dtype(ops, g) for g in grads]))
 
 
 def _norm_code(p) -> int:
@@ -471,37 +499,43 @@ def _norm_code(p) -> int:
 def grad_norm(grads: Sequence, norm, norm_type=2, stream=None):
     """rra_grad_norm: norm[0] (fp32, on the device) = the norm of all tensors of
     ``grads`` taken as one vector; their types may differ."""
-    import torch
-    ptrs, counts, dtypes = _grad_list(grads, "grads")
-    _check(lib().rra_grad_norm(ptrs, counts, dtypes, len(grads), _norm_code(norm_type),
-                               _op(norm, "norm", torch.float32, (1,)), _stream(stream)),
-           "rra_grad_norm")
+    kind = _norm_code(norm_type)
+    if not norm.is_cuda:
+        raise ValueError("norm: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    ptrs, counts, dtypes = _grad_list(ops, grads, "grads", dev)
+    _check(ops.lib.rra_grad_norm(ptrs, counts, dtypes, len(grads), kind,
+                                 _op(norm, "norm", dev, ops.f32, (1,)),
+                                 (stream or ops.stream()).cuda_stream), "rra_grad_norm")
 
 
 def grad_clip(grads: Sequence, outs: Sequence, max_norm: float, norm, norm_type=2,
               eps: float = 1e-6, stream=None):
     """rra_grad_clip: outs[k] = grads[k] * min(1, max_norm / (n + eps)), n the
     norm of all of them, stored in norm[0].  outs may be grads (in place)."""
-    import torch
-    ptrs, counts, dtypes = _grad_list(grads, "grads")
+    kind = _norm_code(norm_type)
+    if not norm.is_cuda:
+        raise ValueError("norm: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    ptrs, counts, dtypes = _grad_list(ops, grads, "grads", dev)
     if outs is grads:
         optrs = ptrs
     else:
         if len(outs) != len(grads):
             raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
-        optrs = (C.c_void_p * len(outs))(*[_op(o, "outs", g.dtype, g.shape)
+        optrs = (C.c_void_p * len(outs))(*[_op(o, "outs", dev, g.dtype, g.shape)
                                            for o, g in zip(outs, grads)])
-    _check(lib().rra_grad_clip(ptrs, optrs, counts, dtypes, len(grads), _norm_code(norm_type),
-                               float(max_norm), float(eps),
-                               _op(norm, "norm", torch.float32, (1,)), _stream(stream)),
-           "rra_grad_clip")
+    _check(ops.lib.rra_grad_clip(ptrs, optrs, counts, dtypes, len(grads), kind, max_norm, eps,
+                                 _op(norm, "norm", dev, ops.f32, (1,)),
+                                 (stream or ops.stream()).cuda_stream), "rra_grad_clip")
 
 
-def _index_code(t) -> int:
-    import torch
-    if t.dtype is torch.int64:
+def _index_code(ops, t) -> int:
+    if t.dtype is ops.i64:
         return RRA_I64
-    if t.dtype is torch.int32:
+    if t.dtype is ops.i32:
         return RRA_I32
     raise TypeError(f"tokens: expected int32 or int64, got {t.dtype}")
 
@@ -511,12 +545,16 @@ def embedding(weight, tokens, out, scale: float = 1.0, stream=None):
     (vocab, dim) weight; tokens outside the table give zeros."""
     if weight.dim() != 2:
         raise ValueError("weight: expected (vocab, dim)")
+    if not weight.is_cuda:
+        raise ValueError("weight: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
     vocab, dim = weight.shape
-    _check(lib().rra_embedding(_op(weight, "weight"), _op(tokens, "tokens"), tokens.numel(),
-                               vocab, dim, _dtype_code(weight.dtype), _index_code(tokens),
-                               float(scale),
-                               _op(out, "out", weight.dtype, tokens.shape + (dim,)),
-                               _stream(stream)), "rra_embedding")
+    _check(ops.lib.rra_embedding(_op(weight, "weight", dev), _op(tokens, "tokens", dev),
+                                 tokens.numel(), vocab, dim, _op_dtype(ops, weight),
+                                 _index_code(ops, tokens), scale,
+                                 _op(out, "out", dev, weight.dtype, tokens.shape + (dim,)),
+                                 (stream or ops.stream()).cuda_stream), "rra_embedding")
 
 
 def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optional[int] = None,
@@ -525,13 +563,18 @@ def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optio
     token is v (zero where there is none), or added to dweight."""
     if dweight.dim() != 2:
         raise ValueError("dweight: expected (vocab, dim)")
+    if not dweight.is_cuda:
+        raise ValueError("dweight: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
     vocab, dim = dweight.shape
-    _check(lib().rra_embedding_grad(_op(dout, "dout", None, tokens.shape + (dim,)),
-                                    _op(tokens, "tokens"), tokens.numel(), vocab, dim,
-                                    _dtype_code(dout.dtype), _index_code(tokens), float(scale),
-                                    -1 if padding_idx is None else int(padding_idx),
-                                    _op(dweight, "dweight"), _dtype_code(dweight.dtype),
-                                    1 if accumulate else 0, _stream(stream)),
+    _check(ops.lib.rra_embedding_grad(_op(dout, "dout", dev, None, tokens.shape + (dim,)),
+                                      _op(tokens, "tokens", dev), tokens.numel(), vocab, dim,
+                                      _op_dtype(ops, dout), _index_code(ops, tokens), scale,
+                                      -1 if padding_idx is None else padding_idx,
+                                      _op(dweight, "dweight", dev), _op_dtype(ops, dweight),
+                                      1 if accumulate else 0,
+                                      (stream or ops.stream()).cuda_stream),
            "rra_embedding_grad")
 
 
@@ -546,15 +589,20 @@ def layer_norm(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, strea
     """rra_layer_norm over the last dimension of x: y = (x - mean) * rstd *
     gamma + beta; gamma and beta may be None.  mean and rstd (fp32, one value
     a row) are stored when given: layer_norm_grad needs them."""
-    import torch
     rows, dim = _rows(x, "x")
+    if not x.is_cuda:
+        raise ValueError("x: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
     wt = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
-    _check(lib().rra_layer_norm(_op(x, "x"), _op(gamma, "gamma", wt, (dim,)),
-                                _op(beta, "beta", wt, (dim,)), rows, dim, _dtype_code(x.dtype),
-                                _dtype_code(wt), float(eps), _op(y, "y", x.dtype, x.shape),
-                                _op(mean, "mean", torch.float32, (rows,)),
-                                _op(rstd, "rstd", torch.float32, (rows,)), _stream(stream)),
-           "rra_layer_norm")
+    w = gamma if gamma is not None else beta if beta is not None else x
+    _check(ops.lib.rra_layer_norm(_op(x, "x", dev), _op(gamma, "gamma", dev, wt, (dim,)),
+                                  _op(beta, "beta", dev, wt, (dim,)), rows, dim,
+                                  _op_dtype(ops, x), _op_dtype(ops, w), eps,
+                                  _op(y, "y", dev, x.dtype, x.shape),
+                                  _op(mean, "mean", dev, ops.f32, (rows,)),
+                                  _op(rstd, "rstd", dev, ops.f32, (rows,)),
+                                  (stream or ops.stream()).cuda_stream), "rra_layer_norm")
 
 
 def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: bool = False,
@@ -562,15 +610,22 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: boo
     """rra_layer_norm_grad: the gradients of x, gamma and beta from dy and the
     forward pass's x, mean and rstd.  dx may be dy or x; outputs that are None
     are not computed; accumulate adds to what dgamma and dbeta hold."""
-    import torch
     rows, dim = _rows(x, "x")
-    wt = next((t.dtype for t in (gamma, dgamma, dbeta) if t is not None), x.dtype)
-    _check(lib().rra_layer_norm_grad(_op(dy, "dy", x.dtype, x.shape), _op(x, "x"),
-                                     _op(gamma, "gamma", wt, (dim,)),
-                                     _op(mean, "mean", torch.float32, (rows,)),
-                                     _op(rstd, "rstd", torch.float32, (rows,)), rows, dim,
-                                     _dtype_code(x.dtype), _dtype_code(wt),
-                                     _op(dx, "dx", x.dtype, x.shape),
-                                     _op(dgamma, "dgamma", wt, (dim,)),
-                                     _op(dbeta, "dbeta", wt, (dim,)), 1 if accumulate else 0,
-                                     _stream(stream)), "rra_layer_norm_grad")
+    if not x.is_cuda:
+        raise ValueError("x: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    w = gamma if gamma is not None else dgamma if dgamma is not None else \
+        dbeta if dbeta is not None else x
+    wt = w.dtype
+    _check(ops.lib.rra_layer_norm_grad(_op(dy, "dy", dev, x.dtype, x.shape), _op(x, "x", dev),
+                                       _op(gamma, "gamma", dev, wt, (dim,)),
+                                       _op(mean, "mean", dev, ops.f32, (rows,)),
+                                       _op(rstd, "rstd", dev, ops.f32, (rows,)), rows, dim,
+                                       _op_dtype(ops, x), _op_dtype(ops, w),
+                                       _op(dx, "dx", dev, x.dtype, x.shape),
+                                       _op(dgamma, "dgamma", dev, wt, (dim,)),
+                                       _op(dbeta, "dbeta", dev, wt, (dim,)),
+                                       1 if accumulate else 0,
+                                       (stream or ops.stream()).cuda_stream),
+           "rra_layer_norm_grad")

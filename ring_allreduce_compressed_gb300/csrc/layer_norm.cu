@@ -351,14 +351,19 @@ struct Bwd {
     Group g;
 };
 
-constexpr int kBwdThreads = 512; // most of a block, one block an SM: 128 registers a thread
+// Most threads of a block, one block an SM.  384 leave a thread the registers
+// for 32 elements of 16 bits (64 bytes of x) and their sums: 75 us at
+// 16384 x 4096 bf16, where 512 threads took 84 and 768 with half the elements
+// 111 -- a row's own sums, barrier and addresses cost as much for few elements.
+// Rows that 384 threads do not hold take 512.
+constexpr int kBwdThreads = 384, kBwdWide = 512;
 constexpr int kMostBarriers = 15; // of groups: a block has 16, __syncthreads takes one
-constexpr int kBwdStages = 3;     // rows in shared memory
+constexpr int kBwdStages = 2; // rows in shared memory
 constexpr int kBwdSums = 2 * 2 * 32; // floats of a group for its rows' sums
 
-// Elements that a lane holds: 64 bytes of x.  (32 bytes and twice the lanes
-// cost twice the instructions for a row's sums and addresses.)
-template <typename T, int V> constexpr int kBwdHeld = V > 1 ? 64 / sizeof(T) : 16;
+// Elements that a lane holds.
+template <typename T, int V, int THREADS>
+constexpr int kBwdHeld = V > 1 ? 64 / sizeof(T) : THREADS == kBwdThreads ? 8 : 16;
 
 // One pack to shared memory, asynchronously where it has a size that can be.
 template <typename T, int V> __device__ __forceinline__ void stage_pack(T *to, const T *from)
@@ -375,11 +380,11 @@ template <typename T, int V> __device__ __forceinline__ void stage_pack(T *to, c
         *to = *from;
 }
 
-template <typename T, typename W, int V, bool MULTI>
-__global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
+template <typename T, typename W, int V, bool MULTI, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
 {
-    constexpr int K = kBwdHeld<T, V> / V;
-    // the groups' sums, then the stages; after the last row: [2][dim]
+    constexpr int K = kBwdHeld<T, V, THREADS> / V;
+    // gamma as fp32, the groups' sums, the stages; after the last row: [2][dim]
     extern __shared__ __align__(16) float smem[];
     const T *const dy = static_cast<const T *>(a.dy), *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
@@ -391,13 +396,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
     const int units = (int)a.dim / V; // (a held row is short)
     const long long step = (long long)gridDim.x * groups;
     const float n = (float)a.dim, inverse = 1.0f / n;
-    GroupOf mine = group_of(a.g, smem + group * kBwdSums, 1 + group);
-    if (MULTI) {
+    float *const weights = smem, *const sums = weights + ((int)a.dim + 3) / 4 * 4;
+    GroupOf mine = group_of(a.g, sums + group * kBwdSums, 1 + group);
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
+        weights[c] = gamma ? to_f32(gamma[c]) : 1.0f;
+    if (MULTI)
         for (int i = threadIdx.x; i < groups * kBwdSums; i += blockDim.x)
-            smem[i] = 0.0f;
-        __syncthreads();
-    }
-    T *const stages = reinterpret_cast<T *>(smem + (MULTI ? groups * kBwdSums : 0));
+            sums[i] = 0.0f;
+    __syncthreads();
+    T *const stages = reinterpret_cast<T *>(sums + (MULTI ? groups * kBwdSums : 0));
     bool in[K];  // does the lane hold a k-th pack?
     int col[K]; // its first column; that of the row's last pack if not
     E dg[K][P::N], db[K][P::N];
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
 
     // The lane's k-th pack of x is k slots behind the stage's first, that of dy
     // K slots further.  Packs that are not there stay zero and add nothing.
-    constexpr int kSlot = kBwdThreads * V, kStage = 2 * K * kSlot;
+    constexpr int kSlot = THREADS * V, kStage = 2 * K * kSlot;
     const int apart = lanes * V;
     T *const slots = stages + threadIdx.x * V;
 #pragma unroll
@@ -452,10 +459,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
     for (; r < end; r += step, px += row_step, pd += row_step, q += row_step) {
         const bool on = MULTI || r < a.rows;
         const T *const now = slots + stage * kStage;
-        stage = stage == kBwdStages - 1 ? 0 : stage + 1;
-        // (the stage after the next one: the one that the last row was in)
-        stage_row(slots + (stage == kBwdStages - 1 ? 0 : stage + 1) * kStage,
+        // into the stage that the last row was in
+        stage_row(slots + (stage == 0 ? kBwdStages - 1 : stage - 1) * kStage,
                   r + (kBwdStages - 1) * step < a.rows, px, pd);
+        stage = stage == kBwdStages - 1 ? 0 : stage + 1;
         const E minus = P::all(-next_mu), scale = P::all(next_rs);
         const float rs = next_rs;
         if (r + step < a.rows) {
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
                 vx.load(now + k * kSlot);
                 vd.load(now + (K + k) * kSlot);
                 E g[P::N];
-                load_weights<W, V>(gamma, col[k], 1.0f, g);
+                load_weights<float, V>(weights, col[k], 1.0f, g);
 #pragma unroll
                 for (int m = 0; m < P::N; ++m) {
                     const E d = P::get(vd, m), xh = mul(add(P::get(vx, m), minus), scale),
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_grad_kernel(const Bwd a)
             vx.load(now + k * kSlot);
             vd.load(now + (K + k) * kSlot);
             E g[P::N];
-            load_weights<W, V>(gamma, col[k], 1.0f, g);
+            load_weights<float, V>(weights, col[k], 1.0f, g);
 #pragma unroll
             for (int m = 0; m < P::N; ++m) {
                 const E xh = mul(add(P::get(vx, m), minus), scale);
@@ -609,36 +616,41 @@ __global__ void __launch_bounds__(kThreads) weight_long_kernel(const Bwd a, long
     }
 }
 
-// Adds the partial rows: a block takes 32 columns of [dgamma, dbeta], its
-// warps a stretch of the partial rows each.
-constexpr int kWarps = kThreads / 32;
-
-template <typename W> __global__ void __launch_bounds__(kThreads) join_kernel(const Bwd a)
+// Adds the partial rows: a block takes 32 columns of [dgamma, dbeta], 32 / V
+// threads for each of its 8 V stretches of the partial rows.
+template <typename W, int V> __global__ void __launch_bounds__(kThreads) join_kernel(const Bwd a)
 {
-    __shared__ float sm[kWarps][32];
+    constexpr int kLanes = 32 / V, kStretches = kThreads / kLanes;
+    __shared__ float sm[kStretches][33];
     dependents_wait();
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-    const int lo = (int)((long long)a.parts * w / kWarps),
-              hi = (int)((long long)a.parts * (w + 1) / kWarps);
+    const int t = threadIdx.x % kLanes, s = threadIdx.x / kLanes;
+    const int lo = (int)((long long)a.parts * s / kStretches),
+              hi = (int)((long long)a.parts * (s + 1) / kStretches);
     for (long long c0 = 32LL * blockIdx.x; c0 < 2 * a.dim; c0 += 32LL * gridDim.x) {
-        const long long c = c0 + lane;
-        float s = 0.0f;
-        if (c < 2 * a.dim)
+        float sum[V] = {};
+        if (c0 + t * V < 2 * a.dim)
 #pragma unroll 8
-            for (int p = lo; p < hi; ++p)
-                s += a.part[2LL * p * a.dim + c];
-        __syncthreads();
-        sm[w][lane] = s;
-        __syncthreads();
-        if (w == 0 && c < 2 * a.dim) {
-            s = 0.0f;
+            for (int p = lo; p < hi; ++p) {
+                const Pack<float, V> v = load_pack<float, V>(a.part + 2LL * p * a.dim + c0 + t * V);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                s += sm[k][lane];
+                for (int j = 0; j < V; ++j)
+                    sum[j] += v.e[j];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            sm[s][t * V + j] = sum[j];
+        __syncthreads();
+        const long long c = c0 + threadIdx.x;
+        if (threadIdx.x < 32 && c < 2 * a.dim) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kStretches; ++k)
+                v += sm[k][threadIdx.x];
             W *const to = static_cast<W *>(c < a.dim ? a.dgamma : a.dbeta);
             const long long at = c < a.dim ? c : c - a.dim;
             if (to)
-                to[at] = from_f32<W>(a.accumulate ? to_f32(to[at]) + s : s);
+                to[at] = from_f32<W>(a.accumulate ? to_f32(to[at]) + v : v);
         }
     }
 }
@@ -648,21 +660,26 @@ struct BwdShape {
     Group g;
     int groups; // of a block
     int parts;  // partial rows: blocks of the first kernel
-    bool packs, held;
+    int threads; // kBwdThreads, kBwdWide, or 0: rows that no block holds
+    bool packs;
 };
 
 template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
 {
     constexpr int V = 16 / sizeof(T);
     BwdShape s;
-    s.packs = packs_fit<T, W, V>(a.dim, {a.dy, a.x, a.dx}, {a.gamma});
-    const int held = s.packs ? kBwdHeld<T, V> : kBwdHeld<T, 1>;
-    s.held = a.dim <= (long long)kBwdThreads * held;
-    if (s.held) {
+    s.packs = packs_fit<T, float, V>(a.dim, {a.dy, a.x, a.dx}, {});
+    int held = s.packs ? kBwdHeld<T, V, kBwdThreads> : kBwdHeld<T, 1, kBwdThreads>;
+    s.threads = kBwdThreads;
+    if (a.dim > (long long)s.threads * held) {
+        held = s.packs ? kBwdHeld<T, V, kBwdWide> : kBwdHeld<T, 1, kBwdWide>;
+        s.threads = a.dim <= (long long)kBwdWide * held ? kBwdWide : 0;
+    }
+    if (s.threads) {
         s.g = group_for(s.packs ? a.dim / V : a.dim, held / (s.packs ? V : 1));
         // one block per SM; groups of a block only where rows are many
-        const long long most = std::min(std::max(1, kBwdThreads / s.g.lanes()),
-                                        s.g.warps > 1 ? kMostBarriers : kBwdThreads);
+        const long long most = std::min(std::max(1, s.threads / s.g.lanes()),
+                                        s.g.warps > 1 ? kMostBarriers : s.threads);
         s.groups = (int)std::max(1LL, std::min(most, a.rows / num_sms()));
         if (s.g.warps == 1) { // whole warps
             const int in_warp = 32 / s.g.lanes();
@@ -678,23 +695,33 @@ template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
     return s;
 }
 
-template <typename T, typename W, int V> cudaError_t held_rows(Bwd a, const BwdShape &s,
-                                                               cudaStream_t st)
+template <typename T, typename W, int V, bool MULTI, int THREADS>
+cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 {
-    const int threads = s.groups * s.g.lanes();
     // the slots of a whole block, whatever its size: their distance is a constant
-    const size_t stages = (size_t)kBwdStages * 2 * kBwdHeld<T, V> * sizeof(T) * kBwdThreads,
-                 sums = s.g.warps > 1 ? sizeof(float) * kBwdSums * s.groups : 0;
-    const int smem = (int)std::max(sums + stages, 8 * (size_t)a.dim);
-    const auto fn = s.g.warps > 1 ? norm_grad_kernel<T, W, V, true> : norm_grad_kernel<T, W, V, false>;
+    const size_t stages = (size_t)kBwdStages * 2 * kBwdHeld<T, V, THREADS> * sizeof(T) * THREADS,
+                 sums = MULTI ? sizeof(float) * kBwdSums * s.groups : 0,
+                 weights = sizeof(float) * ((a.dim + 3) / 4 * 4);
+    const int smem = (int)std::max(weights + sums + stages, 8 * (size_t)a.dim);
+    const auto fn = norm_grad_kernel<T, W, V, MULTI, THREADS>;
     if (smem > 49152) {
         const cudaError_t e =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
     }
-    fn<<<s.parts, threads, smem, st>>>(a);
+    fn<<<s.parts, s.groups * s.g.lanes(), smem, st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, typename W, int V>
+cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
+{
+    if (s.threads == kBwdWide)
+        return held_rows<T, W, V, true, kBwdWide>(a, s, st);
+    if (s.g.warps > 1)
+        return held_rows<T, W, V, true, kBwdThreads>(a, s, st);
+    return held_rows<T, W, V, false, kBwdThreads>(a, s, st);
 }
 
 template <typename T, typename W> cudaError_t backward(Bwd a, const BwdShape &s, cudaStream_t st)
@@ -703,7 +730,7 @@ template <typename T, typename W> cudaError_t backward(Bwd a, const BwdShape &s,
     a.g = s.g;
     a.parts = s.parts;
     if (a.rows > 0) {
-        if (s.held) {
+        if (s.threads) {
             e = s.packs ? held_rows<T, W, 16 / sizeof(T)>(a, s, st) : held_rows<T, W, 1>(a, s, st);
         } else {
             if (a.dgamma || a.dbeta) {
@@ -720,11 +747,12 @@ template <typename T, typename W> cudaError_t backward(Bwd a, const BwdShape &s,
     if (e != cudaSuccess || (!a.dgamma && !a.dbeta))
         return e;
     const unsigned grid = (unsigned)std::min((2 * a.dim + 31) / 32, 1LL << 20);
-    if (a.rows == 0) {
-        join_kernel<W><<<grid, kThreads, 0, st>>>(a);
+    const auto fn = a.dim % 4 == 0 ? join_kernel<W, 4> : join_kernel<W, 1>;
+    if (a.rows == 0) { // nothing of this call to be chained to
+        fn<<<grid, kThreads, 0, st>>>(a);
         return cudaGetLastError();
     }
-    return launch_chained(join_kernel<W>, dim3(grid), kThreads, st, a);
+    return launch_chained(fn, dim3(grid), kThreads, st, a);
 }
 
 template <typename T, typename W> rra_status backward_call(Bwd a, cudaStream_t st)
