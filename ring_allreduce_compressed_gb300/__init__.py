@@ -449,8 +449,11 @@ class _Ops:
         self.lib = lib()
         self.dtypes = {torch.float32: RRA_F32, torch.float16: RRA_F16, torch.bfloat16: RRA_BF16}
         self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
-        self.device = torch.cuda.current_device
-        self.stream = torch.cuda.current_stream
+        torch.cuda.init()
+        # the plain C functions below torch.cuda's: a fifth of their time
+        self.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _setup():
@@ -507,7 +510,7 @@ def grad_norm(grads: Sequence, norm, norm_type=2, stream=None):
     ptrs, counts, dtypes = _grad_list(ops, grads, "grads", dev)
     _check(ops.lib.rra_grad_norm(ptrs, counts, dtypes, len(grads), kind,
                                  _op(norm, "norm", dev, ops.f32, (1,)),
-                                 (stream or ops.stream()).cuda_stream), "rra_grad_norm")
+                                 stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_grad_norm")
 
 
 def grad_clip(grads: Sequence, outs: Sequence, max_norm: float, norm, norm_type=2,
@@ -529,7 +532,7 @@ def grad_clip(grads: Sequence, outs: Sequence, max_norm: float, norm, norm_type=
                                            for o, g in zip(outs, grads)])
     _check(ops.lib.rra_grad_clip(ptrs, optrs, counts, dtypes, len(grads), kind, max_norm, eps,
                                  _op(norm, "norm", dev, ops.f32, (1,)),
-                                 (stream or ops.stream()).cuda_stream), "rra_grad_clip")
+                                 stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_grad_clip")
 
 
 def _index_code(ops, t) -> int:
@@ -554,7 +557,7 @@ def embedding(weight, tokens, out, scale: float = 1.0, stream=None):
                                  tokens.numel(), vocab, dim, _op_dtype(ops, weight),
                                  _index_code(ops, tokens), scale,
                                  _op(out, "out", dev, weight.dtype, tokens.shape + (dim,)),
-                                 (stream or ops.stream()).cuda_stream), "rra_embedding")
+                                 stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_embedding")
 
 
 def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optional[int] = None,
@@ -574,7 +577,7 @@ def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optio
                                       -1 if padding_idx is None else padding_idx,
                                       _op(dweight, "dweight", dev), _op_dtype(ops, dweight),
                                       1 if accumulate else 0,
-                                      (stream or ops.stream()).cuda_stream),
+                                      stream.cuda_stream if stream is not None else ops.stream(dev)),
            "rra_embedding_grad")
 
 
@@ -602,7 +605,7 @@ def layer_norm(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, strea
                                   _op(y, "y", dev, x.dtype, x.shape),
                                   _op(mean, "mean", dev, ops.f32, (rows,)),
                                   _op(rstd, "rstd", dev, ops.f32, (rows,)),
-                                  (stream or ops.stream()).cuda_stream), "rra_layer_norm")
+                                  stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_layer_norm")
 
 
 def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: bool = False,
@@ -627,5 +630,5 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: boo
                                        _op(dgamma, "dgamma", dev, wt, (dim,)),
                                        _op(dbeta, "dbeta", dev, wt, (dim,)),
                                        1 if accumulate else 0,
-                                       (stream or ops.stream()).cuda_stream),
+                                       stream.cuda_stream if stream is not None else ops.stream(dev)),
            "rra_layer_norm_grad")

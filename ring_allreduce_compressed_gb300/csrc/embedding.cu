@@ -439,6 +439,9 @@ void lookup_any(const void *w, const void *tok, long long n, long long vocab, lo
         lookup<T, 1>(w, tok, n, vocab, dim, wide, scale, out, st);
 }
 
+// A table that is not worth a launch for its clearing: the joins' kernel does it.
+constexpr size_t kSmallTable = 8 << 20;
+
 // Table rows that are cleared during the sort: about what the other SMs write
 // in the time that it takes (none, 48 MB + 1 KB a token: 63, 56 us at 16384
 // tokens, 169, 152 us at 131072).
@@ -447,6 +450,8 @@ long long cleared_early(const SumArgs &a, size_t row)
     if (a.accumulate || a.n == 0 || a.n > kCsMost)
         return 0;
     const unsigned long long bytes = (48ull << 20) + 1024ull * a.n;
+    if (a.vocab * row <= kSmallTable)
+        return 0;
     return std::min((long long)(bytes / row), a.vocab);
 }
 

@@ -7,7 +7,8 @@
 // Both passes are bound by memory: the norm reads every gradient once, the
 // scaling reads it again and writes it.  The list is cut into tiles of 32 KB,
 // so that a block works on one tensor at a time and short tensors leave no SM
-// with more than its share.
+// with more than its share.  The scaling's blocks start beside the norm's and
+// have their first tile in registers when the norm is known.
 #include <math.h>
 
 #include "op_common.cuh"
@@ -17,8 +18,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTileBytes = 32768;
-constexpr int kUnroll = kTileBytes / (16 * kThreads); // 16-byte packs per thread and tile
+template <int THREADS> constexpr int kUnroll = kTileBytes / (16 * THREADS); // packs of a thread
 constexpr int kMostItems = 512;                       // tensors of one launch
+constexpr int kFewItems = 16; // of a launch with short arguments
+constexpr int kSmallBytes = 65536; // of a list that one block takes in one launch
 constexpr int kGridPerSm = 8;                         // 256-thread blocks: full SMs
 
 // One tensor of the list.  Its tiles start at a 16-byte boundary of `in`, so
@@ -33,18 +36,19 @@ struct Item {
     short dtype;
 };
 
-struct Args {
+// ITEMS: how many tensors there is room for.  Kernel arguments are copied and
+// read with every launch: 20 KB of them took longer than the norm of a bucket.
+template <int ITEMS> struct Args {
     int items;
     unsigned tiles;
-    int kind; // rra_norm
     int slot; // first partial of this launch
     int last; // the launch that joins the partials of all
     float max_norm, eps;
-    float *partial;   // 3 per slot
+    float4 *partial;  // a slot per block: {sum or maximum, big, small, 0}
     unsigned *ticket; // zero between calls
     float *coef;      // scratch: min(1, max_norm / (norm + eps))
     float *norm;
-    Item item[kMostItems];
+    Item item[ITEMS];
 };
 
 // Sums of squares over the whole range of fp32, without overflow and without
@@ -54,13 +58,21 @@ struct Args {
 // first are scaled by 2^-84, the last by 2^90.  A value far below its pack's
 // largest loses nothing that the sum could hold.
 struct Acc {
-    float mid = 0.0f, big = 0.0f, small = 0.0f;
+    float mid = 0.0f, low = 0.0f; // sum, and what rounding has taken from it
+    float big = 0.0f, small = 0.0f;
 };
 constexpr float kBig = 0x1p44f, kSmall = 0x1p-50f;
 constexpr float kBigScale = 0x1p-84f, kSmallScale = 0x1p90f;
 
-template <int V> __device__ __forceinline__ void add_squares(Acc &a, const float (&x)[V])
+template <int V, bool NARROW>
+__device__ __forceinline__ void add_squares(Acc &a, const float (&x)[V])
 {
+    if constexpr (NARROW) { // fp16: every square is in the middle range
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            a.mid = fmaf(x[i], x[i], a.mid);
+        return;
+    }
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -80,10 +92,11 @@ template <int V> __device__ __forceinline__ void add_squares(Acc &a, const float
     }
 }
 
-template <int KIND, int V> __device__ __forceinline__ void add_pack(Acc &a, const float (&x)[V])
+template <int KIND, int V, bool NARROW = false>
+__device__ __forceinline__ void add_pack(Acc &a, const float (&x)[V])
 {
     if constexpr (KIND == RRA_NORM_L2) {
-        add_squares<V>(a, x);
+        add_squares<V, NARROW>(a, x);
     } else if constexpr (KIND == RRA_NORM_L1) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -97,8 +110,23 @@ template <int KIND, int V> __device__ __forceinline__ void add_pack(Acc &a, cons
     }
 }
 
+// Adds a tile's sum to the thread's, with the rounding error of every addition
+// (D. E. Knuth's two-sum): a thread adds thousands of tiles of a long list.
+template <int KIND> __device__ __forceinline__ void add_tile(Acc &to, const Acc &tile)
+{
+    if (KIND == RRA_NORM_INF) {
+        to.mid = __uint_as_float(max(__float_as_uint(to.mid), __float_as_uint(tile.mid)));
+        return;
+    }
+    const float s = to.mid + tile.mid, t = s - to.mid;
+    to.low += (to.mid - (s - t)) + (tile.mid - t);
+    to.mid = s;
+    to.big += tile.big;
+    to.small += tile.small;
+}
+
 // The item that holds a tile of the launch.
-__device__ __forceinline__ int find_item(const Args &a, unsigned tile)
+template <typename A> __device__ __forceinline__ int find_item(const A &a, unsigned tile)
 {
     int lo = 0, hi = a.items;
     while (hi - lo > 1) {
@@ -121,35 +149,36 @@ __device__ __forceinline__ void tile_range(const Item &it, unsigned tile, long l
     *hi = min(*lo + kElems, it.n);
 }
 
-template <typename T, int KIND>
-__device__ __forceinline__ void norm_tile(const Item &it, unsigned tile, Acc &acc)
+template <typename T, int KIND, int THREADS>
+__device__ __forceinline__ void norm_tile(const Item &it, unsigned tile, Acc &sum)
 {
+    Acc acc;
     constexpr int V = 16 / sizeof(T);
     const T *const p = static_cast<const T *>(it.in);
     long long lo, hi;
     tile_range<T>(it, tile, &lo, &hi);
     if (hi - lo == kTileBytes / (int)sizeof(T)) {
-        Pack<T, V> v[kUnroll];
+        Pack<T, V> v[kUnroll<THREADS>];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_pack<T, V>(p + lo + (u * kThreads + threadIdx.x) * V);
+        for (int u = 0; u < kUnroll<THREADS>; ++u)
+            v[u] = load_pack<T, V>(p + lo + (u * THREADS + threadIdx.x) * V);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kUnroll<THREADS>; ++u) {
             float x[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 x[i] = to_f32(v[u].e[i]);
-            add_pack<KIND, V>(acc, x);
+            add_pack<KIND, V, std::is_same<T, __half>::value>(acc, x);
         }
     } else {
         const long long packs = hi > lo ? (hi - lo) / V : 0;
-        for (long long k = threadIdx.x; k < packs; k += kThreads) {
+        for (long long k = threadIdx.x; k < packs; k += THREADS) {
             const Pack<T, V> v = load_pack<T, V>(p + lo + k * V);
             float x[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 x[i] = to_f32(v.e[i]);
-            add_pack<KIND, V>(acc, x);
+            add_pack<KIND, V, std::is_same<T, __half>::value>(acc, x);
         }
         const long long i = lo + packs * V + threadIdx.x;
         if (i < hi) {
@@ -161,14 +190,56 @@ __device__ __forceinline__ void norm_tile(const Item &it, unsigned tile, Acc &ac
         const float x[1] = {to_f32(p[threadIdx.x])};
         add_pack<KIND, 1>(acc, x);
     }
+    add_tile<KIND>(sum, acc);
 }
 
-// What the list's norm is, from its three sums.
-template <int KIND> __device__ __forceinline__ float norm_of(double mid, double big, double small)
+template <int KIND, int THREADS>
+__device__ __forceinline__ void norm_any(const Item &it, unsigned tile, Acc &sum)
 {
-    if (KIND == RRA_NORM_L2)
-        return (float)sqrt(mid + big * 0x1p168 + small * 0x1p-180);
-    return (float)mid;
+    if (it.dtype == RRA_F32)
+        norm_tile<float, KIND, THREADS>(it, tile, sum);
+    else if (it.dtype == RRA_F16)
+        norm_tile<__half, KIND, THREADS>(it, tile, sum);
+    else
+        norm_tile<__nv_bfloat16, KIND, THREADS>(it, tile, sum);
+}
+
+// A sum of blocks' sums: two floats, exact to about 48 bits (fp64 instructions
+// run at a hundredth of fp32's rate here: joining 152 sums by a block in fp64
+// took 10 us).
+struct Two {
+    float hi = 0.0f, lo = 0.0f;
+};
+
+template <int KIND> __device__ __forceinline__ Two plus(Two a, float hi, float lo)
+{
+    if (KIND == RRA_NORM_INF)
+        return {__uint_as_float(max(__float_as_uint(a.hi), __float_as_uint(hi))), 0.0f};
+    const float s = a.hi + hi, t = s - a.hi;
+    return {s, a.lo + lo + ((a.hi - (s - t)) + (hi - t))};
+}
+
+__device__ __forceinline__ float value(Two a)
+{
+    return a.lo == a.lo ? a.hi + a.lo : a.hi; // (an infinite sum has no error)
+}
+
+template <int KIND> __device__ __forceinline__ Two warp_join(Two a)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a = plus<KIND>(a, __shfl_xor_sync(kFull, a.hi, o), __shfl_xor_sync(kFull, a.lo, o));
+    return a;
+}
+
+// What the list's norm is, from its sums.
+template <int KIND> __device__ __forceinline__ float norm_of(Two mid, float big, float small)
+{
+    if (KIND != RRA_NORM_L2)
+        return value(mid);
+    if (big == 0.0f && small == 0.0f)
+        return sqrtf(value(mid));
+    return (float)sqrt((double)value(mid) + (double)big * 0x1p168 + (double)small * 0x1p-180);
 }
 
 __device__ __forceinline__ float coef_of(float norm, float max_norm, float eps)
@@ -179,15 +250,15 @@ __device__ __forceinline__ float coef_of(float norm, float max_norm, float eps)
     return c < 1.0f ? c : (c == c ? 1.0f : c); // a NaN norm: a NaN factor
 }
 
-template <int KIND> __device__ __forceinline__ double join(double a, double b)
+template <int KIND> __device__ __forceinline__ float join(float a, float b)
 {
-    if (KIND == RRA_NORM_INF) // NaN wins
-        return a != a || a > b ? a : b;
+    if (KIND == RRA_NORM_INF)
+        return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
     return a + b;
 }
 
-// Joins v over the block; the result is valid in thread 0.
-template <int KIND> __device__ double block_join(double v, double *sm)
+// Joins v over the block; the result is valid in the first warp.
+template <int KIND, int THREADS> __device__ __forceinline__ float block_join(float v, float *sm)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -197,42 +268,44 @@ template <int KIND> __device__ double block_join(double v, double *sm)
         sm[threadIdx.x / 32] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
-        v = threadIdx.x < kThreads / 32 ? sm[threadIdx.x] : 0.0;
+        v = threadIdx.x < THREADS / 32 ? sm[threadIdx.x] : 0.0f;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1)
+        for (int o = THREADS / 64; o > 0; o >>= 1)
             v = join<KIND>(v, __shfl_xor_sync(kFull, v, o));
     }
     return v;
 }
 
-// First pass.  Every block leaves three partial sums; the block that finishes
+// A block's sums; big and small ones only where a thread has any.
+template <int KIND, int THREADS>
+__device__ __forceinline__ float4 block_sums(const Acc &acc, float *sm)
+{
+    // (an infinite sum has no rounding error)
+    const float mine = acc.low == acc.low ? acc.mid + acc.low : acc.mid;
+    float4 s = make_float4(block_join<KIND, THREADS>(mine, sm), 0.0f, 0.0f, 0.0f);
+    if (KIND == RRA_NORM_L2 && __syncthreads_or(acc.big != 0.0f || acc.small != 0.0f)) {
+        s.y = block_join<KIND, THREADS>(acc.big, sm);
+        s.z = block_join<KIND, THREADS>(acc.small, sm);
+    }
+    return s;
+}
+
+// First pass.  Every block leaves its sums in a slot; the block that finishes
 // last joins them in the order of their slots, so that the result does not
 // depend on the order in which blocks ran.
-template <int KIND>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Args a)
+template <int KIND, int ITEMS>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Args<ITEMS> a)
 {
-    __shared__ double sm[kThreads / 32];
+    __shared__ float sm[kThreads / 32];
+    __shared__ float4 joined[kThreads / 32];
     __shared__ bool last;
+    dependents_launch();
     Acc acc;
-    for (unsigned t = blockIdx.x; t < a.tiles; t += gridDim.x) {
-        const Item &it = a.item[find_item(a, t)];
-        if (it.dtype == RRA_F32)
-            norm_tile<float, KIND>(it, t, acc);
-        else if (it.dtype == RRA_F16)
-            norm_tile<__half, KIND>(it, t, acc);
-        else
-            norm_tile<__nv_bfloat16, KIND>(it, t, acc);
-    }
-    double mid = block_join<KIND>(acc.mid, sm), big = 0, small = 0;
-    if (KIND == RRA_NORM_L2) {
-        big = block_join<KIND>(acc.big, sm);
-        small = block_join<KIND>(acc.small, sm);
-    }
+    for (unsigned t = blockIdx.x; t < a.tiles; t += gridDim.x)
+        norm_any<KIND, kThreads>(a.item[find_item(a, t)], t, acc);
+    const float4 sums = block_sums<KIND, kThreads>(acc, sm);
     if (threadIdx.x == 0) {
-        float *p = a.partial + 3LL * (a.slot + blockIdx.x);
-        p[0] = (float)mid;
-        p[1] = (float)big;
-        p[2] = (float)small;
+        __stcg(a.partial + a.slot + blockIdx.x, sums);
         last = false;
         if (a.last) {
             __threadfence();
@@ -244,29 +317,36 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         return;
     __threadfence();
     const int slots = a.slot + gridDim.x;
-    mid = big = small = 0;
+    Two mid;
+    float big = 0.0f, small = 0.0f;
+#pragma unroll 4
     for (int s = threadIdx.x; s < slots; s += kThreads) {
-        mid = join<KIND>(mid, __ldcg(a.partial + 3LL * s));
-        if (KIND == RRA_NORM_L2) {
-            big += __ldcg(a.partial + 3LL * s + 1);
-            small += __ldcg(a.partial + 3LL * s + 2);
-        }
+        const float4 p = __ldcg(a.partial + s);
+        mid = plus<KIND>(mid, p.x, 0.0f);
+        big += p.y;
+        small += p.z;
     }
-    mid = block_join<KIND>(mid, sm);
-    if (KIND == RRA_NORM_L2) {
-        big = block_join<KIND>(big, sm);
-        small = block_join<KIND>(small, sm);
-    }
+    mid = warp_join<KIND>(mid);
+    big = warp_sum(big);
+    small = warp_sum(small);
+    if (threadIdx.x % 32 == 0)
+        joined[threadIdx.x / 32] = make_float4(mid.hi, mid.lo, big, small);
+    __syncthreads();
+    if (threadIdx.x >= 32)
+        return;
+    const float4 j = threadIdx.x < kThreads / 32 ? joined[threadIdx.x] : make_float4(0, 0, 0, 0);
+    const float n = norm_of<KIND>(warp_join<KIND>({j.x, j.y}), warp_sum(j.z), warp_sum(j.w));
     if (threadIdx.x == 0) {
-        const float n = norm_of<KIND>(mid, big, small);
         *a.norm = n;
         *a.coef = coef_of(n, a.max_norm, a.eps);
         *a.ticket = 0;
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, float c)
+// `factor()` gives the factor, once the norm is known: a whole tile is read
+// before.
+template <typename T, int THREADS, typename F>
+__device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, const F &factor)
 {
     constexpr int V = 16 / sizeof(T);
     const T *const p = static_cast<const T *>(it.in);
@@ -275,43 +355,90 @@ __device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, float 
     tile_range<T>(it, tile, &lo, &hi);
     // `out` may start elsewhere between two 16-byte boundaries than `in`
     const bool vec = reinterpret_cast<uintptr_t>(q + lo) % 16 == 0;
+    const auto scaled = [](Pack<T, V> v, float c) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v.e[i] = from_f32<T>(to_f32(v.e[i]) * c);
+        return v;
+    };
+    float c;
     if (vec && hi - lo == kTileBytes / (int)sizeof(T)) {
-        Pack<T, V> v[kUnroll];
+        Pack<T, V> v[kUnroll<THREADS>];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_pack<T, V>(p + lo + (u * kThreads + threadIdx.x) * V);
+        for (int u = 0; u < kUnroll<THREADS>; ++u)
+            v[u] = load_pack<T, V>(p + lo + (u * THREADS + threadIdx.x) * V);
+        c = factor();
+        if (c == 1.0f && it.in == it.out)
+            return;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[u].e[i] = from_f32<T>(to_f32(v[u].e[i]) * c);
-            store_pack<T, V>(q + lo + (u * kThreads + threadIdx.x) * V, v[u]);
-        }
+        for (int u = 0; u < kUnroll<THREADS>; ++u)
+            store_pack<T, V>(q + lo + (u * THREADS + threadIdx.x) * V, scaled(v[u], c));
     } else {
-        for (long long i = lo + threadIdx.x; i < hi; i += kThreads)
+        c = factor();
+        if (c == 1.0f && it.in == it.out)
+            return;
+        const long long packs = vec && hi > lo ? (hi - lo) / V : 0;
+        for (long long k = threadIdx.x; k < packs; k += THREADS)
+            store_pack<T, V>(q + lo + k * V, scaled(load_pack<T, V>(p + lo + k * V), c));
+        for (long long i = lo + packs * V + threadIdx.x; i < hi; i += THREADS)
             q[i] = from_f32<T>(to_f32(p[i]) * c);
     }
     if (tile == it.tile0 && threadIdx.x < (unsigned)it.head && threadIdx.x < it.n)
         q[threadIdx.x] = from_f32<T>(to_f32(p[threadIdx.x]) * c);
 }
 
+template <int THREADS, typename F>
+__device__ __forceinline__ void scale_any(const Item &it, unsigned tile, const F &factor)
+{
+    if (it.dtype == RRA_F32)
+        scale_tile<float, THREADS>(it, tile, factor);
+    else if (it.dtype == RRA_F16)
+        scale_tile<__half, THREADS>(it, tile, factor);
+    else
+        scale_tile<__nv_bfloat16, THREADS>(it, tile, factor);
+}
+
 // Second pass, from the last tile down: what the first pass read last may
 // still be in L2.  In place a factor of 1 leaves nothing to do.
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Args a)
+template <int ITEMS>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Args<ITEMS> a)
 {
-    const float c = __ldcg(a.coef);
+    bool known = false;
+    float c = 0.0f;
+    const auto factor = [&]() {
+        if (!known) {
+            dependents_wait();
+            c = __ldcg(a.coef);
+            known = true;
+        }
+        return c;
+    };
     for (unsigned t = blockIdx.x; t < a.tiles; t += gridDim.x) {
         const unsigned tile = a.tiles - 1 - t;
-        const Item &it = a.item[find_item(a, tile)];
-        if (c == 1.0f && it.in == it.out)
-            continue;
-        if (it.dtype == RRA_F32)
-            scale_tile<float>(it, tile, c);
-        else if (it.dtype == RRA_F16)
-            scale_tile<__half>(it, tile, c);
-        else
-            scale_tile<__nv_bfloat16>(it, tile, c);
+        scale_any<kThreads>(a.item[find_item(a, tile)], tile, factor);
     }
+}
+
+// A short list: one block, one launch, the second reading from L1 or L2.
+template <int KIND, int ITEMS>
+__global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ Args<ITEMS> a)
+{
+    __shared__ float sm[kThreads / 32];
+    __shared__ float c;
+    Acc acc;
+    for (unsigned t = 0; t < a.tiles; ++t)
+        norm_any<KIND, kThreads>(a.item[find_item(a, t)], t, acc);
+    const float4 s = block_sums<KIND, kThreads>(acc, sm);
+    if (threadIdx.x == 0) {
+        const float n = norm_of<KIND>({s.x, 0.0f}, s.y, s.z);
+        *a.norm = n;
+        c = coef_of(n, a.max_norm, a.eps);
+    }
+    __syncthreads();
+    const float factor = c;
+    if (a.tiles > 0 && a.item[0].out)
+        for (unsigned t = 0; t < a.tiles; ++t)
+            scale_any<kThreads>(a.item[find_item(a, t)], t, [&]() { return factor; });
 }
 
 struct List {
@@ -346,11 +473,11 @@ bool valid_list(const List &l)
 
 // Fills args with tensors from number k on, as many as one launch takes;
 // returns the number of the first that is left.
-int fill(Args &a, const List &l, int k)
+template <int ITEMS> int fill(Args<ITEMS> &a, const List &l, int k)
 {
     unsigned long long tiles = 0;
     a.items = 0;
-    for (; k < l.n && a.items < kMostItems; ++k) {
+    for (; k < l.n && a.items < ITEMS; ++k) {
         if (l.counts[k] == 0)
             continue;
         const size_t es = dtype_size(l.dtypes[k]);
@@ -369,47 +496,78 @@ int fill(Args &a, const List &l, int k)
     return k;
 }
 
-rra_status run(const List &l, int kind, bool clip, float max_norm, float eps, float *norm,
-               cudaStream_t st)
+template <int KIND, int ITEMS>
+rra_status run(const List &l, bool small, float max_norm, float eps, float *norm, cudaStream_t st)
 {
-    const int most = num_sms() * kGridPerSm;
-    const int launches = std::max(1, (l.n + kMostItems - 1) / kMostItems) + 1;
+    Args<ITEMS> a;
+    a.max_norm = max_norm;
+    a.eps = eps;
+    a.norm = norm;
+    a.slot = 0;
+    if constexpr (ITEMS == kFewItems) {
+        if (small) {
+            fill(a, l, 0);
+            small_kernel<KIND, ITEMS><<<1, kThreads, 0, st>>>(a);
+            return launched(cudaGetLastError());
+        }
+    }
+    const unsigned most = (unsigned)num_sms() * kGridPerSm;
+    const unsigned long long launches = l.n / ITEMS + 1;
     std::unique_lock<std::mutex> lk;
     unsigned char *ws = nullptr;
     const rra_status s =
-        op_scratch(st, kScratchHead + sizeof(float) * (4 + 3ull * most * launches), lk, &ws);
+        op_scratch(st, kScratchHead + 16 + sizeof(float4) * most * launches, lk, &ws);
     if (s != RRA_OK)
         return s;
-    Args a;
-    a.kind = kind;
-    a.max_norm = max_norm;
-    a.eps = eps;
     a.ticket = reinterpret_cast<unsigned *>(ws);
     a.coef = reinterpret_cast<float *>(ws + kScratchHead);
-    a.partial = a.coef + 4;
-    a.norm = norm;
-    a.slot = 0;
-    int k = 0;
-    do {
+    a.partial = reinterpret_cast<float4 *>(ws + kScratchHead + 16);
+    for (int k = 0;;) {
         k = fill(a, l, k);
         a.last = k >= l.n;
-        const int grid = (int)std::max(1u, std::min(a.tiles, (unsigned)most));
-        if (kind == RRA_NORM_L2)
-            norm_kernel<RRA_NORM_L2><<<grid, kThreads, 0, st>>>(a);
-        else if (kind == RRA_NORM_L1)
-            norm_kernel<RRA_NORM_L1><<<grid, kThreads, 0, st>>>(a);
-        else
-            norm_kernel<RRA_NORM_INF><<<grid, kThreads, 0, st>>>(a);
-        a.slot += grid;
-    } while (k < l.n);
-    if (clip) {
-        for (k = 0; k < l.n;) {
-            k = fill(a, l, k);
-            if (a.tiles)
-                scale_kernel<<<std::min(a.tiles, (unsigned)most), kThreads, 0, st>>>(a);
+        const unsigned grid = std::max(1u, std::min(a.tiles, most));
+        norm_kernel<KIND, ITEMS><<<grid, kThreads, 0, st>>>(a);
+        a.slot += (int)grid;
+        if (a.last)
+            break;
+    }
+    cudaError_t e = cudaGetLastError();
+    const bool again = l.n > ITEMS; // is what args hold not the whole list?
+    for (int k = 0; e == cudaSuccess && l.out && k < l.n;) {
+        const bool first = k == 0;
+        k = again ? fill(a, l, k) : l.n;
+        if (a.tiles == 0)
+            continue;
+        const dim3 grid(std::min(a.tiles, most));
+        if (first) {
+            e = launch_chained(scale_kernel<ITEMS>, grid, kThreads, st, a);
+        } else {
+            scale_kernel<ITEMS><<<grid, kThreads, 0, st>>>(a);
+            e = cudaGetLastError();
         }
     }
-    return launched(cudaGetLastError());
+    return launched(e);
+}
+
+template <int KIND>
+rra_status run_kind(const List &l, float max_norm, float eps, float *norm, cudaStream_t st)
+{
+    size_t bytes = 0;
+    for (int k = 0; k < l.n; ++k)
+        bytes += std::min(l.counts[k], (size_t)kSmallBytes) * dtype_size(l.dtypes[k]);
+    if (l.n <= kFewItems)
+        return run<KIND, kFewItems>(l, bytes <= kSmallBytes, max_norm, eps, norm, st);
+    return run<KIND, kMostItems>(l, false, max_norm, eps, norm, st);
+}
+
+rra_status run(const List &l, rra_norm kind, float max_norm, float eps, float *norm,
+               cudaStream_t st)
+{
+    if (kind == RRA_NORM_L2)
+        return run_kind<RRA_NORM_L2>(l, max_norm, eps, norm, st);
+    if (kind == RRA_NORM_L1)
+        return run_kind<RRA_NORM_L1>(l, max_norm, eps, norm, st);
+    return run_kind<RRA_NORM_INF>(l, max_norm, eps, norm, st);
 }
 
 bool valid_kind(rra_norm k) { return k == RRA_NORM_L2 || k == RRA_NORM_L1 || k == RRA_NORM_INF; }
@@ -424,7 +582,7 @@ extern "C" rra_status rra_grad_norm(const void *const *grads, const size_t *coun
     const rra::List l{grads, nullptr, counts, dtypes, ntensors};
     if (!norm || !rra::valid_kind(kind) || !rra::valid_list(l))
         return RRA_ERR_INVALID;
-    return rra::run(l, kind, false, 0.0f, 0.0f, norm, reinterpret_cast<cudaStream_t>(stream));
+    return rra::run(l, kind, 0.0f, 0.0f, norm, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" rra_status rra_grad_clip(const void *const *grads, void *const *out,
@@ -436,5 +594,5 @@ extern "C" rra_status rra_grad_clip(const void *const *grads, void *const *out,
     if (!norm || !rra::valid_kind(kind) || (ntensors > 0 && !out) || !rra::valid_list(l) ||
         !(max_norm >= 0.0f) || !(eps >= 0.0f) || isinf(eps))
         return RRA_ERR_INVALID;
-    return rra::run(l, kind, true, max_norm, eps, norm, reinterpret_cast<cudaStream_t>(stream));
+    return rra::run(l, kind, max_norm, eps, norm, reinterpret_cast<cudaStream_t>(stream));
 }

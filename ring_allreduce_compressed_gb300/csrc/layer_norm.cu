@@ -704,12 +704,9 @@ cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
                  weights = sizeof(float) * ((a.dim + 3) / 4 * 4);
     const int smem = (int)std::max(weights + sums + stages, 8 * (size_t)a.dim);
     const auto fn = norm_grad_kernel<T, W, V, MULTI, THREADS>;
-    if (smem > 49152) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess)
+        return e;
     fn<<<s.parts, s.groups * s.g.lanes(), smem, st>>>(a);
     return cudaGetLastError();
 }

@@ -267,6 +267,10 @@ constexpr size_t kScratchHead = 256;
 rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex> &lk,
                       unsigned char **out);
 
+// Allows a kernel `smem` bytes of dynamic shared memory, and clusters of more
+// than 8 blocks: once per kernel and device, not on every launch.
+cudaError_t op_allow(const void *fn, int smem, bool large_clusters = false);
+
 inline rra_status launched(cudaError_t e) { return e == cudaSuccess ? RRA_OK : RRA_ERR_CUDA; }
 
 } // namespace rra

@@ -12,6 +12,9 @@ namespace {
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, std::pair<unsigned char *, size_t>> g_ws;
 
+std::mutex g_fn_mu;
+std::map<std::pair<int, const void *>, int> g_fn_smem;
+
 } // namespace
 
 rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex> &lk,
@@ -49,6 +52,29 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
     }
     *out = ws->first;
     return RRA_OK;
+}
+
+cudaError_t op_allow(const void *fn, int smem, bool large_clusters)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lk(g_fn_mu);
+    int *have = nullptr;
+    try {
+        have = &g_fn_smem[{dev, fn}];
+    } catch (const std::bad_alloc &) {
+        return cudaErrorMemoryAllocation;
+    }
+    if (smem <= *have)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && large_clusters)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        *have = smem;
+    return e;
 }
 
 } // namespace rra

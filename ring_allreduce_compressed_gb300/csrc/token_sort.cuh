@@ -261,11 +261,8 @@ template <int R> cudaError_t cluster_sort(ClusterSortArgs a, int key_bits, int b
     const size_t digits = (size_t)1 << a.bits;
     const size_t smem = 16 * (size_t)kCsThreads * R + 4 * digits * (blocks + 2) +
                         2 * digits * kCsWarps;
-    cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel<R>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(cluster_sort_kernel<R>,
-                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e =
+        op_allow(reinterpret_cast<const void *>(cluster_sort_kernel<R>), (int)smem, true);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -629,6 +629,42 @@ def test_operators_on_streams_of_their_own():
         assert torch.equal(o, want)
 
 
+def test_operators_in_a_graph():
+    """Captured calls, replayed on new inputs, give the eager calls' bits."""
+    t, d = tokens(9000, 700, 1), randn((9000, 256), 2, dtype="bf16")
+    x, g = randn((500, 768), 3), randn(768, 4)
+    dw = torch.empty(700, 256, device="cuda")
+    y, m, r = torch.empty_like(x), torch.empty(500, device="cuda"), torch.empty(500, device="cuda")
+    dx, dg, db = torch.empty_like(x), torch.empty_like(g), torch.empty_like(g)
+    out, norm = torch.empty_like(dw), torch.empty(1, device="cuda")
+    results = (dw, y, m, r, dx, dg, db, out, norm)
+
+    def step():
+        rra.embedding_grad(d, t, dw)
+        rra.layer_norm(x, g, None, y, m, r)
+        rra.layer_norm_grad(y, x, g, m, r, dx, dg, db)
+        rra.grad_clip([dw, dg, db], [out, dg, db], 1.0, norm)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()  # the stream's scratch
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        step()
+    for seed in (5, 6):
+        t.copy_(tokens(9000, 700, seed))
+        x.copy_(randn((500, 768), seed))
+        step()
+        want = [v.clone() for v in results]
+        for v in results:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for v, w in zip(results, want):
+            assert torch.equal(v, w)
+
+
 def test_refusals_of_the_binding():
     x, t = randn((4, 8), 1), torch.zeros(4, dtype=torch.int64, device="cuda")
     norm = torch.empty(1, device="cuda")
