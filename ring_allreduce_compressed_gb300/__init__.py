@@ -485,11 +485,21 @@ def _op_dtype(ops, t) -> int:
     return code
 
 
-def _grad_list(ops, grads, name, device):
-    n = len(grads)
-    return ((C.c_void_p * n)(*[_op(g, name, device) for g in grads]),
-            (C.c_size_t * n)(*[g.numel() for g in grads]),
-            (C.c_int * n)(*[_op_dtype(ops, g) for g in grads]))
+def _grad_list(ops, grads, device):
+    """Addresses, element counts and type codes of a list of gradients, as
+    arrays; the checks are _op's."""
+    n, codes = len(grads), ops.dtypes
+    ptrs, counts, kinds = (C.c_void_p * n)(), (C.c_size_t * n)(), (C.c_int * n)()
+    for k, g in enumerate(grads):
+        if g.get_device() != device or not g.is_contiguous():
+            _op(g, "grads", device)
+        code = codes.get(g.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {g.dtype}")
+        ptrs[k] = g.data_ptr()
+        counts[k] = g.numel()
+        kinds[k] = code
+    return ptrs, counts, kinds
 
 
 def _norm_code(p) -> int:
@@ -507,7 +517,7 @@ def grad_norm(grads: Sequence, norm, norm_type=2, stream=None):
         raise ValueError("norm: expected a contiguous CUDA tensor")
     ops = _setup()
     dev = ops.device()
-    ptrs, counts, dtypes = _grad_list(ops, grads, "grads", dev)
+    ptrs, counts, dtypes = _grad_list(ops, grads, dev)
     _check(ops.lib.rra_grad_norm(ptrs, counts, dtypes, len(grads), kind,
                                  _op(norm, "norm", dev, ops.f32, (1,)),
                                  stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_grad_norm")
@@ -522,14 +532,19 @@ def grad_clip(grads: Sequence, outs: Sequence, max_norm: float, norm, norm_type=
         raise ValueError("norm: expected a contiguous CUDA tensor")
     ops = _setup()
     dev = ops.device()
-    ptrs, counts, dtypes = _grad_list(ops, grads, "grads", dev)
+    ptrs, counts, dtypes = _grad_list(ops, grads, dev)
     if outs is grads:
         optrs = ptrs
     else:
         if len(outs) != len(grads):
             raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
-        optrs = (C.c_void_p * len(outs))(*[_op(o, "outs", dev, g.dtype, g.shape)
-                                           for o, g in zip(outs, grads)])
+        optrs = (C.c_void_p * len(outs))()
+        for k, (o, g) in enumerate(zip(outs, grads)):
+            if o.get_device() != dev or not o.is_contiguous() or o.dtype is not g.dtype or \
+                    o.numel() != counts[k]:
+                _op(o, "outs", dev, g.dtype, g.shape)
+                raise ValueError(f"outs: expected {counts[k]} elements, got {o.numel()}")
+            optrs[k] = o.data_ptr()
     _check(ops.lib.rra_grad_clip(ptrs, optrs, counts, dtypes, len(grads), kind, max_norm, eps,
                                  _op(norm, "norm", dev, ops.f32, (1,)),
                                  stream.cuda_stream if stream is not None else ops.stream(dev)), "rra_grad_clip")
