@@ -28,6 +28,8 @@ __global__ void __launch_bounds__(kThreads)
     lookup_kernel(const T *__restrict__ w, const I *__restrict__ tok, long long n, long long vocab,
                   long long dim, float scale, T *__restrict__ out, int lg, long long runs)
 {
+    dependents_wait();
+    dependents_launch();
     const int lanes = 1 << lg;
     const int lane = threadIdx.x & (lanes - 1);
     const long long units = dim / V; // packs of a row
@@ -59,7 +61,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int j = 0; j < V; ++j)
                 x[k].e[j] = from_f32<T>(to_f32(x[k].e[j]) * scale);
             if (c < units)
-                store_pack<T, V>(dst + c * V, x[k]);
+                stream_pack<T, V>(dst + c * V, x[k]);
         }
     }
 }
@@ -295,7 +297,8 @@ __global__ void __launch_bounds__(kSumThreads, 7) sum_kernel(const SumArgs a)
     }
 }
 
-// The table from row `cleared` on, before the sums are written over it.
+// The table from row `cleared` on, before the sums are written over it.  (The
+// sort has waited for what was before the call when it lets this kernel in.)
 __global__ void __launch_bounds__(kThreads) clear_kernel(unsigned char *p, long long bytes)
 {
     dependents_launch();
@@ -389,11 +392,14 @@ template <typename O, int V> __device__ __forceinline__ void join_rows(const Sum
 template <typename O, int V>
 __global__ void __launch_bounds__(kThreads) finish_kernel(const SumArgs a)
 {
+    dependents_launch();
     if (blockIdx.x < a.join_blocks) {
         dependents_wait();
         join_rows<O, V>(a);
     } else {
         clear_rows<O>(a, blockIdx.x - a.join_blocks, gridDim.x - a.join_blocks);
+        if (blockIdx.x == 0) // no joins: the sums have ended when this kernel has
+            dependents_wait();
     }
 }
 
@@ -403,7 +409,7 @@ inline unsigned grid_of(long long items, int per_sm)
 }
 
 template <typename T, int V>
-void lookup(const void *w, const void *tok, long long n, long long vocab, long long dim, bool wide,
+cudaError_t lookup(const void *w, const void *tok, long long n, long long vocab, long long dim, bool wide,
             float scale, void *out, cudaStream_t st)
 {
     const long long units = dim / V;
@@ -412,31 +418,29 @@ void lookup(const void *w, const void *tok, long long n, long long vocab, long l
         ++lg;
     const long long runs = (units + (kRun << lg) - 1) / (kRun << lg);
     const long long per_block = kThreads >> lg;
-    const unsigned grid = grid_of((n * runs + per_block - 1) / per_block, 32);
+    const unsigned grid = grid_of((n * runs + per_block - 1) / per_block, 16);
     if (wide)
-        lookup_kernel<T, V, long long><<<grid, kThreads, 0, st>>>(
-            static_cast<const T *>(w), static_cast<const long long *>(tok), n, vocab, dim, scale,
-            static_cast<T *>(out), lg, runs);
-    else
-        lookup_kernel<T, V, int><<<grid, kThreads, 0, st>>>(
-            static_cast<const T *>(w), static_cast<const int *>(tok), n, vocab, dim, scale,
-            static_cast<T *>(out), lg, runs);
+        return launch_chained(lookup_kernel<T, V, long long>, dim3(grid), kThreads, st,
+                              static_cast<const T *>(w), static_cast<const long long *>(tok), n,
+                              vocab, dim, scale, static_cast<T *>(out), lg, runs);
+    return launch_chained(lookup_kernel<T, V, int>, dim3(grid), kThreads, st,
+                          static_cast<const T *>(w), static_cast<const int *>(tok), n, vocab, dim,
+                          scale, static_cast<T *>(out), lg, runs);
 }
 
 template <typename T>
-void lookup_any(const void *w, const void *tok, long long n, long long vocab, long long dim,
+cudaError_t lookup_any(const void *w, const void *tok, long long n, long long vocab, long long dim,
                 bool wide, float scale, void *out, cudaStream_t st)
 {
     const size_t row = (size_t)dim * sizeof(T);
     const auto fits = [&](size_t b) { return pack_fits(w, row, b) && pack_fits(out, row, b); };
     if (fits(16))
-        lookup<T, 16 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
-    else if (fits(8))
-        lookup<T, 8 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
-    else if (sizeof(T) == 2 && fits(4))
-        lookup<T, 4 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
-    else
-        lookup<T, 1>(w, tok, n, vocab, dim, wide, scale, out, st);
+        return lookup<T, 16 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
+    if (fits(8))
+        return lookup<T, 8 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
+    if (sizeof(T) == 2 && fits(4))
+        return lookup<T, 4 / sizeof(T)>(w, tok, n, vocab, dim, wide, scale, out, st);
+    return lookup<T, 1>(w, tok, n, vocab, dim, wide, scale, out, st);
 }
 
 // A table that is not worth a launch for its clearing: the joins' kernel does it.
@@ -548,12 +552,13 @@ extern "C" rra_status rra_embedding(const void *weight, const void *tokens, size
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool wide = index == RRA_I64;
     if (dtype == RRA_F32)
-        lookup_any<float>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st);
-    else if (dtype == RRA_F16)
-        lookup_any<__half>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st);
-    else
-        lookup_any<__nv_bfloat16>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st);
-    return launched(cudaGetLastError());
+        return launched(
+            lookup_any<float>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st));
+    if (dtype == RRA_F16)
+        return launched(
+            lookup_any<__half>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st));
+    return launched(
+        lookup_any<__nv_bfloat16>(weight, tokens, ntokens, vocab, dim, wide, scale, out, st));
 }
 
 extern "C" rra_status rra_embedding_grad(const void *dout, const void *tokens, size_t ntokens,

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     __shared__ float sm[kThreads / 32];
     __shared__ float4 joined[kThreads / 32];
     __shared__ bool last;
+    dependents_wait();
     dependents_launch();
     Acc acc;
     for (unsigned t = blockIdx.x; t < a.tiles; t += gridDim.x)
@@ -403,6 +404,8 @@ __device__ __forceinline__ void scale_any(const Item &it, unsigned tile, const F
 template <int ITEMS>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Args<ITEMS> a)
 {
+    dependents_launch(); // (every block waits for the norm, if after its first reads:
+                         // what the norm's kernel has waited for is done)
     bool known = false;
     float c = 0.0f;
     const auto factor = [&]() {
@@ -425,6 +428,8 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__
 {
     __shared__ float sm[kThreads / 32];
     __shared__ float c;
+    dependents_wait();
+    dependents_launch();
     Acc acc;
     for (unsigned t = 0; t < a.tiles; ++t)
         norm_any<KIND, kThreads>(a.item[find_item(a, t)], t, acc);
@@ -507,8 +512,7 @@ rra_status run(const List &l, bool small, float max_norm, float eps, float *norm
     if constexpr (ITEMS == kFewItems) {
         if (small) {
             fill(a, l, 0);
-            small_kernel<KIND, ITEMS><<<1, kThreads, 0, st>>>(a);
-            return launched(cudaGetLastError());
+            return launched(launch_chained(small_kernel<KIND, ITEMS>, dim3(1), kThreads, st, a));
         }
     }
     const unsigned most = (unsigned)num_sms() * kGridPerSm;
@@ -522,29 +526,24 @@ rra_status run(const List &l, bool small, float max_norm, float eps, float *norm
     a.ticket = reinterpret_cast<unsigned *>(ws);
     a.coef = reinterpret_cast<float *>(ws + kScratchHead);
     a.partial = reinterpret_cast<float4 *>(ws + kScratchHead + 16);
+    cudaError_t e = cudaSuccess;
     for (int k = 0;;) {
         k = fill(a, l, k);
         a.last = k >= l.n;
         const unsigned grid = std::max(1u, std::min(a.tiles, most));
-        norm_kernel<KIND, ITEMS><<<grid, kThreads, 0, st>>>(a);
+        e = launch_chained(norm_kernel<KIND, ITEMS>, dim3(grid), kThreads, st, a);
+        if (e != cudaSuccess)
+            return RRA_ERR_CUDA;
         a.slot += (int)grid;
         if (a.last)
             break;
     }
-    cudaError_t e = cudaGetLastError();
     const bool again = l.n > ITEMS; // is what args hold not the whole list?
     for (int k = 0; e == cudaSuccess && l.out && k < l.n;) {
-        const bool first = k == 0;
         k = again ? fill(a, l, k) : l.n;
         if (a.tiles == 0)
             continue;
-        const dim3 grid(std::min(a.tiles, most));
-        if (first) {
-            e = launch_chained(scale_kernel<ITEMS>, grid, kThreads, st, a);
-        } else {
-            scale_kernel<ITEMS><<<grid, kThreads, 0, st>>>(a);
-            e = cudaGetLastError();
-        }
+        e = launch_chained(scale_kernel<ITEMS>, dim3(std::min(a.tiles, most)), kThreads, st, a);
     }
     return launched(e);
 }

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(MULTI ? 1024 : kFwdThreads, MULTI ? 1 : 4) nor
         __syncthreads();
     }
     const int first = threadIdx.x / lanes;
+    dependents_wait();
+    dependents_launch();
     for (long long base = (long long)blockIdx.x * groups; base < a.rows;
          base += (long long)gridDim.x * groups) {
         // every lane takes part in the sums, some in vain: they read the last row
@@ -239,6 +241,8 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const Fwd a)
 {
     __shared__ __align__(16) float sm[2 * 32];
     GroupOf block = group_of(Group{5, kLongThreads / 32}, sm, 1);
+    dependents_wait();
+    dependents_launch();
     const float n = (float)a.dim;
     for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *const p = static_cast<const T *>(a.x) + r * a.dim;
@@ -286,11 +290,12 @@ inline Group group_for(long long units, int K)
 constexpr int kShort = 8; // elements that a lane holds: of short rows
 template <int V> constexpr int kHeld = V > 1 ? 32 : 16;
 
-template <typename T, typename W, int V> void forward_packs(Fwd a, cudaStream_t st)
+template <typename T, typename W, int V> cudaError_t forward_packs(Fwd a, cudaStream_t st)
 {
     const long long units = a.dim / V;
     if (a.dim > 1024LL * kHeld<V>) {
-        norm_long_kernel<T, W><<<grid_of(a.rows, 2), kLongThreads, 0, st>>>(a);
+        return launch_chained(norm_long_kernel<T, W>, dim3(grid_of(a.rows, 2)), kLongThreads, st,
+                              a);
     } else if (a.dim <= 32 * kHeld<V>) {
         // a warp or a part of one; few elements a lane for short rows
         const bool few = a.dim <= 32 * kShort;
@@ -298,14 +303,15 @@ template <typename T, typename W, int V> void forward_packs(Fwd a, cudaStream_t 
         const int per_block = kFwdThreads / a.g.lanes();
         const unsigned grid = grid_of((a.rows + per_block - 1) / per_block, 16);
         if (few)
-            norm_kernel<T, W, V, kShort / V, false><<<grid, kFwdThreads, 0, st>>>(a);
-        else
-            norm_kernel<T, W, V, kHeld<V> / V, false><<<grid, kFwdThreads, 0, st>>>(a);
+            return launch_chained(norm_kernel<T, W, V, kShort / V, false>, dim3(grid), kFwdThreads,
+                                  st, a);
+        return launch_chained(norm_kernel<T, W, V, kHeld<V> / V, false>, dim3(grid), kFwdThreads,
+                              st, a);
     } else {
         a.g = group_for(units, kHeld<V> / V);
         const int threads = 32 * a.g.warps;
-        norm_kernel<T, W, V, kHeld<V> / V, true>
-            <<<grid_of(a.rows, 2048 / threads), threads, 0, st>>>(a);
+        return launch_chained(norm_kernel<T, W, V, kHeld<V> / V, true>,
+                              dim3(grid_of(a.rows, 2048 / threads)), threads, st, a);
     }
 }
 
@@ -323,13 +329,12 @@ bool packs_fit(long long dim, std::initializer_list<const void *> rows,
     return true;
 }
 
-template <typename T, typename W> void forward(const Fwd &a, cudaStream_t st)
+template <typename T, typename W> rra_status forward(const Fwd &a, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
-    if (packs_fit<T, W, V>(a.dim, {a.x, a.y}, {a.gamma, a.beta}))
-        forward_packs<T, W, V>(a, st);
-    else
-        forward_packs<T, W, 1>(a, st);
+    return launched(packs_fit<T, W, V>(a.dim, {a.x, a.y}, {a.gamma, a.beta})
+                        ? forward_packs<T, W, V>(a, st)
+                        : forward_packs<T, W, 1>(a, st));
 }
 
 // ---------------------------------------------------------------- backward
@@ -398,6 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
     const float n = (float)a.dim, inverse = 1.0f / n;
     float *const weights = smem, *const sums = weights + ((int)a.dim + 3) / 4 * 4;
     GroupOf mine = group_of(a.g, sums + group * kBwdSums, 1 + group);
+    dependents_wait();
     for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
         weights[c] = gamma ? to_f32(gamma[c]) : 1.0f;
     if (MULTI)
@@ -623,6 +629,7 @@ template <typename W, int V> __global__ void __launch_bounds__(kThreads) join_ke
     constexpr int kLanes = 32 / V, kStretches = kThreads / kLanes;
     __shared__ float sm[kStretches][33];
     dependents_wait();
+    dependents_launch();
     const int t = threadIdx.x % kLanes, s = threadIdx.x / kLanes;
     const int lo = (int)((long long)a.parts * s / kStretches),
               hi = (int)((long long)a.parts * (s + 1) / kStretches);
@@ -707,8 +714,7 @@ cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
     const cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
-    fn<<<s.parts, s.groups * s.g.lanes(), smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained_smem(fn, dim3(s.parts), s.groups * s.g.lanes(), smem, st, a);
 }
 
 template <typename T, typename W, int V>
@@ -808,16 +814,14 @@ extern "C" rra_status rra_layer_norm(const void *x, const void *gamma, const voi
     const Fwd a{x, gamma, beta, (long long)rows, (long long)dim, eps, y, mean, rstd, {}};
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == RRA_F32)
-        forward<float, float>(a, st);
-    else if (dtype == RRA_F16 && weight_t == RRA_F16)
-        forward<__half, __half>(a, st);
-    else if (dtype == RRA_F16)
-        forward<__half, float>(a, st);
-    else if (weight_t == RRA_BF16)
-        forward<__nv_bfloat16, __nv_bfloat16>(a, st);
-    else
-        forward<__nv_bfloat16, float>(a, st);
-    return launched(cudaGetLastError());
+        return forward<float, float>(a, st);
+    if (dtype == RRA_F16 && weight_t == RRA_F16)
+        return forward<__half, __half>(a, st);
+    if (dtype == RRA_F16)
+        return forward<__half, float>(a, st);
+    if (weight_t == RRA_BF16)
+        return forward<__nv_bfloat16, __nv_bfloat16>(a, st);
+    return forward<__nv_bfloat16, float>(a, st);
 }
 
 extern "C" rra_status rra_layer_norm_grad(const void *dy, const void *x, const void *gamma,

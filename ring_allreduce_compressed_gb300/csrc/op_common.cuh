@@ -48,6 +48,16 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
     *reinterpret_cast<Pack<T, V> *>(p) = v;
 }
 
+// The same for results that the call does not read again: they leave L2 first.
+template <typename T, int V>
+__device__ __forceinline__ void stream_pack(T *p, const Pack<T, V> &v)
+{
+    if constexpr (sizeof(T) * V == 16)
+        __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&v));
+    else
+        store_pack<T, V>(p, v);
+}
+
 // A pack as the words that it was loaded in; elements are taken out where they
 // are used, so that a pack in flight costs its own size in registers.
 template <typename T, int V> struct Raw {
@@ -217,13 +227,20 @@ __device__ __forceinline__ void dependents_wait()
 
 // ---------------------------------------------------------------- host
 
-// Launch after which the next kernel of the stream may start early.
+// A kernel launched so may start before the one ahead of it in the stream has
+// ended, if that one lets it in (dependents_launch).  It waits for that one
+// (dependents_wait) before it touches memory, except where a comment says why
+// it need not: then the one ahead lets it in only when it has itself waited.
+// No kernel ends before the ones ahead of it, so what is behind a call finds
+// all of the call done.  A launch costs 1 to 2 us less so.
 template <typename... P, typename... A>
-cudaError_t launch_chained(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args)
+cudaError_t launch_chained_smem(void (*fn)(P...), dim3 grid, int threads, int smem,
+                                cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1] = {};
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -231,6 +248,12 @@ cudaError_t launch_chained(void (*fn)(P...), dim3 grid, int threads, cudaStream_
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*fn)(P...), dim3 grid, int threads, cudaStream_t st, A... args)
+{
+    return launch_chained_smem(fn, grid, threads, 0, st, args...);
 }
 
 inline bool valid_dt(rra_dtype t) { return t == RRA_F32 || t == RRA_F16 || t == RRA_BF16; }

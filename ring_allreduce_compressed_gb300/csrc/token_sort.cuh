@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     uint16_t *const mine = cnt + w * digits;
     const uint32_t n = a.t.n;
+    dependents_wait();
     dependents_launch();
     if (me == 0 && threadIdx.x < 2)
         a.joins[threadIdx.x] = 0;
@@ -270,12 +271,14 @@ template <int R> cudaError_t cluster_sort(ClusterSortArgs a, int key_bits, int b
     cfg.blockDim = dim3(kCsThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1] = {};
+    cudaLaunchAttribute at[2] = {};
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = blocks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, cluster_sort_kernel<R>, a);
 }
 

@@ -445,6 +445,20 @@ def test_layer_norm_rows(rows, dim):
     check_layer_norm(randn((rows, dim), 1, dtype="bf16"), randn(dim, 2), randn(dim, 3))
 
 
+@pytest.mark.parametrize("t,w", PAIRS)
+@pytest.mark.parametrize("rows,dim", [(10_001, 1032), (5003, 4096), (2500, 6152), (1300, 16_384)])
+def test_layer_norm_of_many_long_rows(rows, dim, t, w):
+    check_layer_norm(randn((rows, dim), 1, 1.5, t) + 0.25, randn(dim, 2, 0.1, w) + 1,
+                     randn(dim, 3, 0.1, w))
+    check_layer_norm_grad(randn((rows, dim), 4, dtype=t), randn((rows, dim), 1, 1.5, t) + 0.25,
+                          randn(dim, 2, 0.1, w) + 1)
+    x = randn((rows, dim), 1, 1.5, t)
+    y = torch.empty_like(x)
+    rra.layer_norm(x, None, None, y)
+    rra.layer_norm(x, None, None, x)
+    assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("gamma,beta", [(False, False), (True, False), (False, True)])
 def test_layer_norm_without_weights(gamma, beta):
     check_layer_norm(randn((3, 4, 260), 1), randn(260, 2) if gamma else None,
