@@ -20,7 +20,12 @@ constexpr int kWarps = kThreads / 32;
 // ---------------------------------------------------------------- lookup
 
 // A group of 2^lg lanes takes `kRun` packs a lane of one row: one run of
-// columns.  A token outside the table gives a row of zeros.
+// columns.  A token outside the table gives a row of zeros.  The rows are
+// streamed out, so that the table's stay in L2 for the tokens to come.
+//
+// Measured: 30.3 us for 32768 rows of 2048 bf16 out of 128000, 6.0 TB/s of the
+// rows read once and written (32.8 us with plain stores; 50 us with 8 packs a
+// lane, whose registers leave too few warps).
 constexpr int kRun = 4;
 
 template <typename T, int V, typename I>
@@ -75,6 +80,10 @@ __global__ void __launch_bounds__(kThreads)
 // the row that came in, slot 1: the row that goes on), which join_kernel adds
 // in the order of the tiles.  So a frequent token's terms are spread over as
 // many groups as there are tiles of it.
+//
+// Measured: 49 us for 16384 x 2048 bf16 into 50000 rows (272 MB, 5.55 TB/s),
+// 152 us for 131072 x 1024 bf16 into 128000 fp32 rows (793 MB, 5.2 TB/s): the
+// sort's 11 and 31 us, in which only the clears use memory, then near its rate.
 //
 // Rows of no token are cleared: the table's last rows, where tokens are
 // fewest, while the sort runs on 16 of the SMs (and written over by the sums
@@ -231,9 +240,10 @@ __device__ __forceinline__ void sum_tile(const SumArgs &a, uint32_t tile, uint32
 
 // Clears the rows that no token has.  A warp takes a few rows of about 4 KB,
 // then the next ones a grid further, so that the grid goes through the table
-// in order.  Its lanes read the marks of its next 32 turns at once: a read that
-// waits behind the writes of a whole GPU at every turn cost a third of the
-// rate.
+// in order.  Its lanes read the marks of its next 32 turns at once: at every
+// turn, behind the writes of a whole GPU, the read cost more than the writes
+// (whole gradient at 16384 x 2048 bf16, 4 blocks an SM: 72 against 65 us; with
+// 8 blocks 62).
 constexpr int kClearBytes = 4096;
 constexpr int kClearPerSm = 8; // blocks
 
@@ -493,7 +503,7 @@ template <typename T, typename O, int V> cudaError_t sum_rows(SumArgs a, cudaStr
         a.accumulate || a.cleared == 0
             ? 0
             : grid_of((a.cleared + at_once - 1) / at_once, kClearPerSm);
-    // joins wait more than they read: a block per SM lasts as long as the
+    // joins wait more than they read: two blocks an SM last as long as the
     // clears beside it, many are better where there are none
     a.join_blocks = a.tiles < 2 ? 0
                                 : grid_of((long long)a.tiles * ((a.dim + 127) / 128) / 4,

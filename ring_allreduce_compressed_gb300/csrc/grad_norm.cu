@@ -9,6 +9,13 @@
 // so that a block works on one tensor at a time and short tensors leave no SM
 // with more than its share.  The scaling's blocks start beside the norm's and
 // have their first tile in registers when the norm is known.
+//
+// Measured: 16.5 us for 25 MiB of fp16 (7.7 us to read and write it once; what
+// is left is two passes' ramps, 11 and 5 us, around the one point where every
+// sum has to be known), 1138 us for 10^9 elements in 40 tensors of bf16 and
+// fp32 (three passes over 2.5 GB, 6.6 TB/s).  Holding the 25 MiB in the SMs'
+// shared memory in one cooperative launch took 20.6 us; tiles of 8 and 16 KB,
+// 128 and 512 threads, and 5 to 8 blocks an SM were no faster.
 #include <math.h>
 
 #include "op_common.cuh"
@@ -37,7 +44,7 @@ struct Item {
 };
 
 // ITEMS: how many tensors there is room for.  Kernel arguments are copied and
-// read with every launch: 20 KB of them took longer than the norm of a bucket.
+// read with every launch: a short list has short ones.
 template <int ITEMS> struct Args {
     int items;
     unsigned tiles;
@@ -422,7 +429,8 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     }
 }
 
-// A short list: one block, one launch, the second reading from L1 or L2.
+// A short list: one block, one launch, the second reading from L1 or L2 (7 us
+// a call of 4096 fp32 from Python, 12 us with two launches; the GPU has 3 to do).
 template <int KIND, int ITEMS>
 __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ Args<ITEMS> a)
 {

@@ -8,6 +8,10 @@
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
 // Bound by memory: x read and y written; x and dy read and dx written.
+// Measured at 16384 x 4096 bf16: 47 us forward (268 MB, 5.7 TB/s), 72.5 us
+// backward (403 MB, 5.55 TB/s; 6 of the 72.5 for adding the partial rows of
+// dgamma and dbeta); 15.8 us backward at 3001 x 1001 fp32, whose rows only
+// 4-byte copies can read.
 #include <initializer_list>
 
 #include "op_common.cuh"
@@ -19,6 +23,8 @@ namespace {
 // all lanes of `warps` warps.  Lane i holds packs i, i + lanes, ... of V
 // elements (V: the widest that every row's address allows), so x is read once
 // and the variance is the mean of squares about the mean, not a difference.
+// 32 elements a lane: a row's own sums, barriers and addresses are some 150
+// instructions of every warp, and 16 a lane took 62 us where 32 take 49.
 struct Group {
     int lg;    // one warp or less: 2^lg lanes
     int warps; // more
