@@ -179,10 +179,6 @@ template <int V> struct Values {
         for (int n = 0; n < N; ++n)
             halves(e[n], v[2 * n], v[2 * n + 1]);
     }
-    static __device__ __forceinline__ E from_array(const float (&v)[V], int n)
-    {
-        return pair_of(v[2 * n], v[2 * n + 1]);
-    }
 };
 template <> struct Values<1> {
     using E = float;
@@ -193,18 +189,9 @@ template <> struct Values<1> {
         return raw.get(0);
     }
     static __device__ __forceinline__ void to_array(const E (&e)[1], float (&v)[1]) { v[0] = e[0]; }
-    static __device__ __forceinline__ E from_array(const float (&v)[1], int) { return v[0]; }
 };
 
 __device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
-__device__ __forceinline__ double warp_sum(double v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)

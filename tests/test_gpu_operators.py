@@ -228,6 +228,17 @@ def test_scratch_does_not_grow_during_a_capture():
     assert float(norm) == 1.0
 
 
+def test_grad_clip_beyond_32_bits():
+    """A tensor of more than 2^31 elements whose last ones alone are not zero."""
+    n = (1 << 31) + 5
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-3:] = torch.tensor([2.0, -1.0, 2.0])
+    norm = torch.empty(1, device="cuda")
+    rra.grad_clip([g], [g], 1.5, norm, eps=0.0)
+    assert float(norm) == 3.0
+    assert g[-4:].tolist() == [0.0, 1.0, -0.5, 1.0] and int((g != 0).sum()) == 3
+
+
 # ---------------------------------------------------------------- embedding
 
 DIMS = [1, 3, 8, 33, 64, 513, 1024, 2050, 4104]
@@ -281,6 +292,20 @@ def test_embedding_beyond_32_bits():
     dw = torch.full((vocab, dim), 2.0, dtype=torch.bfloat16, device="cuda")
     rra.embedding_grad(w[-3:], torch.tensor([vocab - 1, vocab - 1, vocab - 2], device="cuda"), dw)
     assert (dw[:-2] == 0).all() and (dw[-1] == 0).all() and torch.equal(dw[-2], w[-1])
+
+
+def test_embedding_grad_of_rows_beyond_32_bits():
+    """More than 2^31 elements of dout, in many tokens."""
+    n, dim = (1 << 21) + 3, 1024
+    d = torch.zeros(n, dim, dtype=torch.bfloat16, device="cuda")
+    d[-2:] = randn((2, dim), 2, dtype="bf16")
+    t = torch.arange(n, device="cuda", dtype=torch.int32) % 1000
+    t[-1] = t[0] = 1000
+    dw = torch.full((1001, dim), 2.0, device="cuda")
+    rra.embedding_grad(d, t, dw)
+    assert torch.equal(dw[1000], d[-1].float())
+    assert torch.equal(dw[(n - 2) % 1000], d[-2].float())
+    assert int((dw != 0).any(1).sum()) == 2
 
 
 def check_embedding_grad(dout, t, vocab, out, scale, padding=None, accumulate=False, offset=0):
@@ -677,6 +702,58 @@ def test_operators_in_a_graph():
         torch.cuda.synchronize()
         for v, w in zip(results, want):
             assert torch.equal(v, w)
+
+
+def test_operators_in_a_graph_of_two_streams():
+    """Captured behind copies, a fork and a join, calls wait for what they read."""
+    src, x = randn((64, 512), 3), torch.empty(64, 512, device="cuda")
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    t, dw = tokens(3000, 64, 1), torch.empty(64, 512, device="cuda")
+    d, norm = randn((3000, 512), 2), torch.empty(1, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for st in (main, side):  # the streams' scratch
+        rra.embedding_grad(d, t, dw, stream=st)
+        rra.grad_norm([dw], norm, stream=st)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        x.copy_(src)
+        dw.zero_()
+        side.wait_stream(main)
+        rra.embedding_grad(d, t, dw, stream=side)
+        rra.layer_norm(x, None, None, y)
+        x.fill_(0.0)  # y has been read from x
+        main.wait_stream(side)
+        rra.grad_norm([y, dw], norm)
+        rra.embedding(dw, t[:64], z)
+    for seed in (7, 8):
+        src.copy_(randn((64, 512), seed))
+        want_y, want_dw = torch.empty_like(y), torch.empty_like(dw)
+        rra.layer_norm(src, None, None, want_y)
+        rra.embedding_grad(d, t, want_dw)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(dw, want_dw)
+        assert torch.equal(z, dw[t[:64]])
+        n = exact_norm([y, dw], 2)
+        assert abs(float(norm) - n) <= CHAIN * U * n
+
+
+def test_operators_right_behind_other_kernels():
+    """A call that starts early still reads what is written just before it."""
+    x, w = torch.empty(2000, 1024, device="cuda"), torch.empty(2000, 1024, device="cuda")
+    y, out, norm = torch.empty_like(x), torch.empty_like(x), torch.empty(1, device="cuda")
+    t = torch.arange(2000, device="cuda").flip(0).contiguous()
+    for k in range(20):
+        w.fill_(float(k))
+        rra.embedding(w, t, x)
+        rra.embedding_grad(x, t, w)
+        rra.grad_clip([w], [w], 1e30, norm)
+        rra.embedding(w, t, out)
+        rra.layer_norm(out, None, None, y)
+        assert torch.equal(out, torch.full_like(out, float(k)))
+        assert (y == 0).all()
 
 
 def test_refusals_of_the_binding():
