@@ -8,10 +8,10 @@
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
 // Bound by memory: x read and y written; x and dy read and dx written.
-// Measured at 16384 x 4096 bf16: 47 us forward (268 MB, 5.7 TB/s), 72.5 us
-// backward (403 MB, 5.55 TB/s; 6 of the 72.5 for adding the partial rows of
-// dgamma and dbeta); 15.8 us backward at 3001 x 1001 fp32, whose rows only
-// 4-byte copies can read.
+// Measured at 16384 x 4096 bf16: 47 us forward (268 MB, 5.7 TB/s), 73.6 us
+// backward (403 MB, 5.5 TB/s; 5 of the 73.6 for adding the partial rows of
+// dgamma and dbeta); 15.3 us backward at 3001 x 1001 fp32 (36 MB): 20 rows an
+// SM, so a start, an end and 4 turns of a row's latency, and 5 us for the join.
 #include <initializer_list>
 
 #include "op_common.cuh"
@@ -351,6 +351,12 @@ template <typename T, typename W> rra_status forward(const Fwd &a, cudaStream_t 
 // join_kernel adds.  The packs of the next rows are on their way to shared
 // memory while a row is worked on, each lane's to slots of its own, so that
 // nothing but the row's two sums crosses lanes.
+//
+// Rows that do not begin on a 16-byte boundary are still read and written in
+// whole packs, but for those at their ends: a block takes rows that all begin
+// equally far behind one (every V-th row), so a lane's packs are the same
+// columns in all of them.  60000 x 1001 bf16 take 99 us so and took 499 element by
+// element; 3001 x 1001 fp32 15.3 and 15.8 (fp32 has 4-byte copies).
 struct Bwd {
     const void *dy, *x, *gamma;
     const float *mean, *rstd;
@@ -359,6 +365,7 @@ struct Bwd {
     int accumulate;
     float *part; // [parts][2][dim]
     int parts;
+    int period; // rows between two that begin equally far behind a boundary
     Group g;
 };
 
@@ -391,11 +398,13 @@ template <typename T, int V> __device__ __forceinline__ void stage_pack(T *to, c
         *to = *from;
 }
 
-template <typename T, typename W, int V, bool MULTI, int THREADS>
+// SHIFT: rows may begin and end inside a pack.
+template <typename T, typename W, int V, bool MULTI, int THREADS, bool SHIFT>
 __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
 {
     constexpr int K = kBwdHeld<T, V, THREADS> / V;
-    // gamma as fp32, the groups' sums, the stages; after the last row: [2][dim]
+    // gamma as fp32, the groups' sums, the stages; after the last row: the
+    // holders' [2][width]
     extern __shared__ __align__(16) float smem[];
     const T *const dy = static_cast<const T *>(a.dy), *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
@@ -404,76 +413,123 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
               groups = blockDim.x / lanes;
     using P = Values<V>;
     using E = typename P::E;
-    const int units = (int)a.dim / V; // (a held row is short)
-    const long long step = (long long)gridDim.x * groups;
-    const float n = (float)a.dim, inverse = 1.0f / n;
-    float *const weights = smem, *const sums = weights + ((int)a.dim + 3) / 4 * 4;
+    const int period = SHIFT ? a.period : 1;
+    const int dim = (int)a.dim, phase = blockIdx.x % period; // (a held row is short)
+    // elements between the last boundary and the row, in all rows of the block
+    const int shift =
+        SHIFT ? (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (unsigned)(phase * (dim % V))) %
+                      V)
+              : 0;
+    const int units = (dim + shift + V - 1) / V, width = units * V;
+    const long long step = (long long)(gridDim.x / period) * groups * period;
+    const float n = (float)dim, inverse = 1.0f / n;
+    float *const weights = smem, *const sums = weights + (width + 3) / 4 * 4;
     GroupOf mine = group_of(a.g, sums + group * kBwdSums, 1 + group);
     dependents_wait();
-    for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
-        weights[c] = gamma ? to_f32(gamma[c]) : 1.0f;
-    if (MULTI)
-        for (int i = threadIdx.x; i < groups * kBwdSums; i += blockDim.x)
-            sums[i] = 0.0f;
-    __syncthreads();
     T *const stages = reinterpret_cast<T *>(sums + (MULTI ? groups * kBwdSums : 0));
-    bool in[K];  // does the lane hold a k-th pack?
-    int col[K]; // its first column; that of the row's last pack if not
+    bool in[K];   // does the lane hold a k-th pack?
+    bool full[K]; // one that is all in the row?
+    int col[K];   // its first place (column + shift); that of the row's last pack if not
     E dg[K][P::N], db[K][P::N];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        in[k] = li + k * lanes < units;
-        col[k] = min(li + k * lanes, units - 1) * V;
+        const int u = li + k * lanes;
+        in[k] = u < units;
+        full[k] = SHIFT ? u * V >= shift && (u + 1) * V <= shift + dim : in[k];
+        col[k] = min(u, units - 1) * V;
 #pragma unroll
         for (int m = 0; m < P::N; ++m)
             dg[k][m] = db[k][m] = P::all(0.0f);
     }
 
     // The lane's k-th pack of x is k slots behind the stage's first, that of dy
-    // K slots further.  Packs that are not there stay zero and add nothing.
+    // K slots further.  What is not in the row stays zero and adds nothing.
     constexpr int kSlot = THREADS * V, kStage = 2 * K * kSlot;
     const int apart = lanes * V;
     T *const slots = stages + threadIdx.x * V;
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (!in[k])
+        if (!full[k])
 #pragma unroll
             for (int i = 0; i < kBwdStages; ++i)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     slots[i * kStage + k * kSlot + j] = slots[i * kStage + (K + k) * kSlot + j] =
                         from_f32<T>(0.0f);
-    const auto stage_row = [&](T *to, bool there, const T *px, const T *pd) {
+    // Of a pack at an end of the row: its elements in the row, asynchronously
+    // in pieces of 4 bytes.  A piece may bring an element of the row beside, if
+    // there is one, which forget() clears.
+    const auto valid = [&](int place) { return place >= shift && place < shift + dim; };
+    const auto stage_end = [&](T *to, const T *from, int place, bool before, bool behind) {
+        constexpr int Q = sizeof(T) == 4 ? 1 : 2; // elements of a piece
+#pragma unroll
+        for (int j = 0; j < V; j += Q) {
+            const bool p = valid(place + j), q = valid(place + j + Q - 1);
+            if ((p && q) || (p && behind) || (q && before)) {
+                stage_pack<T, Q>(to + j, from + j);
+            } else if (Q == 2 && p) {
+                to[j] = from[j];
+            } else if (Q == 2 && q) {
+                to[j + Q - 1] = from[j + Q - 1];
+            }
+        }
+    };
+    const auto forget = [&](T *stage) {
+        if (sizeof(T) == 4)
+            return;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (there && in[k]) {
+            if (in[k] && !full[k])
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (!valid(col[k] + j))
+                        stage[k * kSlot + j] = stage[(K + k) * kSlot + j] = from_f32<T>(0.0f);
+    };
+    const auto stage_row = [&](T *to, long long r, const T *px, const T *pd) {
+        const bool there = r < a.rows;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (there && full[k]) {
                 stage_pack<T, V>(to + k * kSlot, px + k * apart);
                 stage_pack<T, V>(to + (K + k) * kSlot, pd + k * apart);
+            } else if (SHIFT && there && in[k]) {
+                const bool before = r > 0, behind = r < a.rows - 1;
+                stage_end(to + k * kSlot, px + k * apart, col[k], before, behind);
+                stage_end(to + (K + k) * kSlot, pd + k * apart, col[k], before, behind);
             }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    long long r = (long long)blockIdx.x * groups + group;
+    long long r = ((long long)(blockIdx.x / period) * groups + group) * period + phase;
     const long long row_step = step * a.dim;
-    const T *px = x + r * a.dim + li * V, *pd = dy + r * a.dim + li * V; // staged next
-    T *q = dx + r * a.dim + li * V;
+    const T *px = x + r * a.dim - shift + li * V, *pd = dy + r * a.dim - shift + li * V; // staged next
+    T *q = dx + r * a.dim - shift + li * V;
 #pragma unroll
     for (int i = 0; i < kBwdStages - 1; ++i, px += row_step, pd += row_step)
-        stage_row(slots + i * kStage, r + i * step < a.rows, px, pd);
+        stage_row(slots + i * kStage, r + i * step, px, pd);
     float next_mu = 0.0f, next_rs = 0.0f;
     if (r < a.rows) {
         next_mu = a.mean[r];
         next_rs = a.rstd[r];
     }
+    for (int i = threadIdx.x; i < width; i += blockDim.x) {
+        const int c = i - shift;
+        weights[i] = c < 0 || c >= dim ? 0.0f : gamma ? to_f32(gamma[c]) : 1.0f;
+    }
+    if (MULTI)
+        for (int i = threadIdx.x; i < groups * kBwdSums; i += blockDim.x)
+            sums[i] = 0.0f;
+    __syncthreads();
     int stage = 0;
     // a group of several warps has barriers of its own: it ends with its last
     // row; the groups of a warp go on together
-    const long long end = MULTI ? a.rows : a.rows + group - (group & -(32 / lanes));
+    const long long end =
+        MULTI ? a.rows : a.rows + (group - (group & -(32 / lanes))) * period;
     for (; r < end; r += step, px += row_step, pd += row_step, q += row_step) {
         const bool on = MULTI || r < a.rows;
-        const T *const now = slots + stage * kStage;
+        T *const now = slots + stage * kStage;
         // into the stage that the last row was in
         stage_row(slots + (stage == 0 ? kBwdStages - 1 : stage - 1) * kStage,
-                  r + (kBwdStages - 1) * step < a.rows, px, pd);
+                  r + (kBwdStages - 1) * step, px, pd);
         stage = stage == kBwdStages - 1 ? 0 : stage + 1;
         const E minus = P::all(-next_mu), scale = P::all(next_rs);
         const float rs = next_rs;
@@ -482,6 +538,8 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
             next_rs = a.rstd[r + step];
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+        if (SHIFT)
+            forget(now);
         E s0 = P::all(0.0f), s1 = s0;
         if (on) {
 #pragma unroll
@@ -522,8 +580,16 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
                 const E w = mul(P::get(vd, m), g[m]);
                 g[m] = fma(xh, m1, fma(w, scale, m0));
             }
-            if (on && in[k])
+            if (on && full[k]) {
                 store_vals<T, V>(q + k * apart, g);
+            } else if (SHIFT && on && in[k]) {
+                float o[V];
+                P::to_array(g, o);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (valid(col[k] + j))
+                        q[k * apart + j] = from_f32<T>(o[j]);
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -550,34 +616,25 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
     }
     const int holders = MULTI ? groups : blockDim.x / 32, me = MULTI ? group : threadIdx.x / 32;
     const bool holds = MULTI || threadIdx.x % 32 < lanes;
-    float *const to = holders > 1 ? smem : out; // (the stages are done with)
+    __syncthreads(); // (gamma and the stages are done with)
+    float *const own = smem + me * 2 * width;
+    if (holds)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (in[k]) {
+                store_values<float, V>(own + (li + k * lanes) * V, fg[k]);
+                store_values<float, V>(own + width + (li + k * lanes) * V, fb[k]);
+            }
     __syncthreads();
-    for (int h = 0; h < holders; ++h) {
-        if (h == me && holds)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (in[k]) {
-                    float *const pg = to + (li + k * lanes) * V, *const pb = pg + a.dim;
-                    if (h > 0) {
-                        float u[V];
-                        load_values<float, V>(pg, u);
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            fg[k][j] += u[j];
-                        load_values<float, V>(pb, u);
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            fb[k][j] += u[j];
-                    }
-                    store_values<float, V>(pg, fg[k]);
-                    store_values<float, V>(pb, fb[k]);
-                }
-        if (holders > 1)
-            __syncthreads();
+    for (int c = threadIdx.x; c < dim; c += blockDim.x) {
+        float g = 0.0f, b = 0.0f;
+        for (int h = 0; h < holders; ++h) {
+            g += smem[h * 2 * width + shift + c];
+            b += smem[(h * 2 + 1) * width + shift + c];
+        }
+        out[c] = g;
+        out[dim + c] = b;
     }
-    if (holders > 1)
-        for (long long c = threadIdx.x; c < 2 * a.dim; c += blockDim.x)
-            out[c] = smem[c];
 }
 
 constexpr int kThreads = 256;
@@ -674,22 +731,32 @@ struct BwdShape {
     int groups; // of a block
     int parts;  // partial rows: blocks of the first kernel
     int threads; // kBwdThreads, kBwdWide, or 0: rows that no block holds
-    bool packs;
+    int period;
+    bool packs, shift;
 };
 
 template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
 {
     constexpr int V = 16 / sizeof(T);
     BwdShape s;
-    s.packs = packs_fit<T, float, V>(a.dim, {a.dy, a.x, a.dx}, {});
-    int held = s.packs ? kBwdHeld<T, V, kBwdThreads> : kBwdHeld<T, 1, kBwdThreads>;
+    // packs at the same places of x, dy and dx
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) % 16;
+    s.packs = reinterpret_cast<uintptr_t>(a.dy) % 16 == at &&
+              (!a.dx || reinterpret_cast<uintptr_t>(a.dx) % 16 == at);
+    s.period = s.packs && a.dim % V != 0 ? V : 1;
+    s.shift = s.packs && (at != 0 || s.period > 1);
+    // packs that a row touches at most
+    const long long units = !s.packs  ? a.dim
+                            : s.shift ? (a.dim + 2 * V - 2) / V
+                                      : a.dim / V;
+    int held = s.packs ? kBwdHeld<T, V, kBwdThreads> / V : kBwdHeld<T, 1, kBwdThreads>;
     s.threads = kBwdThreads;
-    if (a.dim > (long long)s.threads * held) {
-        held = s.packs ? kBwdHeld<T, V, kBwdWide> : kBwdHeld<T, 1, kBwdWide>;
-        s.threads = a.dim <= (long long)kBwdWide * held ? kBwdWide : 0;
+    if (units > (long long)s.threads * held) {
+        held = s.packs ? kBwdHeld<T, V, kBwdWide> / V : kBwdHeld<T, 1, kBwdWide>;
+        s.threads = units <= (long long)kBwdWide * held ? kBwdWide : 0;
     }
     if (s.threads) {
-        s.g = group_for(s.packs ? a.dim / V : a.dim, held / (s.packs ? V : 1));
+        s.g = group_for(units, held);
         // one block per SM; groups of a block only where rows are many
         const long long most = std::min(std::max(1, s.threads / s.g.lanes()),
                                         s.g.warps > 1 ? kMostBarriers : s.threads);
@@ -698,8 +765,9 @@ template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
             const int in_warp = 32 / s.g.lanes();
             s.groups = std::max(1, s.groups / in_warp) * in_warp;
         }
-        const long long blocks = (a.rows + s.groups - 1) / s.groups;
-        s.parts = (int)std::min(blocks, (long long)num_sms());
+        const long long rows = (a.rows + s.period - 1) / s.period; // of a phase
+        s.parts = s.period * (int)std::min((rows + s.groups - 1) / s.groups,
+                                           (long long)std::max(1, num_sms() / s.period));
     } else {
         const long long stretch = std::max(16LL, (a.rows + 127) / 128);
         s.groups = 1;
@@ -708,15 +776,17 @@ template <typename T, typename W> BwdShape backward_shape(const Bwd &a)
     return s;
 }
 
-template <typename T, typename W, int V, bool MULTI, int THREADS>
+template <typename T, typename W, int V, bool MULTI, int THREADS, bool SHIFT>
 cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 {
     // the slots of a whole block, whatever its size: their distance is a constant
     const size_t stages = (size_t)kBwdStages * 2 * kBwdHeld<T, V, THREADS> * sizeof(T) * THREADS,
                  sums = MULTI ? sizeof(float) * kBwdSums * s.groups : 0,
-                 weights = sizeof(float) * ((a.dim + 3) / 4 * 4);
-    const int smem = (int)std::max(weights + sums + stages, 8 * (size_t)a.dim);
-    const auto fn = norm_grad_kernel<T, W, V, MULTI, THREADS>;
+                 weights = sizeof(float) * ((a.dim + 2 * V + 3) / 4 * 4);
+    // at the end: the sums of every holder (a group, or a warp of groups)
+    const int holders = MULTI ? s.groups : s.groups * s.g.lanes() / 32;
+    const int smem = (int)std::max(weights + sums + stages, 2 * weights * holders);
+    const auto fn = norm_grad_kernel<T, W, V, MULTI, THREADS, SHIFT>;
     const cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
@@ -726,11 +796,15 @@ cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 template <typename T, typename W, int V>
 cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 {
+    constexpr bool shift = V > 1; // may rows be shifted?
     if (s.threads == kBwdWide)
-        return held_rows<T, W, V, true, kBwdWide>(a, s, st);
-    if (s.g.warps > 1)
-        return held_rows<T, W, V, true, kBwdThreads>(a, s, st);
-    return held_rows<T, W, V, false, kBwdThreads>(a, s, st);
+        return held_rows<T, W, V, true, kBwdWide, shift>(a, s, st);
+    if constexpr (shift)
+        if (s.shift)
+            return s.g.warps > 1 ? held_rows<T, W, V, true, kBwdThreads, true>(a, s, st)
+                                 : held_rows<T, W, V, false, kBwdThreads, true>(a, s, st);
+    return s.g.warps > 1 ? held_rows<T, W, V, true, kBwdThreads, false>(a, s, st)
+                         : held_rows<T, W, V, false, kBwdThreads, false>(a, s, st);
 }
 
 template <typename T, typename W> cudaError_t backward(Bwd a, const BwdShape &s, cudaStream_t st)
@@ -738,6 +812,7 @@ template <typename T, typename W> cudaError_t backward(Bwd a, const BwdShape &s,
     cudaError_t e = cudaSuccess;
     a.g = s.g;
     a.parts = s.parts;
+    a.period = s.period;
     if (a.rows > 0) {
         if (s.threads) {
             e = s.packs ? held_rows<T, W, 16 / sizeof(T)>(a, s, st) : held_rows<T, W, 1>(a, s, st);
@@ -862,7 +937,7 @@ extern "C" rra_status rra_layer_norm_grad(const void *dy, const void *x, const v
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const Bwd a{dy, x,  gamma,  mean,  rstd,       (long long)rows, (long long)dim,
                 dx, dgamma, dbeta, accumulate, nullptr,         0,
-                {}};
+                1,  {}};
     if (dtype == RRA_F32)
         return backward_call<float, float>(a, st);
     if (dtype == RRA_F16 && weight_t == RRA_F16)

@@ -532,6 +532,23 @@ def test_layer_norm_of_misaligned_buffers(offset, dim):
     check_layer_norm_grad(x, randn((9, dim), 4, dtype="bf16"), g)
 
 
+def test_layer_norm_grad_of_rows_at_every_phase():
+    """Rows of every length modulo 16 bytes, buffers that begin at every place
+    between two 16-byte boundaries, equal and different ones."""
+    for t in ("bf16", "f32"):
+        for dim in (9, 62, 63, 515, 1001):
+            for off in range(0, 8 if t == "bf16" else 4):
+                for rows in (1, 7, 400):
+                    x, dy = (randn((rows, dim), s, 1.0, t, off) for s in (1, 4))
+                    dx = torch.full((off + rows * dim + 1,), 9.0, dtype=DT[t],
+                                    device="cuda")
+                    check_layer_norm_grad(dy, x, randn(dim, 2),
+                                          dx=dx[off:off + rows * dim].view(rows, dim))
+                    assert (dx[:off] == 9).all() and dx[-1] == 9
+            check_layer_norm_grad(randn((50, dim), 4, 1.0, t, 1), randn((50, dim), 1, 1.0, t),
+                                  randn(dim, 2))
+
+
 def check_layer_norm_grad(dy, x, gamma, eps=1e-5, accumulate=False, wt=None, dx=None):
     dim = x.shape[-1]
     rows = x.numel() // dim
