@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads)
 // the rows of one tile over a slab of 8 columns a lane, all in registers, and
 // writes a row of the table when its last term has come.  A row whose terms
 // cross a tile's edge leaves a partial sum on either side (slot 0 of a tile:
-// the row that came in, slot 1: the row that goes on), which join_kernel adds
+// the row that came in, slot 1: the row that goes on), which finish_kernel adds
 // in the order of the tiles.  So a frequent token's terms are spread over as
 // many groups as there are tiles of it.
 //

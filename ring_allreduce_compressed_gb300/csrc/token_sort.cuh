@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
     uint32_t key[R], pos[R], rank[R];
     const uint32_t local = w * (32 * R) + lane, first = me * kLocal + local;
     const uint32_t held = min(n - min(n, me * kLocal), kLocal); // pairs of this block
+    const int used = (held + 32 * R - 1) / (32 * R);            // warps that hold them
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         pos[r] = first + r * 32;
@@ -166,22 +167,24 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
     }
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * a.bits;
-        for (uint32_t d = lane; d < digits / 2; d += 32)
-            reinterpret_cast<uint32_t *>(mine)[d] = 0;
-        __syncwarp();
-        // place of every pair among its warp's pairs of the same digit
+        if (w < used) {
+            for (uint32_t d = lane; d < digits / 2; d += 32)
+                reinterpret_cast<uint32_t *>(mine)[d] = 0;
+            __syncwarp();
+            // place of every pair among its warp's pairs of the same digit
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool on = first + r * 32 < n;
-            const uint32_t d = (key[r] >> shift) & (digits - 1);
-            const uint32_t same = same_digit(d, a.bits, on);
-            const uint32_t before = __popc(same & ((1u << lane) - 1));
-            const uint32_t at = on ? mine[d] : 0;
-            __syncwarp();
-            rank[r] = at + before;
-            if (on && before == 0)
-                mine[d] = (uint16_t)(at + __popc(same));
-            __syncwarp();
+            for (int r = 0; r < R; ++r) {
+                const bool on = first + r * 32 < n;
+                const uint32_t d = (key[r] >> shift) & (digits - 1);
+                const uint32_t same = same_digit(d, a.bits, on);
+                const uint32_t before = __popc(same & ((1u << lane) - 1));
+                const uint32_t at = on ? mine[d] : 0;
+                __syncwarp();
+                rank[r] = at + before;
+                if (on && before == 0)
+                    mine[d] = (uint16_t)(at + __popc(same));
+                __syncwarp();
+            }
         }
         __syncthreads();
         // thread d: digit d's pairs before each warp, and the block's total,
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
         uint32_t own = 0;
         if (threadIdx.x < digits) {
 #pragma unroll 8
-            for (int k = 0; k < kCsWarps; ++k) {
+            for (int k = 0; k < used; ++k) {
                 const uint32_t c = cnt[k * digits + threadIdx.x];
                 cnt[k * digits + threadIdx.x] = (uint16_t)own;
                 own += c;
