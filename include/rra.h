@@ -625,7 +625,8 @@ typedef enum { RRA_I32 = 0, RRA_I64 = 1 } rra_index;
  * finite and exact to fp32 whenever it is an fp32 number.  A NaN anywhere
  * gives NaN, else an infinity gives infinity.
  * Errors: RRA_ERR_INVALID (NULL, a bad enum, ntensors < 0, a count above
- * 2^40, a list of more than 64 TB), RRA_ERR_NOMEM, RRA_ERR_CUDA.
+ * 2^40, a list of more than 64 TB, norm inside a gradient), RRA_ERR_NOMEM,
+ * RRA_ERR_CUDA.
  */
 rra_status rra_grad_norm(const void *const *grads, const size_t *counts, const rra_dtype *dtypes,
                          int ntensors, rra_norm kind, float *norm, void *stream);

@@ -462,8 +462,10 @@ struct List {
     int n;
 };
 
-bool valid_list(const List &l)
+bool valid_list(const List &l, const float *norm)
 {
+    if (!norm || !aligned_to(norm, sizeof(float)))
+        return false;
     if (l.n < 0 || (l.n > 0 && (!l.in || !l.counts || !l.dtypes)))
         return false;
     unsigned long long tiles = 0; // of the whole list: their numbers are 32-bit
@@ -473,9 +475,11 @@ bool valid_list(const List &l)
         if (l.counts[k] == 0)
             continue;
         const size_t es = dtype_size(l.dtypes[k]);
-        if (!l.in[k] || !aligned_to(l.in[k], es))
+        if (!l.in[k] || !aligned_to(l.in[k], es) ||
+            overlap(l.in[k], l.counts[k] * es, norm, sizeof(float)))
             return false;
         if (l.out && (!l.out[k] || !aligned_to(l.out[k], es) ||
+                      overlap(l.out[k], l.counts[k] * es, norm, sizeof(float)) ||
                       (l.out[k] != l.in[k] &&
                        overlap(l.in[k], l.counts[k] * es, l.out[k], l.counts[k] * es))))
             return false;
@@ -587,7 +591,7 @@ extern "C" rra_status rra_grad_norm(const void *const *grads, const size_t *coun
                                     float *norm, void *stream)
 {
     const rra::List l{grads, nullptr, counts, dtypes, ntensors};
-    if (!norm || !rra::valid_kind(kind) || !rra::valid_list(l))
+    if (!rra::valid_kind(kind) || !rra::valid_list(l, norm))
         return RRA_ERR_INVALID;
     return rra::run(l, kind, 0.0f, 0.0f, norm, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -598,7 +602,7 @@ extern "C" rra_status rra_grad_clip(const void *const *grads, void *const *out,
                                     void *stream)
 {
     const rra::List l{grads, out, counts, dtypes, ntensors};
-    if (!norm || !rra::valid_kind(kind) || (ntensors > 0 && !out) || !rra::valid_list(l) ||
+    if (!rra::valid_kind(kind) || (ntensors > 0 && !out) || !rra::valid_list(l, norm) ||
         !(max_norm >= 0.0f) || !(eps >= 0.0f) || isinf(eps))
         return RRA_ERR_INVALID;
     return rra::run(l, kind, max_norm, eps, norm, reinterpret_cast<cudaStream_t>(stream));

@@ -30,6 +30,8 @@ def _list(ptrs, counts, dtypes):
     ([None], [8], [0], 0, E),           # a gradient without an address
     ([A + 2], [8], [0], 0, E),          # an fp32 gradient at an odd half-word
     ([A], [(1 << 40) + 1], [1], 0, E),  # too many elements
+    ([A], [8], [0], 0, A + 28),         # the norm inside a gradient
+    ([A], [8], [0], 0, E + 2),          # the norm at an odd half-word
 ])
 def test_grad_norm_refuses(lib, ptrs, counts, dtypes, kind, norm):
     p, c, d = _list(ptrs, counts, dtypes)
