@@ -114,11 +114,21 @@ __device__ __forceinline__ uint32_t cluster_blocks()
     return r;
 }
 
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_wait();
+}
+
+// The first half of a barrier that says only that this block has started.
+__device__ __forceinline__ void cluster_started()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 // Shared-memory address of the same place in another block of the cluster.
@@ -145,6 +155,7 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     uint16_t *const mine = cnt + w * digits;
     const uint32_t n = a.t.n;
+    cluster_started();
     dependents_wait();
     dependents_launch();
     if (me == 0 && threadIdx.x < 2)
@@ -187,6 +198,12 @@ __global__ void __launch_bounds__(kCsThreads) cluster_sort_kernel(const ClusterS
             }
         }
         __syncthreads();
+        // A block's shared memory may be written by others once it is known to
+        // have started: blocks of a cluster are scheduled together, but nothing
+        // says that they have all begun.  The wait's other half stands at the
+        // kernel's beginning, so that ranking the first digit hides it.
+        if (pass == 0)
+            cluster_wait();
         // thread d: digit d's pairs before each warp, and the block's total,
         // which goes to every block of the cluster
         uint32_t own = 0;
