@@ -601,8 +601,11 @@ rra_status rra_debug_withhold(rra_comm *comm, int rank, int step);
  *  - Infinities and NaN are carried through as the formulas have it.
  *  - rra_grad_norm, rra_grad_clip, rra_embedding_grad and
  *    rra_layer_norm_grad use scratch memory that the library keeps per device
- *    and stream, allocates with cudaMalloc when a call needs more than it
- *    holds, and frees never (it at least doubles when it grows).  A call
+ *    and stream (cudaStreamPerThread: per thread) and allocates with
+ *    cudaMalloc when a call needs more than it holds (it at least doubles when
+ *    it grows).  What it replaces, then or when a destroyed stream's handle
+ *    comes back, it frees with cudaFree, which waits for the device, unless a
+ *    captured graph may hold it: that is kept until the process ends.  A call
  *    that would have to allocate while its stream is being captured returns
  *    RRA_ERR_INVALID: make one call of that size before the capture.  Graphs
  *    captured on one stream share its scratch: do not replay two of them, or

@@ -22,7 +22,7 @@ LIB = os.path.join(LIBDIR, "librra.so")
 SOURCES = ["rra_host.cu", "ring_none.cu", "ring_bfp8.cu", "ring_bfp4.cu", "ring_bfp8_ef.cu", "ring_bfp4_ef.cu", "ring_sparse.cu", "ring_sparse_chunk.cu", "coll_kernels.cu",
            "codec_kernels.cu", "noalloc.cu", "op_scratch.cu", "grad_norm.cu", "embedding.cu", "layer_norm.cu"]
 HEADERS = ["rra_device.cuh", "rra_kernels.h", "bfp_group.cuh", "ring_kernel.cuh", "wire_sparse.cuh",
-           "op_common.cuh", "token_sort.cuh"]
+           "op_common.cuh", "token_sort.cuh", "stream_slot.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -264,13 +264,13 @@ __host__ __device__ inline bool pack_fits(const void *base, size_t row_bytes, si
     return aligned_to(base, bytes) && row_bytes % bytes == 0;
 }
 
-// Scratch memory of the operators, one buffer per (device, stream): calls on
-// one stream run in order and share it, calls on different streams never do.
-// Its first kScratchHead bytes are zero between calls (tickets that their
-// last user clears).  The lock in `lk` is held until the launches of the
-// call are queued.  A buffer that has become too small is kept, not freed: a
-// captured graph may still hold its address; sizes at least double, so what
-// is kept never exceeds what is in use.
+// Scratch memory of the operators, one buffer per stream (the per-thread
+// default stream: one per thread): calls on one stream run in order and share
+// it, calls on different streams never do.  Its first kScratchHead bytes are
+// zero between calls (tickets that their last user clears).  The lock in `lk`
+// is held until the launches of the call are queued.  A buffer that has become
+// too small, or whose stream is gone, is freed once the device's work is done,
+// but kept if a captured graph may hold its address; sizes at least double.
 // RRA_ERR_INVALID: the buffer would have to grow while the stream is being
 // captured; RRA_ERR_NOMEM, RRA_ERR_CUDA.
 constexpr size_t kScratchHead = 256;

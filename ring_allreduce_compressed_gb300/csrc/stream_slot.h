@@ -1,0 +1,33 @@
+// stream_slot.h -- what scratch memory that is kept per stream is kept by.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <tuple>
+
+namespace rra {
+
+// A stream's place among those of its device: its handle or, for the
+// per-thread default stream (one handle, a stream of its own in every host
+// thread), the number of the calling thread.  A handle or a number comes back
+// when its stream is destroyed or its thread ends; `id` does not.  A buffer
+// that was kept under another id belongs to a stream that is gone, whose last
+// work may still be running.
+struct StreamSlot {
+    int device = 0;
+    bool thread = false;
+    uintptr_t number = 0;
+    unsigned long long id = 0;
+
+    bool operator<(const StreamSlot &o) const // places, whatever the id
+    {
+        return std::tie(device, thread, number) < std::tie(o.device, o.thread, o.number);
+    }
+};
+
+// The slot of `st` on the current device; cudaErrorMemoryAllocation when there
+// is no memory for a thread's number.
+cudaError_t stream_slot(cudaStream_t st, StreamSlot *slot);
+
+} // namespace rra

@@ -1,0 +1,84 @@
+"""Scratch memory of the training-step operators: calls on different streams
+never share it, whatever the streams' handles."""
+import threading
+
+import pytest
+import torch
+
+import ring_allreduce_compressed_gb300 as rra
+
+pytestmark = pytest.mark.gpu
+
+PER_THREAD = 2  # cudaStreamPerThread
+
+
+class Handle:
+    """A stream as the binding takes it, by its handle."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def problem(seed, n, vocab, dim):
+    """Tokens and gradients of small whole numbers: sums in any order are exact."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    d = torch.randint(-8, 9, (n, dim), generator=g, device="cuda").float()
+    want = torch.zeros(vocab, dim, device="cuda").index_add_(0, t, d)
+    return t, d, want
+
+
+def test_per_thread_default_streams_keep_their_scratch_apart():
+    """One handle names another stream in every thread.  Two threads' gradients
+    of different sizes run at the same time, over and over."""
+    problems = [problem(1, 40_000, 3000, 64), problem(2, 9000, 500, 200)]
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(problems))
+
+    def work(k):
+        try:
+            t, d, want = problems[k]
+            dw = [torch.empty_like(want) for _ in range(60)]
+            norm = [torch.empty(1, device="cuda") for _ in dw]
+            torch.cuda.synchronize()
+            start.wait()
+            for o, n in zip(dw, norm):
+                rra.embedding_grad(d, t, o, stream=Handle(PER_THREAD))
+                rra.grad_norm([d], n, norm_type=1, stream=Handle(PER_THREAD))
+            torch.cuda.synchronize()
+            size = float(d.double().abs().sum())
+            for o, n in zip(dw, norm):
+                assert torch.equal(o, want)
+                assert float(n) == size  # whole numbers below 2^24
+        except BaseException as e:  # noqa: BLE001 (reported by the test's own thread)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(problems))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed, failed
+
+
+def test_threads_that_come_and_go_leave_their_scratch_to_others():
+    t, d, want = problem(3, 50_000, 100, 512)
+    before, failed = None, []
+
+    def work():
+        try:
+            dw = torch.empty_like(want)
+            torch.cuda.synchronize()
+            rra.embedding_grad(d, t, dw, stream=Handle(PER_THREAD))
+            torch.cuda.synchronize()
+            assert torch.equal(dw, want)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+    for k in range(30):
+        th = threading.Thread(target=work)
+        th.start()
+        th.join()
+        assert not failed, failed
+        if k == 4:
+            before = torch.cuda.mem_get_info()[0]
+    # a call's scratch has more than 6 MB of partial sums; 25 calls since
+    assert before - torch.cuda.mem_get_info()[0] < 64_000_000
