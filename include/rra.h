@@ -337,10 +337,10 @@ rra_status rra_bfp_decode(const int8_t *exps, const uint8_t *mants, size_t n, in
  * and an emit pass that writes each chunk's nonzeros at its offset (or copies
  * x when the message is dense; idx is then left as it was).
  * Uses scratch (one uint32 per 1024 elements, one per 4096 chunks) from a
- * workspace per device and stream that the library allocates with
- * cudaMalloc on the first call that needs more than it holds (so that first
- * call must not be made during stream capture).  Encodes on different streams may overlap: each stream
- * has its own workspace.  Errors: RRA_ERR_INVALID, RRA_ERR_NOMEM,
+ * workspace per device and stream (cudaStreamPerThread: per thread) that the
+ * library allocates with cudaMalloc on the first call that needs more than it
+ * holds (so that first call must not be made during stream capture).  Encodes
+ * on different streams may overlap: each stream has its own workspace.  Errors: RRA_ERR_INVALID, RRA_ERR_NOMEM,
  * RRA_ERR_CUDA.
  */
 rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float threshold,
@@ -381,8 +381,9 @@ rra_status rra_sparse_encode_noalloc(const void *x, size_t n, rra_dtype dtype, f
  * Sparse decode into fp32 acc[0..n) (hdr, vals, idx as written by
  * rra_sparse_encode: indices ascending; the format is read on the device).
  * A sparse message is restored (or added) in one pass over acc, 4096
- * elements at a time, using a scratch of n/4096 + 1 words per device
- * and stream that the library allocates on first use and grows as needed
+ * elements at a time, using a scratch of n/4096 + 1 words per device and
+ * stream (cudaStreamPerThread: per thread) that the library allocates on
+ * first use and grows as needed
  * (so the first call on a stream, or the first with a larger n, must not be
  * made during stream capture; decodes on different streams may overlap);
  * an index out of order or outside [0, n) is ignored.

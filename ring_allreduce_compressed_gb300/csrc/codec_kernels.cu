@@ -7,6 +7,7 @@
 #include "bfp_group.cuh"
 #include "rra_device.cuh"
 #include "rra_kernels.h"
+#include "stream_slot.h"
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -952,40 +953,39 @@ cudaError_t launch_sparse_encode(const void *x, long long n, int dtype, double o
     return cudaGetLastError();
 }
 
-// Scratch of the decoder, one per (device, stream): where each tile's values
-// start.  Grown on demand; decodes on different streams never share one, and
+// Scratch of the decoder, one per stream: where each tile's values start.  Grown on demand; decodes on different streams never share one, and
 // the lock is held until the launches are queued, so no growth by another
 // thread frees a buffer under a launch.
 std::mutex g_dec_mu;
-std::map<std::pair<int, cudaStream_t>, std::pair<uint32_t *, long long>> g_dec_ws;
+std::map<StreamSlot, StreamWords> g_dec_ws;
 
 cudaError_t launch_sparse_decode(const uint32_t *hdr, const void *vals, const int32_t *idx,
                                  long long n, int dtype, float *acc, int accumulate,
                                  cudaStream_t st)
 {
     const long long words = (n + kSpTile - 1) / kSpTile + 1;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    StreamSlot slot;
+    cudaError_t e = stream_slot(st, &slot);
     if (e != cudaSuccess)
         return e;
     std::lock_guard<std::mutex> lk(g_dec_mu);
-    auto &ws = g_dec_ws[{dev, st}];
-    if (ws.second < words) {
-        if (ws.first) {
+    StreamWords &ws = g_dec_ws[slot];
+    if (ws.count < words || ws.id != slot.id) {
+        if (ws.p) {
             cudaDeviceSynchronize(); // a decode in flight may still read it
-            cudaFree(ws.first);
-            ws.first = nullptr;
-            ws.second = 0;
+            cudaFree(ws.p);
+            ws = StreamWords{};
         }
         const long long want = std::max(words, 1LL << 12);
-        e = cudaMalloc(&ws.first, (size_t)want * sizeof(uint32_t));
+        e = cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t));
         if (e != cudaSuccess) {
-            ws.first = nullptr;
+            ws.p = nullptr;
             return e;
         }
-        ws.second = want;
+        ws.count = want;
+        ws.id = slot.id;
     }
-    uint32_t *const scratch = ws.first;
+    uint32_t *const scratch = ws.p;
     const int vec = aligned16(vals) && aligned16(acc) ? 1 : 0;
     // the dense stream's grid; its threads also cover the tiles + 1 starts
     const long long tiles = (n + kSpTile - 1) / kSpTile;

@@ -15,6 +15,7 @@
 #include "rra.h"
 #include "rra_device.cuh"
 #include "rra_kernels.h"
+#include "stream_slot.h"
 
 namespace rra {
 const void *ring_fn_none(int in_t, bool fast, int groups, int rmap);
@@ -621,12 +622,12 @@ rra_status copy_common(rra_comm *comm, int which, void *const *buf, size_t count
     return RRA_OK;
 }
 
-// Scratch of the standalone sparse encoder, one per (device, stream), grown
-// on demand.  Encodes on different streams never share one, and the lock is
-// held until the launches are queued, so no growth by another thread frees a
-// buffer under a launch.
+// Scratch of the standalone sparse encoder, one per stream, grown on demand.
+// Encodes on different streams never share one, and the lock is held until
+// the launches are queued, so no growth by another thread frees a buffer under
+// a launch.
 std::mutex g_ws_mu;
-std::map<std::pair<int, cudaStream_t>, std::pair<uint32_t *, long long>> g_ws;
+std::map<StreamSlot, StreamWords> g_ws;
 
 } // namespace
 
@@ -830,29 +831,30 @@ rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float thr
     if (!x || n == 0 || !hdr || !vals || !idx || !valid_dtype(dtype) ||
         !(threshold >= 0.0f && threshold < 1.0f) || n > 0x7fffffffull)
         return RRA_ERR_INVALID;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return RRA_ERR_CUDA;
     const long long words = sparse_encode_scratch_words((long long)n);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    StreamSlot slot;
+    const cudaError_t e = stream_slot(st, &slot);
+    if (e != cudaSuccess)
+        return e == cudaErrorMemoryAllocation ? RRA_ERR_NOMEM : RRA_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_ws_mu);
-    auto &ws = g_ws[{dev, st}];
-    if (ws.second < words) {
-        if (ws.first) {
+    StreamWords &ws = g_ws[slot];
+    if (ws.count < words || ws.id != slot.id) {
+        if (ws.p) {
             cudaDeviceSynchronize(); // an encode in flight may still use it
-            cudaFree(ws.first);
-            ws.first = nullptr;
-            ws.second = 0;
+            cudaFree(ws.p);
+            ws = StreamWords{};
         }
         long long want = std::max(words, 1LL << 16);
-        if (cudaMalloc(&ws.first, (size_t)want * sizeof(uint32_t)) != cudaSuccess) {
-            ws.first = nullptr;
+        if (cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t)) != cudaSuccess) {
+            ws.p = nullptr;
             return RRA_ERR_NOMEM;
         }
-        ws.second = want;
+        ws.count = want;
+        ws.id = slot.id;
     }
     return launch_sparse_encode(x, (long long)n, dtype, 1.0 - (double)threshold, hdr, vals, idx,
-                                ws.first, st) == cudaSuccess
+                                ws.p, st) == cudaSuccess
                ? RRA_OK
                : RRA_ERR_CUDA;
 }

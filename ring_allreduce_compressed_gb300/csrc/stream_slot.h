@@ -26,6 +26,13 @@ struct StreamSlot {
     }
 };
 
+// A buffer of words that is kept for a slot.
+struct StreamWords {
+    uint32_t *p = nullptr;
+    long long count = 0;
+    unsigned long long id = 0; // of the stream that it belongs to
+};
+
 // The slot of `st` on the current device; cudaErrorMemoryAllocation when there
 // is no memory for a thread's number.
 cudaError_t stream_slot(cudaStream_t st, StreamSlot *slot);

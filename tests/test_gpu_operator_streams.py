@@ -82,3 +82,36 @@ def test_threads_that_come_and_go_leave_their_scratch_to_others():
             before = torch.cuda.mem_get_info()[0]
     # a call's scratch has more than 6 MB of partial sums; 25 calls since
     assert before - torch.cuda.mem_get_info()[0] < 64_000_000
+
+
+def test_sparse_codec_on_per_thread_default_streams():
+    """Two threads encode and decode messages of different sizes at the same time."""
+    failed, start = [], threading.Barrier(2)
+
+    def work(k):
+        try:
+            n = (3_000_001, 700_003)[k]
+            g = torch.Generator(device="cuda").manual_seed(k)
+            x = torch.randn(n, generator=g, device="cuda")
+            x = torch.where(torch.rand(n, generator=g, device="cuda") < 0.8, torch.zeros_like(x), x)
+            back = [torch.empty_like(x) for _ in range(20)]
+            hdr = [torch.empty(2, dtype=torch.int32, device="cuda") for _ in back]
+            vals, idx = torch.empty_like(x), torch.empty(n, dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize()
+            start.wait()
+            for h, b in zip(hdr, back):
+                rra.sparse_encode(x, 0.5, h, vals, idx, stream=Handle(PER_THREAD))
+                rra.sparse_decode(h, vals, idx, n, b, stream=Handle(PER_THREAD))
+            torch.cuda.synchronize()
+            nnz = int((x != 0).sum())
+            for h, b in zip(hdr, back):
+                assert h.tolist() == [1, nnz]
+                assert torch.equal(b, x)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed, failed
