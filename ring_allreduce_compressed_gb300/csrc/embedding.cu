@@ -21,7 +21,10 @@ constexpr int kWarps = kThreads / 32;
 
 // A group of 2^lg lanes takes `kRun` packs a lane of one row: one run of
 // columns.  A token outside the table gives a row of zeros.  The rows are
-// streamed out, so that the table's stay in L2 for the tokens to come.
+// streamed out, so that the table's stay in L2 for the tokens to come.  No
+// pointer is marked as read alone: the read-only path holds for memory that
+// nobody writes while the kernel lives, and this one may begin while the kernel
+// ahead still writes the table.
 //
 // Measured: 30.3 us for 32768 rows of 2048 bf16 out of 128000, 6.0 TB/s of the
 // rows read once and written (32.8 us with plain stores; 50 us with 8 packs a
@@ -30,8 +33,8 @@ constexpr int kRun = 4;
 
 template <typename T, int V, typename I>
 __global__ void __launch_bounds__(kThreads)
-    lookup_kernel(const T *__restrict__ w, const I *__restrict__ tok, long long n, long long vocab,
-                  long long dim, float scale, T *__restrict__ out, int lg, long long runs)
+    lookup_kernel(const T *w, const I *tok, long long n, long long vocab, long long dim,
+                  float scale, T *out, int lg, long long runs)
 {
     dependents_wait();
     dependents_launch();

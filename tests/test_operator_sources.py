@@ -34,3 +34,24 @@ def test_blocks_of_a_cluster_have_started_before_their_memory_is_written():
         arrives = sort.index("cluster_started()")
         assert arrives < waits[0]
         assert sort[:arrives].count("{") == 1 and "return" not in sort[:waits[0]]
+
+
+def kernels(text):
+    """(name, definition) of every kernel."""
+    for part in re.split(r"\b__global__\b", text)[1:]:
+        name = re.search(r"(\w+)\(\s*(?:const )?[\w<>]+ ?[*\w]", re.sub(
+            r"__launch_bounds__\((?:[^()]|\([^()]*\))*\)", "", part)).group(1)
+        yield name, part[:part.index("{")] + body(part, name)
+
+
+def test_kernels_that_begin_early_do_not_read_through_the_read_only_path():
+    """That path is for memory that nobody writes while the kernel lives; a
+    chained kernel lives before the one ahead of it has done its writes."""
+    found = set()
+    for name in ("embedding.cu", "grad_norm.cu", "layer_norm.cu", "token_sort.cuh"):
+        for kernel, text in kernels(source(name)):
+            if "dependents_wait" in text or "dependents_launch" in text:
+                found.add(kernel)
+                assert "__restrict__" not in text and "__ldg" not in text, kernel
+    assert {"lookup_kernel", "sum_kernel", "scale_kernel", "norm_grad_kernel",
+            "cluster_sort_kernel"} <= found
