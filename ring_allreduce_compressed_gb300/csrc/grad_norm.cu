@@ -352,8 +352,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 }
 
 // `factor()` gives the factor, once the norm is known: a whole tile is read
-// before.
-template <typename T, int THREADS, typename F>
+// before.  EARLY: possibly before this kernel's own wait, which alone makes
+// another kernel's writes visible to ordinary loads.  The norm's kernel has
+// waited for whoever wrote the gradients, so they are in L2 by then; an SM's
+// L1, where the norm's kernel may never have run, could hold older ones, so the
+// loads pass it by.
+template <typename T, int THREADS, bool EARLY, typename F>
 __device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, const F &factor)
 {
     constexpr int V = 16 / sizeof(T);
@@ -373,8 +377,10 @@ __device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, const 
     if (vec && hi - lo == kTileBytes / (int)sizeof(T)) {
         Pack<T, V> v[kUnroll<THREADS>];
 #pragma unroll
-        for (int u = 0; u < kUnroll<THREADS>; ++u)
-            v[u] = load_pack<T, V>(p + lo + (u * THREADS + threadIdx.x) * V);
+        for (int u = 0; u < kUnroll<THREADS>; ++u) {
+            const T *const from = p + lo + (u * THREADS + threadIdx.x) * V;
+            v[u] = EARLY ? load_pack_l2<T, V>(from) : load_pack<T, V>(from);
+        }
         c = factor();
         if (c == 1.0f && it.in == it.out)
             return;
@@ -395,15 +401,15 @@ __device__ __forceinline__ void scale_tile(const Item &it, unsigned tile, const 
         q[threadIdx.x] = from_f32<T>(to_f32(p[threadIdx.x]) * c);
 }
 
-template <int THREADS, typename F>
+template <int THREADS, bool EARLY, typename F>
 __device__ __forceinline__ void scale_any(const Item &it, unsigned tile, const F &factor)
 {
     if (it.dtype == RRA_F32)
-        scale_tile<float, THREADS>(it, tile, factor);
+        scale_tile<float, THREADS, EARLY>(it, tile, factor);
     else if (it.dtype == RRA_F16)
-        scale_tile<__half, THREADS>(it, tile, factor);
+        scale_tile<__half, THREADS, EARLY>(it, tile, factor);
     else
-        scale_tile<__nv_bfloat16, THREADS>(it, tile, factor);
+        scale_tile<__nv_bfloat16, THREADS, EARLY>(it, tile, factor);
 }
 
 // Second pass, from the last tile down: what the first pass read last may
@@ -411,8 +417,7 @@ __device__ __forceinline__ void scale_any(const Item &it, unsigned tile, const F
 template <int ITEMS>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Args<ITEMS> a)
 {
-    dependents_launch(); // (every block waits for the norm, if after its first reads:
-                         // what the norm's kernel has waited for is done)
+    dependents_launch(); // (every block waits for the norm, if after its first reads)
     bool known = false;
     float c = 0.0f;
     const auto factor = [&]() {
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     };
     for (unsigned t = blockIdx.x; t < a.tiles; t += gridDim.x) {
         const unsigned tile = a.tiles - 1 - t;
-        scale_any<kThreads>(a.item[find_item(a, tile)], tile, factor);
+        scale_any<kThreads, true>(a.item[find_item(a, tile)], tile, factor);
     }
 }
 
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__
     const float factor = c;
     if (a.tiles > 0 && a.item[0].out)
         for (unsigned t = 0; t < a.tiles; ++t)
-            scale_any<kThreads>(a.item[find_item(a, t)], t, [&]() { return factor; });
+            scale_any<kThreads, false>(a.item[find_item(a, t)], t, [&]() { return factor; });
 }
 
 struct List {

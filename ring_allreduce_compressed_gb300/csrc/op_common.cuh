@@ -42,6 +42,15 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(con
     return *reinterpret_cast<const Pack<T, V> *>(p);
 }
 
+// The same for 16 bytes, from L2 past L1.
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack_l2(const T *p)
+{
+    static_assert(sizeof(T) * V == 16, "a whole load");
+    Pack<T, V> v;
+    *reinterpret_cast<uint4 *>(&v) = __ldcg(reinterpret_cast<const uint4 *>(p));
+    return v;
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
 {

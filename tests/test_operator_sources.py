@@ -55,3 +55,14 @@ def test_kernels_that_begin_early_do_not_read_through_the_read_only_path():
                 assert "__restrict__" not in text and "__ldg" not in text, kernel
     assert {"lookup_kernel", "sum_kernel", "scale_kernel", "norm_grad_kernel",
             "cluster_sort_kernel"} <= found
+
+
+def test_what_scaling_reads_before_its_wait_comes_from_l2():
+    text = source("grad_norm.cu")
+    assert re.search(r"scale_any<kThreads, true>\(.*?, factor\)", body(text, "scale_kernel"))
+    tile = body(text, "scale_tile")
+    before = tile[:tile.index("factor()")]
+    # a tile's reads that stand before the factor is asked for
+    loads = re.findall(r"[^;{}]*\bload_pack\w*<[^;]*;", before)
+    assert loads and all("EARLY ? load_pack_l2" in x for x in loads)
+    assert "__ldcg" in body(source("op_common.cuh"), "load_pack_l2")
