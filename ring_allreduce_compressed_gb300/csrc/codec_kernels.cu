@@ -970,7 +970,7 @@ cudaError_t launch_sparse_decode(const uint32_t *hdr, const void *vals, const in
         return e;
     std::lock_guard<std::mutex> lk(g_dec_mu);
     StreamWords &ws = g_dec_ws[slot];
-    if (ws.count < words || ws.id != slot.id) {
+    if (ws.count < words || !slot.owns(ws.id)) {
         if (ws.p) {
             cudaDeviceSynchronize(); // a decode in flight may still read it
             cudaFree(ws.p);

@@ -68,10 +68,14 @@ cudaError_t stream_slot(cudaStream_t st, StreamSlot *slot)
     cudaError_t e = cudaGetDevice(&slot->device);
     if (e != cudaSuccess)
         return e;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if ((e = cudaStreamIsCapturing(st, &cap)) != cudaSuccess)
+        return e;
+    slot->capturing = cap != cudaStreamCaptureStatusNone;
     slot->thread = st == cudaStreamPerThread;
     if (!slot->thread) {
         slot->number = reinterpret_cast<uintptr_t>(st);
-        return cudaStreamGetId(st, &slot->id);
+        return slot->capturing ? cudaSuccess : cudaStreamGetId(st, &slot->id);
     }
     try {
         static thread_local const ThreadNumber mine;
@@ -90,9 +94,6 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
     cudaError_t e = stream_slot(st, &slot);
     if (e != cudaSuccess)
         return e == cudaErrorMemoryAllocation ? RRA_ERR_NOMEM : RRA_ERR_CUDA;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &cap) != cudaSuccess)
-        return RRA_ERR_CUDA;
     lk = std::unique_lock<std::mutex>(g_mu);
     Buffer *ws = nullptr;
     try {
@@ -100,8 +101,8 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
     } catch (const std::bad_alloc &) {
         return RRA_ERR_NOMEM;
     }
-    if (ws->bytes < bytes || ws->id != slot.id) {
-        if (cap != cudaStreamCaptureStatusNone)
+    if (ws->bytes < bytes || !slot.owns(ws->id)) {
+        if (slot.capturing)
             return RRA_ERR_INVALID;
         const size_t want = ws->id == slot.id
                                 ? std::max({bytes, 2 * ws->bytes, (size_t)1 << 20})
@@ -124,7 +125,7 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
         }
         *ws = Buffer{p, want, slot.id, false};
     }
-    ws->captured |= cap != cudaStreamCaptureStatusNone;
+    ws->captured |= slot.capturing;
     *out = ws->p;
     return RRA_OK;
 }

@@ -839,7 +839,7 @@ rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float thr
         return e == cudaErrorMemoryAllocation ? RRA_ERR_NOMEM : RRA_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_ws_mu);
     StreamWords &ws = g_ws[slot];
-    if (ws.count < words || ws.id != slot.id) {
+    if (ws.count < words || !slot.owns(ws.id)) {
         if (ws.p) {
             cudaDeviceSynchronize(); // an encode in flight may still use it
             cudaFree(ws.p);

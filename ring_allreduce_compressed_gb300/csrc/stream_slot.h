@@ -13,12 +13,17 @@ namespace rra {
 // thread), the number of the calling thread.  A handle or a number comes back
 // when its stream is destroyed or its thread ends; `id` does not.  A buffer
 // that was kept under another id belongs to a stream that is gone, whose last
-// work may still be running.
+// work may still be running.  A stream that is being captured cannot be asked
+// for its id (the question ends the capture): it is taken for the one that the
+// place's buffer belongs to.
 struct StreamSlot {
     int device = 0;
     bool thread = false;
     uintptr_t number = 0;
+    bool capturing = false;
     unsigned long long id = 0;
+
+    bool owns(unsigned long long buffer_id) const { return capturing || id == buffer_id; }
 
     bool operator<(const StreamSlot &o) const // places, whatever the id
     {

@@ -115,3 +115,28 @@ def test_sparse_codec_on_per_thread_default_streams():
     for th in threads:
         th.join()
     assert not failed, failed
+
+
+def test_sparse_codec_in_a_graph():
+    """A stream that is captured keeps the scratch of its calls before."""
+    n = 500_003
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, generator=g, device="cuda")
+    x = torch.where(torch.rand(n, generator=g, device="cuda") < 0.7, torch.zeros_like(x), x)
+    hdr, back = torch.empty(2, dtype=torch.int32, device="cuda"), torch.zeros_like(x)
+    vals, idx = torch.empty_like(x), torch.empty(n, dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    rra.sparse_encode(x, 0.5, hdr, vals, idx, stream=st)
+    rra.sparse_decode(hdr, vals, idx, n, back, stream=st)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        rra.sparse_encode(x, 0.5, hdr, vals, idx)
+        rra.sparse_decode(hdr, vals, idx, n, back)
+    for _ in range(2):
+        x.copy_(x.flip(0))
+        back.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(back, x)
