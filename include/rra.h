@@ -340,8 +340,10 @@ rra_status rra_bfp_decode(const int8_t *exps, const uint8_t *mants, size_t n, in
  * workspace per device and stream (cudaStreamPerThread: per thread) that the
  * library allocates with cudaMalloc on the first call that needs more than it
  * holds (so that first call must not be made during stream capture).  Encodes
- * on different streams may overlap: each stream has its own workspace.  Errors: RRA_ERR_INVALID, RRA_ERR_NOMEM,
- * RRA_ERR_CUDA.
+ * on different streams may overlap: each stream has its own workspace.  A
+ * workspace that a captured graph may hold is kept when a larger one replaces
+ * it.  Errors: RRA_ERR_INVALID, RRA_ERR_NOMEM (also: it would have to allocate
+ * during a capture), RRA_ERR_CUDA.
  */
 rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float threshold,
                              uint32_t *hdr, void *vals, int32_t *idx, void *stream);
@@ -383,10 +385,11 @@ rra_status rra_sparse_encode_noalloc(const void *x, size_t n, rra_dtype dtype, f
  * A sparse message is restored (or added) in one pass over acc, 4096
  * elements at a time, using a scratch of n/4096 + 1 words per device and
  * stream (cudaStreamPerThread: per thread) that the library allocates on
- * first use and grows as needed
- * (so the first call on a stream, or the first with a larger n, must not be
- * made during stream capture; decodes on different streams may overlap);
- * an index out of order or outside [0, n) is ignored.
+ * first use and grows as needed (so the first call on a stream, or the first
+ * with a larger n, must not be made during stream capture: RRA_ERR_CUDA;
+ * decodes on different streams may overlap; a scratch that a captured graph
+ * may hold is kept when a larger one replaces it); an index out of order or
+ * outside [0, n) is ignored.
  *  accumulate == 0: acc = the restored message (+0.0 where a sparse message
  *                   lists nothing).
  *  accumulate != 0: acc[i] = acc[i] + v at every position the message

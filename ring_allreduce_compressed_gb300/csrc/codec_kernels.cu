@@ -971,11 +971,13 @@ cudaError_t launch_sparse_decode(const uint32_t *hdr, const void *vals, const in
     std::lock_guard<std::mutex> lk(g_dec_mu);
     StreamWords &ws = g_dec_ws[slot];
     if (ws.count < words || !slot.owns(ws.id)) {
-        if (ws.p) {
+        if (slot.capturing)
+            return cudaErrorStreamCaptureUnsupported; // no allocation during a capture
+        if (ws.p && !ws.captured) {
             cudaDeviceSynchronize(); // a decode in flight may still read it
             cudaFree(ws.p);
-            ws = StreamWords{};
         }
+        ws = StreamWords{}; // (a graph's buffer stays where it is)
         const long long want = std::max(words, 1LL << 12);
         e = cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t));
         if (e != cudaSuccess) {
@@ -985,6 +987,7 @@ cudaError_t launch_sparse_decode(const uint32_t *hdr, const void *vals, const in
         ws.count = want;
         ws.id = slot.id;
     }
+    ws.captured |= slot.capturing;
     uint32_t *const scratch = ws.p;
     const int vec = aligned16(vals) && aligned16(acc) ? 1 : 0;
     // the dense stream's grid; its threads also cover the tiles + 1 starts

@@ -840,11 +840,13 @@ rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float thr
     std::lock_guard<std::mutex> lk(g_ws_mu);
     StreamWords &ws = g_ws[slot];
     if (ws.count < words || !slot.owns(ws.id)) {
-        if (ws.p) {
+        if (slot.capturing)
+            return RRA_ERR_NOMEM; // no allocation during a capture
+        if (ws.p && !ws.captured) {
             cudaDeviceSynchronize(); // an encode in flight may still use it
             cudaFree(ws.p);
-            ws = StreamWords{};
         }
+        ws = StreamWords{}; // (a graph's buffer stays where it is)
         long long want = std::max(words, 1LL << 16);
         if (cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t)) != cudaSuccess) {
             ws.p = nullptr;
@@ -853,6 +855,7 @@ rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float thr
         ws.count = want;
         ws.id = slot.id;
     }
+    ws.captured |= slot.capturing;
     return launch_sparse_encode(x, (long long)n, dtype, 1.0 - (double)threshold, hdr, vals, idx,
                                 ws.p, st) == cudaSuccess
                ? RRA_OK

@@ -36,6 +36,7 @@ struct StreamWords {
     uint32_t *p = nullptr;
     long long count = 0;
     unsigned long long id = 0; // of the stream that it belongs to
+    bool captured = false;     // a graph may hold its address
 };
 
 // The slot of `st` on the current device; cudaErrorMemoryAllocation when there

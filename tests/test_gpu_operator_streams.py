@@ -1,5 +1,6 @@
 """Scratch memory of the training-step operators: calls on different streams
 never share it, whatever the streams' handles."""
+import ctypes
 import threading
 
 import pytest
@@ -140,3 +141,74 @@ def test_sparse_codec_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(back, x)
+
+
+def new_stream():
+    """A stream that no other test has used, and the function that destroys it."""
+    rt = torch.cuda.cudart()
+    handle = ctypes.c_void_p()
+    assert int(rt.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    return torch.cuda.ExternalStream(handle.value), lambda: rt.cudaStreamDestroy(handle.value)
+
+
+def sparse(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(n, generator=g, device="cuda")
+    return torch.where(torch.rand(n, generator=g, device="cuda") < 0.7, torch.zeros_like(x), x)
+
+
+def test_sparse_codec_keeps_a_graph_s_scratch_when_it_grows():
+    """A larger call behind the capture takes a buffer of its own."""
+    small, large = 300_007, 80_000_003
+    x, big = sparse(small, 6), sparse(large, 7)
+    hdr, back = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty_like(big)
+    vals, idx = torch.empty_like(big), torch.empty(large, dtype=torch.int32, device="cuda")
+    st, destroy = new_stream()
+
+    def call(v):
+        rra.sparse_encode(v, 0.5, hdr, vals, idx, stream=st)
+        rra.sparse_decode(hdr, vals, idx, v.numel(), back, stream=st)
+    torch.cuda.synchronize()
+    call(x)
+    st.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        call(x)
+    call(big)
+    st.synchronize()
+    assert torch.equal(back, big)
+    for seed in (8, 9):
+        x.copy_(sparse(small, seed))
+        call(big)
+        st.synchronize()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(back[:small], x) and torch.equal(back[small:], big[small:])
+    destroy()
+
+
+def test_sparse_codec_that_would_grow_in_a_capture_is_refused():
+    """The capture stays usable, and so does the stream's scratch."""
+    x = sparse(80_000_003, 7)
+    hdr, back = torch.empty(2, dtype=torch.int32, device="cuda"), torch.zeros_like(x)
+    vals, idx = torch.empty_like(x), torch.empty(x.numel(), dtype=torch.int32, device="cuda")
+    y = torch.zeros(4, device="cuda")
+    st, destroy = new_stream()
+    torch.cuda.synchronize()
+    rra.sparse_encode(x[:5000], 0.5, hdr, vals, idx, stream=st)
+    rra.sparse_decode(hdr, vals, idx, 5000, back, stream=st)
+    st.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        for call in (lambda: rra.sparse_encode(x, 0.5, hdr, vals, idx),
+                     lambda: rra.sparse_decode(hdr, vals, idx, x.numel(), back)):
+            with pytest.raises(rra.RRAError):
+                call()
+        rra.sparse_encode(x[:5000], 0.5, hdr, vals, idx)
+        y.add_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (y == 1).all() and torch.equal(back[:5000], x[:5000])
+    assert hdr.tolist() == [1, int((x[:5000] != 0).sum())]
+    destroy()
