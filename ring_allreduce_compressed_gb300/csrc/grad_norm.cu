@@ -253,6 +253,8 @@ __device__ __forceinline__ float coef_of(float norm, float max_norm, float eps)
 {
     if (norm == 0.0f)
         return 1.0f;
+    if (isinf(norm)) // (an infinite max_norm has no quotient with it)
+        return 0.0f;
     const float c = max_norm / (norm + eps);
     return c < 1.0f ? c : (c == c ? 1.0f : c); // a NaN norm: a NaN factor
 }
