@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads)
         const bool in = v >= 0 && v < vocab;
         const T *const src = w + (in ? v : 0) * dim;
         T *const dst = out + t * dim;
+        const float factor = in ? scale : 1.0f; // a row of zeros stays one for every scale
         Pack<T, V> x[kRun];
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads)
             const long long c = c0 + k * lanes;
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                x[k].e[j] = from_f32<T>(to_f32(x[k].e[j]) * scale);
+                x[k].e[j] = from_f32<T>(to_f32(x[k].e[j]) * factor);
             if (c < units)
                 stream_pack<T, V>(dst + c * V, x[k]);
         }

@@ -44,3 +44,23 @@ def test_grad_clip_without_a_limit_changes_nothing(n):
     out = torch.zeros_like(g)
     rra.grad_clip([g], [out], math.inf, norm)
     assert torch.equal(out, g)
+
+
+# ---------------------------------------------------------------- lookup
+
+@pytest.mark.parametrize("scale", [-2.0, math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dtype,dim", [("f32", 24), ("f32", 7), ("f16", 64), ("bf16", 1024),
+                                       ("bf16", 33)])
+def test_embedding_of_tokens_outside_the_table_is_zero_for_every_scale(dtype, dim, scale):
+    w = randn((10, dim), 1, dtype).abs() + 1
+    t = torch.tensor([0, -1, 9, 10, 1 << 40, 3], device="cuda")
+    out = torch.full((6, dim), 9.0, dtype=DT[dtype], device="cuda")
+    rra.embedding(w, t, out, scale=scale)
+    bits = out.view(torch.int32 if dtype == "f32" else torch.int16)
+    for k, v in enumerate(t.tolist()):
+        if 0 <= v < 10:
+            want = (w[v].float() * scale).to(DT[dtype])
+            assert torch.equal(out[k], want) or (torch.isnan(want).all()
+                                                 and torch.isnan(out[k]).all())
+        else:
+            assert (bits[k] == 0).all()  # +0
