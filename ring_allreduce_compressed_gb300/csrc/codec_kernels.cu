@@ -973,10 +973,9 @@ cudaError_t launch_sparse_decode(const uint32_t *hdr, const void *vals, const in
     if (ws.count < words || !slot.owns(ws.id)) {
         if (slot.capturing)
             return cudaErrorStreamCaptureUnsupported; // no allocation during a capture
-        if (ws.p && !ws.captured) {
-            cudaDeviceSynchronize(); // a decode in flight may still read it
-            cudaFree(ws.p);
-        }
+        const AllocationAllowed allowed;
+        if (ws.p && !ws.captured)
+            cudaFree(ws.p); // waits for the device: a decode in flight may still read it
         ws = StreamWords{}; // (a graph's buffer stays where it is)
         const long long want = std::max(words, 1LL << 12);
         e = cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t));

@@ -107,6 +107,7 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
         const size_t want = ws->id == slot.id
                                 ? std::max({bytes, 2 * ws->bytes, (size_t)1 << 20})
                                 : std::max(bytes, (size_t)1 << 20);
+        const AllocationAllowed allowed;
         unsigned char *const old = ws->captured ? nullptr : ws->p;
         *ws = Buffer{};
         // cudaFree waits for all of the device's work: the last calls that used

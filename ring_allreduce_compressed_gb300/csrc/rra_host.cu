@@ -842,10 +842,9 @@ rra_status rra_sparse_encode(const void *x, size_t n, rra_dtype dtype, float thr
     if (ws.count < words || !slot.owns(ws.id)) {
         if (slot.capturing)
             return RRA_ERR_NOMEM; // no allocation during a capture
-        if (ws.p && !ws.captured) {
-            cudaDeviceSynchronize(); // an encode in flight may still use it
-            cudaFree(ws.p);
-        }
+        const AllocationAllowed allowed;
+        if (ws.p && !ws.captured)
+            cudaFree(ws.p); // waits for the device: an encode in flight may still use it
         ws = StreamWords{}; // (a graph's buffer stays where it is)
         long long want = std::max(words, 1LL << 16);
         if (cudaMalloc(&ws.p, (size_t)want * sizeof(uint32_t)) != cudaSuccess) {

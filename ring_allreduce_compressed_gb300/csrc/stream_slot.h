@@ -31,6 +31,20 @@ struct StreamSlot {
     }
 };
 
+// While one lives, its thread may allocate and free although a stream is being
+// captured, by this thread or another: those calls are otherwise refused, and
+// end the capture.
+class AllocationAllowed {
+public:
+    AllocationAllowed() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~AllocationAllowed() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    AllocationAllowed(const AllocationAllowed &) = delete;
+    AllocationAllowed &operator=(const AllocationAllowed &) = delete;
+
+private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
 // A buffer of words that is kept for a slot.
 struct StreamWords {
     uint32_t *p = nullptr;

@@ -1,6 +1,7 @@
 """What the header says of the training-step operators at the ends of their
 contract: infinite limits, tokens outside the table, captures elsewhere, and
 calls that begin while the kernels ahead of them still write."""
+import ctypes
 import math
 
 import pytest
@@ -64,3 +65,88 @@ def test_embedding_of_tokens_outside_the_table_is_zero_for_every_scale(dtype, di
                                                  and torch.isnan(out[k]).all())
         else:
             assert (bits[k] == 0).all()  # +0
+
+
+# ---------------------------------------------------------------- captures
+
+def new_stream():
+    """A stream that no other test has used, and the function that destroys it."""
+    rt = torch.cuda.cudart()
+    handle = ctypes.c_void_p()
+    assert int(rt.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    st = torch.cuda.ExternalStream(handle.value)
+    return st, lambda: rt.cudaStreamDestroy(handle.value)
+
+
+def test_scratch_grows_while_another_stream_is_captured():
+    """The capture goes on as if nothing had been."""
+    d = torch.ones(20_000, 64, device="cuda")
+    t = torch.arange(20_000, device="cuda") % 10
+    dw, y = torch.empty(10, 64, device="cuda"), torch.zeros(4, device="cuda")
+    want = torch.full((10, 64), 2000.0, device="cuda")
+    rra.embedding_grad(d, t, dw)  # kernels are loaded
+    dw.zero_()
+    st, destroy = new_stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y.add_(1.0)
+        rra.embedding_grad(d, t, dw, stream=st)  # the new stream's first call
+        y.add_(1.0)
+    st.synchronize()
+    assert torch.equal(dw, want)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (y == 2).all()
+    destroy()
+
+
+def test_sparse_codec_s_scratch_grows_while_another_stream_is_captured():
+    x = randn(9_000_001, 3)
+    x = torch.where(x > 1, x, torch.zeros_like(x))
+    hdr, back = torch.empty(2, dtype=torch.int32, device="cuda"), torch.zeros_like(x)
+    vals, idx = torch.empty_like(x), torch.empty(x.numel(), dtype=torch.int32, device="cuda")
+    y = torch.zeros(4, device="cuda")
+    rra.sparse_encode(x, 0.5, hdr, vals, idx)  # kernels are loaded
+    rra.sparse_decode(hdr, vals, idx, x.numel(), back)
+    nnz = int((x != 0).sum())
+    st, destroy = new_stream()
+    torch.cuda.synchronize()
+    rra.sparse_encode(x[:5], 0.5, hdr, vals, idx, stream=st)
+    rra.sparse_decode(hdr, vals, idx, 5, back, stream=st)
+    back.zero_()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y.add_(1.0)
+        rra.sparse_encode(x, 0.5, hdr, vals, idx, stream=st)
+        rra.sparse_decode(hdr, vals, idx, x.numel(), back, stream=st)
+        y.add_(1.0)
+    st.synchronize()
+    assert hdr.tolist() == [1, nnz] and torch.equal(back, x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (y == 2).all()
+    destroy()
+
+
+def test_streams_that_come_and_go():
+    """A stream may be destroyed while its last call runs; the next one, often
+    of the same handle, has a scratch that the old call does not write."""
+    problems = []
+    for seed, (n, vocab, dim) in enumerate([(50_000, 100, 512), (3000, 2000, 64)]):
+        t = torch.randint(0, vocab, (n,), generator=gen(seed), device="cuda")
+        d = torch.randint(-8, 9, (n, dim), generator=gen(seed), device="cuda").float()
+        problems.append((t, d, torch.zeros(vocab, dim, device="cuda").index_add_(0, t, d)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for t, d, want in problems:
+            st, destroy = new_stream()
+            got.append(torch.empty_like(want))
+            torch.cuda.synchronize()
+            rra.embedding_grad(d, t, got[-1], stream=st)
+            destroy()
+        torch.cuda.synchronize()
+        for o, (_, _, want) in zip(got, problems):
+            assert torch.equal(o, want)
