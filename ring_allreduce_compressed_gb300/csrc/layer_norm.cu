@@ -888,6 +888,9 @@ extern "C" rra_status rra_layer_norm(const void *x, const void *gamma, const voi
         overlap(x, bytes, mean, rows * 4) || overlap(x, bytes, rstd, rows * 4) ||
         overlap(mean, rows * 4, rstd, rows * 4))
         return RRA_ERR_INVALID;
+    for (const float *out : {mean, rstd})
+        if (overlap(out, rows * 4, gamma, dim * ws) || overlap(out, rows * 4, beta, dim * ws))
+            return RRA_ERR_INVALID;
     if (weight_t != dtype && weight_t != RRA_F32)
         return RRA_ERR_UNSUPPORTED;
     if (rows == 0)
