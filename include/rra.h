@@ -660,8 +660,8 @@ rra_status rra_grad_clip(const void *const *grads, void *const *out, const size_
  * numbers of type index; out: ntokens rows of dim elements.  A token outside
  * [0, vocab) gives a row of zeros.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, vocab or dim 0, ntokens or vocab
- * above 2^31 - 1, dim above 2^32, out overlapping weight or tokens),
- * RRA_ERR_CUDA.
+ * above 2^31 - 1, dim above 2^32, an array of more than 64 TB, out overlapping
+ * weight or tokens), RRA_ERR_CUDA.
  */
 rra_status rra_embedding(const void *weight, const void *tokens, size_t ntokens, size_t vocab,
                          size_t dim, rra_dtype dtype, rra_index index, float scale, void *out,
@@ -696,8 +696,8 @@ rra_status rra_embedding_grad(const void *dout, const void *tokens, size_t ntoke
  *               RRA_ERR_UNSUPPORTED); NULL: 1 and 0.
  *  mean, rstd   device fp32[rows], for rra_layer_norm_grad; NULL: not stored.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, dim 0 or above 2^31, rows above
- * 2^40, a negative or NaN eps, outputs that overlap an input or each other
- * otherwise), RRA_ERR_CUDA.
+ * 2^40, an array of more than 64 TB, a negative or NaN eps, outputs that
+ * overlap an input or each other otherwise), RRA_ERR_CUDA.
  */
 rra_status rra_layer_norm(const void *x, const void *gamma, const void *beta, size_t rows,
                           size_t dim, rra_dtype dtype, rra_dtype weight_t, float eps, void *y,

@@ -559,6 +559,8 @@ extern "C" rra_status rra_embedding(const void *weight, const void *tokens, size
     if (ntokens == 0)
         return RRA_OK;
     const size_t es = dtype_size(dtype), is = index == RRA_I64 ? 8 : 4;
+    if (!holdable(vocab, dim, es) || !holdable(ntokens, dim, es))
+        return RRA_ERR_INVALID;
     if (!weight || !tokens || !out || !aligned_to(weight, es) || !aligned_to(out, es) ||
         !aligned_to(tokens, is) || overlap(weight, vocab * dim * es, out, ntokens * dim * es) ||
         overlap(tokens, ntokens * is, out, ntokens * dim * es))
@@ -587,6 +589,8 @@ extern "C" rra_status rra_embedding_grad(const void *dout, const void *tokens, s
         return RRA_ERR_INVALID;
     const size_t es = dtype_size(dout_t), os = dtype_size(dweight_t),
                  is = index == RRA_I64 ? 8 : 4;
+    if (!holdable(vocab, dim, os) || !holdable(ntokens, dim, es))
+        return RRA_ERR_INVALID;
     if (!aligned_to(dweight, os) ||
         (ntokens > 0 &&
          (!dout || !tokens || !aligned_to(dout, es) || !aligned_to(tokens, is) ||

@@ -858,7 +858,8 @@ constexpr size_t kMostRows = (size_t)1 << 40, kMostDim = (size_t)1 << 31;
 
 bool valid_sizes(size_t rows, size_t dim, rra_dtype t, rra_dtype w)
 {
-    return valid_dt(t) && valid_dt(w) && dim > 0 && dim <= kMostDim && rows <= kMostRows;
+    return valid_dt(t) && valid_dt(w) && dim > 0 && dim <= kMostDim && rows <= kMostRows &&
+           holdable(rows, dim, dtype_size(t));
 }
 
 // Either apart or the same buffer.

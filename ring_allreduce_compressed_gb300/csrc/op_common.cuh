@@ -254,6 +254,13 @@ cudaError_t launch_chained(void (*fn)(P...), dim3 grid, int threads, cudaStream_
 
 inline bool valid_dt(rra_dtype t) { return t == RRA_F32 || t == RRA_F16 || t == RRA_BF16; }
 
+// Is an array of a * b elements of es bytes one that a memory could hold?  (64 TB;
+// the product of sizes that are each in range may not fit 64 bits.)
+inline bool holdable(size_t a, size_t b, size_t es)
+{
+    return a == 0 || b <= ((size_t)1 << 46) / es / a;
+}
+
 // Do [a, a + na) and [b, b + nb) share a byte?
 inline bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {

@@ -29,3 +29,16 @@ def layer_norm(lib, **given):
 ])
 def test_layer_norm_refuses_statistics_over_the_weights(lib, bad):
     assert layer_norm(lib, **bad) == INV
+
+
+# Products of sizes that are each in range can pass 64 bits, and what is left of
+# them then says nothing about overlaps.
+def test_operators_refuse_arrays_beyond_any_memory(lib):
+    most = (1 << 31) - 1
+    assert lib.rra_embedding(A, B, 4, most, 1 << 32, 0, 1, 1.0, D, None) == INV
+    assert lib.rra_embedding(A, B, most, 8, 1 << 32, 0, 1, 1.0, D, None) == INV
+    assert lib.rra_embedding_grad(A, B, 4, most, 1 << 32, 0, 1, 1.0, -1, D, 0, 0, None) == INV
+    assert lib.rra_embedding_grad(A, B, most, 8, 1 << 32, 1, 1, 1.0, -1, D, 0, 0, None) == INV
+    assert layer_norm(lib, rows=1 << 40, dim=1 << 31, mean=None, rstd=None) == INV
+    assert lib.rra_layer_norm_grad(A, B, None, D, E, 1 << 40, 1 << 22, 0, 0, None, None, E + 4096,
+                                   0, None) == INV
