@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
         SHIFT ? (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (unsigned)(phase * (dim % V))) %
                       V)
               : 0;
-    const int units = (dim + shift + V - 1) / V, width = units * V;
+    const int units = SHIFT ? (dim + shift + V - 1) / V : dim / V, width = SHIFT ? units * V : dim;
     const long long step = (long long)(gridDim.x / period) * groups * period;
     const float n = (float)dim, inverse = 1.0f / n;
     float *const weights = smem, *const sums = weights + (width + 3) / 4 * 4;
@@ -501,10 +501,18 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
     };
     long long r = ((long long)(blockIdx.x / period) * groups + group) * period + phase;
     const long long row_step = step * a.dim;
-    const T *px = x + r * a.dim - shift + li * V, *pd = dy + r * a.dim - shift + li * V; // staged next
-    T *q = dx + r * a.dim - shift + li * V;
+    // The lane's first pack: three pointers, those of x and dy a stage ahead, or
+    // one offset where a block is so wide that its threads have 128 registers
+    // (16-bit rows of 16384 spill no register then: 90 us against 113 for 4096 of
+    // them; narrower blocks, which spill none, take 74 us so at 16384 x 4096 and
+    // 76 with an offset).
+    constexpr bool kOffset = THREADS == kBwdWide;
+    constexpr int kAhead = kBwdStages - 1;
+    long long at = r * a.dim - shift + li * V;
+    const T *px = x + at, *pd = dy + at;
+    T *q = dx + at;
 #pragma unroll
-    for (int i = 0; i < kBwdStages - 1; ++i, px += row_step, pd += row_step)
+    for (int i = 0; i < kAhead; ++i, px += row_step, pd += row_step)
         stage_row(slots + i * kStage, r + i * step, px, pd);
     float next_mu = 0.0f, next_rs = 0.0f;
     if (r < a.rows) {
@@ -524,12 +532,13 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
     // row; the groups of a warp go on together
     const long long end =
         MULTI ? a.rows : a.rows + (group - (group & -(32 / lanes))) * period;
-    for (; r < end; r += step, px += row_step, pd += row_step, q += row_step) {
+    for (; r < end; r += step, at += row_step, px += row_step, pd += row_step, q += row_step) {
         const bool on = MULTI || r < a.rows;
         T *const now = slots + stage * kStage;
         // into the stage that the last row was in
-        stage_row(slots + (stage == 0 ? kBwdStages - 1 : stage - 1) * kStage,
-                  r + (kBwdStages - 1) * step, px, pd);
+        stage_row(slots + (stage == 0 ? kAhead : stage - 1) * kStage, r + kAhead * step,
+                  kOffset ? x + at + kAhead * row_step : px,
+                  kOffset ? dy + at + kAhead * row_step : pd);
         stage = stage == kBwdStages - 1 ? 0 : stage + 1;
         const E minus = P::all(-next_mu), scale = P::all(next_rs);
         const float rs = next_rs;
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
             next_mu = a.mean[r + step];
             next_rs = a.rstd[r + step];
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
         if (SHIFT)
             forget(now);
         E s0 = P::all(0.0f), s1 = s0;
@@ -567,6 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
         // dx = rs w - rs mean(w) - xh rs mean(w xh)
         const E m0 = P::all(-rs * quotient(s.v[0], n, inverse)),
                 m1 = P::all(-rs * quotient(s.v[1], n, inverse));
+        T *const to = kOffset ? dx + at : q;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             Raw<T, V> vx, vd;
@@ -581,14 +591,14 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
                 g[m] = fma(xh, m1, fma(w, scale, m0));
             }
             if (on && full[k]) {
-                store_vals<T, V>(q + k * apart, g);
+                store_vals<T, V>(to + k * apart, g);
             } else if (SHIFT && on && in[k]) {
                 float o[V];
                 P::to_array(g, o);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     if (valid(col[k] + j))
-                        q[k * apart + j] = from_f32<T>(o[j]);
+                        to[k * apart + j] = from_f32<T>(o[j]);
             }
         }
     }
@@ -617,6 +627,16 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const Bwd a)
     const int holders = MULTI ? groups : blockDim.x / 32, me = MULTI ? group : threadIdx.x / 32;
     const bool holds = MULTI || threadIdx.x % 32 < lanes;
     __syncthreads(); // (gamma and the stages are done with)
+    if (!SHIFT && holders == 1) { // nothing to add: 71.7 us against 73.5 at 4096 x 8192 fp32
+        if (holds)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in[k]) {
+                    store_values<float, V>(out + (li + k * lanes) * V, fg[k]);
+                    store_values<float, V>(out + dim + (li + k * lanes) * V, fb[k]);
+                }
+        return;
+    }
     float *const own = smem + me * 2 * width;
     if (holds)
 #pragma unroll
@@ -796,13 +816,15 @@ cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 template <typename T, typename W, int V>
 cudaError_t held_rows(const Bwd &a, const BwdShape &s, cudaStream_t st)
 {
-    constexpr bool shift = V > 1; // may rows be shifted?
-    if (s.threads == kBwdWide)
-        return held_rows<T, W, V, true, kBwdWide, shift>(a, s, st);
-    if constexpr (shift)
-        if (s.shift)
+    if constexpr (V > 1) // rows that may be shifted
+        if (s.shift) {
+            if (s.threads == kBwdWide)
+                return held_rows<T, W, V, true, kBwdWide, true>(a, s, st);
             return s.g.warps > 1 ? held_rows<T, W, V, true, kBwdThreads, true>(a, s, st)
                                  : held_rows<T, W, V, false, kBwdThreads, true>(a, s, st);
+        }
+    if (s.threads == kBwdWide)
+        return held_rows<T, W, V, true, kBwdWide, false>(a, s, st);
     return s.g.warps > 1 ? held_rows<T, W, V, true, kBwdThreads, false>(a, s, st)
                          : held_rows<T, W, V, false, kBwdThreads, false>(a, s, st);
 }
