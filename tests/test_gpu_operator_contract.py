@@ -150,3 +150,52 @@ def test_streams_that_come_and_go():
         torch.cuda.synchronize()
         for o, (_, _, want) in zip(got, problems):
             assert torch.equal(o, want)
+
+
+# ---------------------------------------------------------------- early starts
+
+@pytest.mark.parametrize("rows,dim", [(40, 1024), (2000, 1024), (300, 8192)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_calls_behind_one_another_read_what_was_written_last(rows, dim, dtype):
+    """Every result differs from what its buffer held and from the last turn's,
+    so a value that is read too early shows.  Sums of whole numbers and factors
+    that are powers of two: all of it is exact."""
+    dt = DT[dtype]
+    t = torch.randint(0, rows, (3 * rows,), generator=gen(1), device="cuda")
+    count = torch.bincount(t, minlength=rows).double()[:, None]
+    most = float(count.max())
+    table = torch.zeros(rows, dim, dtype=dt, device="cuda")
+    dw = torch.empty(rows, dim, device="cuda")
+    x = torch.empty(3 * rows, dim, dtype=dt, device="cuda")
+    y, clipped = torch.empty_like(x), torch.empty_like(dw)
+    norm, norm2 = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    mean, rstd = torch.empty(3 * rows, device="cuda"), torch.empty(3 * rows, device="cuda")
+    # +1 and -1 in turn: rows of mean 0 whose square is the turn's
+    sign = torch.ones(dim, device="cuda")
+    sign[1::2] = -1
+    for k in range(1, 13):
+        a = float(k % 7 + 1)
+        m = most * a
+        dw.fill_(-5.0)
+        torch.mul(sign.to(dt), a, out=table[0])
+        table.copy_(table[0].expand_as(table).clone())
+        rra.embedding(table, t, x, scale=2.0)                       # 2 a sign
+        rra.embedding_grad(x, t, dw, scale=0.5)                     # count a sign
+        rra.grad_clip([dw], [clipped], m / 4, norm2, norm_type=math.inf, eps=0.0)
+        rra.grad_norm([dw], norm, norm_type=math.inf)               # a max(count)
+        rra.layer_norm(x, None, None, y, mean, rstd, eps=0.0)
+        rra.grad_clip([dw], [dw], m / 2, norm2, norm_type=math.inf, eps=0.0)
+        got = [v.clone() for v in (x, dw, clipped, norm, norm2, y, mean, rstd)]
+        x.fill_(7.0)
+        y.fill_(7.0)
+        clipped.fill_(7.0)
+        want_dw = count * a * sign.double()
+        assert torch.equal(got[0].double(), 2 * a * sign.double().expand_as(x)), k
+        assert torch.equal(got[1].double(), want_dw / 2), k
+        assert torch.equal(got[2].double(), want_dw / 4), k
+        assert float(got[3]) == m and float(got[4]) == m, k
+        assert (got[6] == 0).all(), k
+        # a square root and one product away from 1
+        assert float((got[5].double() - sign.double()).abs().max()) <= (
+            2.0 ** -20 if dtype == "f32" else 2.0 ** -8), k
+        assert float((got[7].double() * 2 * a - 1).abs().max()) <= 2.0 ** -20, k
