@@ -629,8 +629,12 @@ typedef enum { RRA_I32 = 0, RRA_I64 = 1 } rra_index;
  *           the tensors' element counts and types.  Read during the call.
  *  norm     device fp32[1].
  * The sum of squares neither overflows nor loses small values: the norm is
- * finite and exact to fp32 whenever it is an fp32 number.  A NaN anywhere
- * gives NaN, else an infinity gives infinity.
+ * finite whenever it is an fp32 number.  It is within 2^-17 of the exact one,
+ * relatively (no more than 64 terms in a row are added without their rounding
+ * errors); the maximum is exact.  Squares of packs of 16 bytes whose largest
+ * magnitude is above 2^44 or below 2^-50 are added without: 2^-25 more for
+ * every 40 MB of the list.  A NaN anywhere gives NaN, else an infinity gives
+ * infinity.
  * Errors: RRA_ERR_INVALID (NULL, a bad enum, ntensors < 0, a count above
  * 2^40, a list of more than 64 TB, norm inside a gradient), RRA_ERR_NOMEM,
  * RRA_ERR_CUDA.
@@ -646,7 +650,7 @@ rra_status rra_grad_norm(const void *const *grads, const size_t *counts, const r
  *        output.  Tensors have their gradient's type.
  *  norm  device fp32[1], receives n (before clipping).
  * n is never read on the host.  NaN: n, c and every output are NaN.
- * An infinite n: c is 0.  Errors: as rra_grad_norm; RRA_ERR_INVALID for a
+ * An infinite n: c is 0, whatever max_norm is (it may be infinite: no limit).  Errors: as rra_grad_norm; RRA_ERR_INVALID for a
  * max_norm or eps that is negative or NaN, an infinite eps, and an output
  * that overlaps its own gradient in part.
  */

@@ -560,7 +560,7 @@ def _index_code(ops, t) -> int:
 
 def embedding(weight, tokens, out, scale: float = 1.0, stream=None):
     """rra_embedding: out[..., :] = scale * weight[tokens[...], :] for a
-    (vocab, dim) weight; tokens outside the table give zeros."""
+    (vocab, dim) weight; tokens outside the table, negative ones too, give zeros."""
     if weight.dim() != 2:
         raise ValueError("weight: expected (vocab, dim)")
     if not weight.is_cuda:
@@ -578,7 +578,9 @@ def embedding(weight, tokens, out, scale: float = 1.0, stream=None):
 def embedding_grad(dout, tokens, dweight, scale: float = 1.0, padding_idx: Optional[int] = None,
                    accumulate: bool = False, stream=None):
     """rra_embedding_grad: dweight[v, :] = scale * the sum of dout's rows whose
-    token is v (zero where there is none), or added to dweight."""
+    token is v (zero where there is none), or added to dweight.  padding_idx is
+    a token that gets no gradient; None or a negative number (which does not
+    count from the table's end): there is none."""
     if dweight.dim() != 2:
         raise ValueError("dweight: expected (vocab, dim)")
     if not dweight.is_cuda:

@@ -461,8 +461,9 @@ cudaError_t lookup_any(const void *w, const void *tok, long long n, long long vo
 constexpr size_t kSmallTable = 8 << 20;
 
 // Table rows that are cleared during the sort: about what the other SMs write
-// in the time that it takes (none, 48 MB + 1 KB a token: 63, 56 us at 16384
-// tokens, 169, 152 us at 131072).
+// in the time that it takes.  A line through two measured sizes (none, 48 MB +
+// 1 KB a token: 63, 56 us at 16384 tokens, 169, 152 us at 131072); a sort by
+// fewer than 16 blocks was not measured and may leave room for more.
 long long cleared_early(const SumArgs &a, size_t row)
 {
     if (a.accumulate || a.n == 0 || a.n > kCsMost)

@@ -10,10 +10,11 @@
 // with more than its share.  The scaling's blocks start beside the norm's and
 // have their first tile in registers when the norm is known.
 //
-// Measured: 16.5 us for 25 MiB of fp16 (7.7 us to read and write it once; what
-// is left is two passes' ramps, 11 and 5 us, around the one point where every
-// sum has to be known), 1138 us for 10^9 elements in 40 tensors of bf16 and
-// fp32 (three passes over 2.5 GB, 6.6 TB/s).  Holding the 25 MiB in the SMs'
+// Measured: 16.2 us for 25 MiB of fp16 (7.7 us to read and write it once), 13.4
+// in place; 1125 us for 10^9 elements in 40 tensors of bf16 and fp32 (three
+// passes over 2.5 GB, 6.7 TB/s).  Of the 16.2 the norm takes 11 to 12, at a
+// third of the memory's rate: 63 registers leave room for four blocks an SM, so
+// the 800 tiles run as 608 and a second wave of 192.  Holding the 25 MiB in the SMs'
 // shared memory in one cooperative launch took 20.6 us; tiles of 8 and 16 KB,
 // 128 and 512 threads, and 5 to 8 blocks an SM were no faster.
 #include <math.h>
@@ -29,7 +30,8 @@ template <int THREADS> constexpr int kUnroll = kTileBytes / (16 * THREADS); // p
 constexpr int kMostItems = 512;                       // tensors of one launch
 constexpr int kFewItems = 16; // of a launch with short arguments
 constexpr int kSmallBytes = 65536; // of a list that one block takes in one launch
-constexpr int kGridPerSm = 8;                         // 256-thread blocks: full SMs
+constexpr int kGridPerSm = 8; // blocks; the squares' 63 registers hold 4 of them at a time, the
+                              // scaling's 48 hold 5, the other norms' 32 hold 8
 
 // One tensor of the list.  Its tiles start at a 16-byte boundary of `in`, so
 // that every pack of a tile is aligned; the `head` elements before it belong

@@ -273,8 +273,8 @@ __host__ __device__ inline bool aligned_to(const void *p, size_t n)
     return reinterpret_cast<uintptr_t>(p) % n == 0;
 }
 
-// Elements per pack: the widest of 16 bytes or less at which every address
-// (a multiple of `bytes` from the base) is aligned.
+// Are packs of `bytes` bytes aligned in every row, rows of row_bytes lying one
+// behind the other from `base` on?
 __host__ __device__ inline bool pack_fits(const void *base, size_t row_bytes, size_t bytes)
 {
     return aligned_to(base, bytes) && row_bytes % bytes == 0;
