@@ -83,19 +83,24 @@ def _blocks(x):
     return torch.nn.functional.pad(x, (0, -dim % BLOCK)).view(rows, -1, BLOCK)
 
 
+def _power(n):
+    """2^n for whole n from -126 to 127, by its bits: pow() may miss by a last place."""
+    return ((n.int() + 127) << 23).view(torch.float32)
+
+
 def _encode(x):
     """Exponents and codes of the rows of x (fp32): one exponent per block."""
     b = _blocks(x)
     top = b.abs().amax(2)
     e = (top.view(torch.int32) >> 23).clamp(min=1) - 127
-    m = torch.ldexp(b, (6 - e).unsqueeze(2)).round().clamp(-127, 127)
+    m = (b * _power(-e).unsqueeze(2) * 64).round().clamp(-127, 127)
     return e.to(torch.int8), m.to(torch.int8).view(x.shape[0], -1)
 
 
 def _decode(exps, codes, dim):
     """The values, fp32: m * 2^(e - 6)."""
     m = codes.view(exps.shape[0], exps.shape[1], BLOCK).float()
-    return torch.ldexp(m, (exps.int() - 6).unsqueeze(2)).view(exps.shape[0], -1)[:, :dim]
+    return (m / 64 * _power(exps).unsqueeze(2)).view(exps.shape[0], -1)[:, :dim]
 
 
 # ---------------------------------------------------------------- inputs
@@ -289,6 +294,10 @@ def work(case):
 
 # ---------------------------------------------------------------- in 64 bits
 
+def _exact_power(n):
+    return ((n.long() + 1023) << 52).view(torch.float64)
+
+
 def _exact_codes(x):
     """Exponents and codes of x, from the definition: the exponent of a block's largest magnitude,
     and the nearest whole numbers of its 64ths."""
@@ -298,12 +307,12 @@ def _exact_codes(x):
     b[:, :dim] = x
     top = b.abs().reshape(rows, n, BLOCK).max(2).values
     e = torch.where(top > 0, torch.frexp(top).exponent - 1, -126).clamp(min=-126)
-    unit = torch.pow(2.0, e.double() - 6).repeat_interleave(BLOCK, 1)
+    unit = _exact_power(e.long() - 6).repeat_interleave(BLOCK, 1)
     return e.to(torch.int8), torch.clamp(torch.round(b / unit), -127, 127).to(torch.int8)
 
 
 def _exact_values(exps, codes, dim):
-    unit = torch.pow(2.0, exps.double() - 6)
+    unit = _exact_power(exps.long() - 6)
     return (codes.double() * unit.repeat_interleave(BLOCK, 1))[:, :dim]
 
 
