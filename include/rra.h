@@ -724,6 +724,110 @@ rra_status rra_layer_norm_grad(const void *dy, const void *x, const void *gamma,
                                rra_dtype dtype, rra_dtype weight_t, void *dx, void *dgamma,
                                void *dbeta, int accumulate, void *stream);
 
+/*
+ * Activations in 8 bits: what a training step keeps of its forward pass for its
+ * backward pass, as block floating point ([cccl] §2.1), 8 bits an element.
+ * Each of `rows` rows of `dim` elements is cut into nb = ceil(dim / 128) blocks.
+ *  exps   int8[rows][nb]: e = floor(log2 max|v|) of the block, -126 for a zero
+ *         or subnormal maximum.
+ *  codes  int8[rows][nb * 128], on a 16-byte boundary: m = clamp(rne(v *
+ *         2^(6-e)), +-127) of every element, zeros behind the row's last one.
+ * An element stands for m * 2^(e-6), which fp32 and bf16 hold exactly.  These are
+ * rra_bfp_encode's bytes for rows of whole blocks, and rra_bfp_decode reads rows
+ * of any length with the zeros behind them.  A block with an infinity or NaN has
+ * e = -128 and codes 0 and stands for NaN throughout.
+ */
+
+/*
+ * Layer norm that also saves its input in 8 bits: y, mean and rstd as
+ * rra_layer_norm has them (from x itself), exps and codes of x.
+ * Errors: as rra_layer_norm; mean, rstd, exps and codes are required.
+ */
+rra_status rra_layer_norm_save(const void *x, const void *gamma, const void *beta, size_t rows,
+                               size_t dim, rra_dtype dtype, rra_dtype weight_t, float eps, void *y,
+                               int8_t *exps, int8_t *codes, float *mean, float *rstd,
+                               void *stream);
+
+/*
+ * Layer norm of a saved input: y = (v - mean) * rstd * gamma + beta, v what the
+ * codes stand for, rounded to dtype.
+ *  mean, rstd   fp32[rows]; NULL: 0 and 1.
+ *  gamma, beta  dim elements of weight_t (dtype or RRA_F32, else
+ *               RRA_ERR_UNSUPPORTED); NULL: 1 and 0.
+ * With all four NULL, y is any saved activation's values.
+ * Errors: as rra_layer_norm.
+ */
+rra_status rra_layer_norm_restore(const int8_t *exps, const int8_t *codes, const float *mean,
+                                  const float *rstd, const void *gamma, const void *beta,
+                                  size_t rows, size_t dim, rra_dtype dtype, rra_dtype weight_t,
+                                  void *y, void *stream);
+
+/*
+ * Gradients of layer norm from a saved input: rra_layer_norm_grad with
+ * xh = (v - mean) * rstd.  dx may be dy.
+ * Errors: as rra_layer_norm_grad.
+ */
+rra_status rra_layer_norm_saved_grad(const void *dy, const int8_t *exps, const int8_t *codes,
+                                     const void *gamma, const float *mean, const float *rstd,
+                                     size_t rows, size_t dim, rra_dtype dtype, rra_dtype weight_t,
+                                     void *dx, void *dgamma, void *dbeta, int accumulate,
+                                     void *stream);
+
+/* Activations a of the gated feed-forward block: g * logistic(g); g * P(g), P the
+ * normal distribution; g * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))) / 2;
+ * max(g, 0). */
+typedef enum {
+    RRA_ACT_SILU = 0,
+    RRA_ACT_GELU = 1,
+    RRA_ACT_GELU_TANH = 2,
+    RRA_ACT_RELU = 3
+} rra_act;
+
+/*
+ * Gated feed-forward block, up to its inner activation:
+ *   g = x * w_gate^T,  u = x * w_up^T,  h = a(g) * u
+ *  x              rows * dim elements of dtype.
+ *  w_gate, w_up   ff * dim elements of dtype.
+ *  h              rows * ff elements of dtype, from g and u in fp32.
+ *  gate, up       what is kept of g and u for the backward pass: in 8 bits
+ *                 (gate_exps and gate as codes, of rows of ff elements), or
+ *                 rounded to dtype (rows * ff elements; gate_exps NULL), or
+ *                 nothing (both NULL); up the same, apart from gate.
+ * Arrays of 16-byte alignment with dim a multiple of 16 bytes run fastest;
+ * others of 16-bit types are laid out anew in scratch memory first.
+ * Errors: RRA_ERR_INVALID (NULL, bad enums, dim or ff 0, rows, dim or ff above
+ * 2^31 - 1, an array of more than 64 TB, an output that overlaps an input or
+ * another output), RRA_ERR_NOMEM, RRA_ERR_CUDA.
+ */
+rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, size_t rows,
+                        size_t dim, size_t ff, rra_dtype dtype, rra_act act, void *h,
+                        int8_t *gate_exps, void *gate, int8_t *up_exps, void *up, void *stream);
+
+/*
+ * Gradient of the gated feed-forward block, from the kept g and u (both in 8
+ * bits, or both of dtype: gate_exps and up_exps NULL):
+ *   dup = dh * a(g),  dgate = dh * u * a'(g),  h = a(g) * u
+ *   dx = dgate * w_gate + dup * w_up
+ *   dw_gate = dgate^T * x,  dw_up = dup^T * x
+ *  dgate, dup     rows * ff elements of dtype, required: the products below are
+ *                 taken of these rounded values.
+ *  h              the inner activation again (for the gradient of what follows
+ *                 it); NULL: not computed.
+ *                 Each of the three may take the place of dh, gate or up (not of
+ *                 codes).
+ *  dx             rows * dim elements of dtype; NULL: not computed.
+ *  dw_gate, dw_up ff * dim elements of dweight_t (dtype or RRA_F32, else
+ *                 RRA_ERR_UNSUPPORTED); either may be NULL.  accumulate nonzero:
+ *                 added to what they hold, in fp32.
+ * x is not read when both weights' gradients are NULL, the weights not when dx is.
+ * Errors: as rra_gated_ff.
+ */
+rra_status rra_gated_ff_grad(const void *dh, const void *x, const void *w_gate, const void *w_up,
+                             const int8_t *gate_exps, const void *gate, const int8_t *up_exps,
+                             const void *up, size_t rows, size_t dim, size_t ff, rra_dtype dtype,
+                             rra_act act, void *dgate, void *dup, void *h, void *dx, void *dw_gate,
+                             void *dw_up, rra_dtype dweight_t, int accumulate, void *stream);
+
 /* Human-readable name of a status code (static string). */
 const char *rra_status_string(rra_status s);
 

@@ -11,7 +11,9 @@ Names follow the C ABI: ``Comm.ring_allreduce``, ``Comm.reduce_scatter``,
 ``Comm.allgather``, ``Comm.broadcast``, ``Comm.tree_allreduce``,
 ``bfp_encode``/``bfp_decode``, ``sparse_encode``/``sparse_decode``,
 ``diff_encode``; the training-step operators ``grad_norm``/``grad_clip``,
-``embedding``/``embedding_grad``, ``layer_norm``/``layer_norm_grad``.
+``embedding``/``embedding_grad``, ``layer_norm``/``layer_norm_grad``,
+``layer_norm_save``/``layer_norm_restore``/``layer_norm_saved_grad`` (an input
+kept in 8 bits, ``Saved``), ``gated_ff``/``gated_ff_grad``.
 """
 from __future__ import annotations
 
@@ -42,6 +44,7 @@ RING_SLICE = 256
 SPARSE_PER_CHUNK, SPARSE_PER_SLICE = 0, 1
 RRA_NORM_L2, RRA_NORM_L1, RRA_NORM_INF = 0, 1, 2
 RRA_I32, RRA_I64 = 0, 1
+RRA_ACT_SILU, RRA_ACT_GELU, RRA_ACT_GELU_TANH, RRA_ACT_RELU = range(4)
 
 _lib = None
 
@@ -119,6 +122,13 @@ def lib():
         L.rra_layer_norm.argtypes = [vp, vp, vp, sz, sz, i32, i32, f32, vp, vp, vp, vp]
         L.rra_layer_norm_grad.argtypes = [vp, vp, vp, vp, vp, sz, sz, i32, i32, vp, vp, vp, i32,
                                           vp]
+        L.rra_layer_norm_save.argtypes = [vp, vp, vp, sz, sz, i32, i32, f32, vp, vp, vp, vp, vp,
+                                          vp]
+        L.rra_layer_norm_restore.argtypes = [vp] * 6 + [sz, sz, i32, i32, vp, vp]
+        L.rra_layer_norm_saved_grad.argtypes = [vp] * 6 + [sz, sz, i32, i32, vp, vp, vp, i32, vp]
+        L.rra_gated_ff.argtypes = [vp, vp, vp, sz, sz, sz, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.rra_gated_ff_grad.argtypes = [vp] * 8 + [sz, sz, sz, i32, i32] + [vp] * 6 + \
+            [i32, i32, vp]
         L.rra_status_string.argtypes = [i32]
         L.rra_status_string.restype = C.c_char_p
         for name in ("rra_comm_create", "rra_comm_destroy", "rra_ring_allreduce",
@@ -133,7 +143,9 @@ def lib():
                      "rra_get_crossover", "rra_autotune_crossover", "rra_codec_measure",
                      "rra_codec_advise", "rra_codec_measure_op", "rra_codec_advise_op",
                      "rra_grad_norm", "rra_grad_clip", "rra_embedding", "rra_embedding_grad",
-                     "rra_layer_norm", "rra_layer_norm_grad"):
+                     "rra_layer_norm", "rra_layer_norm_grad", "rra_layer_norm_save",
+                     "rra_layer_norm_restore", "rra_layer_norm_saved_grad", "rra_gated_ff",
+                     "rra_gated_ff_grad"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -649,3 +661,180 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate: boo
                                        1 if accumulate else 0,
                                        stream.cuda_stream if stream is not None else ops.stream(dev)),
            "rra_layer_norm_grad")
+
+
+class Saved:
+    """An activation in 8 bits (rows of ``dim`` elements): ``exps``, int8 (rows,
+    blocks of 128), and ``codes``, int8 (rows, blocks * 128).  An element stands
+    for code * 2^(exponent - 6); layer_norm_restore gives them all."""
+
+    __slots__ = ("exps", "codes", "dim")
+
+    def __init__(self, exps, codes, dim: int):
+        nb = -(-dim // BFP_BLOCK)
+        if exps.dim() != 2 or exps.shape[1] != nb or \
+                codes.shape != (exps.shape[0], nb * BFP_BLOCK):
+            raise ValueError(f"Saved: expected exps (rows, {nb}) and codes (rows, "
+                             f"{nb * BFP_BLOCK}) for rows of {dim} elements, got "
+                             f"{tuple(exps.shape)} and {tuple(codes.shape)}")
+        self.exps, self.codes, self.dim = exps, codes, dim
+
+    @classmethod
+    def empty(cls, rows: int, dim: int, device="cuda"):
+        """Room for ``rows`` rows of ``dim`` elements."""
+        import torch
+        nb = -(-dim // BFP_BLOCK)
+        return cls(torch.empty(rows, nb, dtype=torch.int8, device=device),
+                   torch.empty(rows, nb * BFP_BLOCK, dtype=torch.int8, device=device), dim)
+
+    def _at(self, name, device, rows, dim):
+        """Addresses of exps and codes, for rows of dim elements."""
+        import torch
+        if self.dim != dim or self.exps.shape[0] != rows:
+            raise ValueError(f"{name}: expected {rows} saved rows of {dim} elements, got "
+                             f"{self.exps.shape[0]} of {self.dim}")
+        return (_op(self.exps, name, device, torch.int8), _op(self.codes, name, device, torch.int8))
+
+
+def layer_norm_save(x, gamma, beta, y, saved: Saved, mean, rstd, eps: float = 1e-5, stream=None):
+    """rra_layer_norm_save: layer_norm, and x into ``saved`` for
+    layer_norm_restore and layer_norm_saved_grad (with mean and rstd)."""
+    rows, dim = _rows(x, "x")
+    if not x.is_cuda:
+        raise ValueError("x: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    w = gamma if gamma is not None else beta if beta is not None else x
+    wt = w.dtype
+    exps, codes = saved._at("saved", dev, rows, dim)
+    _check(ops.lib.rra_layer_norm_save(_op(x, "x", dev), _op(gamma, "gamma", dev, wt, (dim,)),
+                                       _op(beta, "beta", dev, wt, (dim,)), rows, dim,
+                                       _op_dtype(ops, x), _op_dtype(ops, w), eps,
+                                       _op(y, "y", dev, x.dtype, x.shape), exps, codes,
+                                       _op(mean, "mean", dev, ops.f32, (rows,)),
+                                       _op(rstd, "rstd", dev, ops.f32, (rows,)),
+                                       stream.cuda_stream if stream is not None else ops.stream(dev)),
+           "rra_layer_norm_save")
+
+
+def layer_norm_restore(saved: Saved, y, gamma=None, beta=None, mean=None, rstd=None, stream=None):
+    """rra_layer_norm_restore: y = (v - mean) * rstd * gamma + beta, v the saved
+    values; what is None is left out (with nothing given, y = v)."""
+    rows, dim = _rows(y, "y")
+    if not y.is_cuda:
+        raise ValueError("y: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    w = gamma if gamma is not None else beta if beta is not None else y
+    wt = w.dtype
+    exps, codes = saved._at("saved", dev, rows, dim)
+    _check(ops.lib.rra_layer_norm_restore(exps, codes, _op(mean, "mean", dev, ops.f32, (rows,)),
+                                          _op(rstd, "rstd", dev, ops.f32, (rows,)),
+                                          _op(gamma, "gamma", dev, wt, (dim,)),
+                                          _op(beta, "beta", dev, wt, (dim,)), rows, dim,
+                                          _op_dtype(ops, y), _op_dtype(ops, w), _op(y, "y", dev),
+                                          stream.cuda_stream if stream is not None else ops.stream(dev)),
+           "rra_layer_norm_restore")
+
+
+def layer_norm_saved_grad(dy, saved: Saved, gamma, mean, rstd, dx, dgamma, dbeta,
+                          accumulate: bool = False, stream=None):
+    """rra_layer_norm_saved_grad: layer_norm_grad from an input that
+    layer_norm_save has kept.  dx may be dy."""
+    rows, dim = _rows(dy, "dy")
+    if not dy.is_cuda:
+        raise ValueError("dy: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    w = gamma if gamma is not None else dgamma if dgamma is not None else \
+        dbeta if dbeta is not None else dy
+    wt = w.dtype
+    exps, codes = saved._at("saved", dev, rows, dim)
+    _check(ops.lib.rra_layer_norm_saved_grad(_op(dy, "dy", dev), exps, codes,
+                                             _op(gamma, "gamma", dev, wt, (dim,)),
+                                             _op(mean, "mean", dev, ops.f32, (rows,)),
+                                             _op(rstd, "rstd", dev, ops.f32, (rows,)), rows, dim,
+                                             _op_dtype(ops, dy), _op_dtype(ops, w),
+                                             _op(dx, "dx", dev, dy.dtype, dy.shape),
+                                             _op(dgamma, "dgamma", dev, wt, (dim,)),
+                                             _op(dbeta, "dbeta", dev, wt, (dim,)),
+                                             1 if accumulate else 0,
+                                             stream.cuda_stream if stream is not None else ops.stream(dev)),
+           "rra_layer_norm_saved_grad")
+
+
+_ACTS = {"silu": RRA_ACT_SILU, "gelu": RRA_ACT_GELU, "gelu_tanh": RRA_ACT_GELU_TANH,
+         "relu": RRA_ACT_RELU}
+
+
+def _act_code(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {', '.join(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _kept(t, name, device, dtype, shape, rows, ff):
+    """Addresses (exps, data) of gate or up: Saved, a tensor, or None."""
+    if isinstance(t, Saved):
+        return t._at(name, device, rows, ff)
+    return None, _op(t, name, device, dtype, shape)
+
+
+def gated_ff(x, w_gate, w_up, h, gate=None, up=None, act: str = "silu", stream=None):
+    """rra_gated_ff: h = a(x w_gate^T) * (x w_up^T) for (ff, dim) weights and x
+    (..., dim).  gate and up keep the two products for gated_ff_grad: a Saved (8
+    bits), a tensor of h's shape and type, or None."""
+    kind = _act_code(act)
+    rows, dim = _rows(x, "x")
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate: expected (ff, dim)")
+    if not x.is_cuda:
+        raise ValueError("x: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    ff = w_gate.shape[0]
+    shape = x.shape[:-1] + (ff,)
+    gate_exps, gate_data = _kept(gate, "gate", dev, x.dtype, shape, rows, ff)
+    up_exps, up_data = _kept(up, "up", dev, x.dtype, shape, rows, ff)
+    _check(ops.lib.rra_gated_ff(_op(x, "x", dev), _op(w_gate, "w_gate", dev, x.dtype, (ff, dim)),
+                                _op(w_up, "w_up", dev, x.dtype, (ff, dim)), rows, dim, ff,
+                                _op_dtype(ops, x), kind, _op(h, "h", dev, x.dtype, shape),
+                                gate_exps, gate_data, up_exps, up_data,
+                                stream.cuda_stream if stream is not None else ops.stream(dev)),
+           "rra_gated_ff")
+
+
+def gated_ff_grad(dh, x, w_gate, w_up, gate, up, dgate, dup, dx=None, dw_gate=None, dw_up=None,
+                  h=None, act: str = "silu", accumulate: bool = False, stream=None):
+    """rra_gated_ff_grad: the gradients of gated_ff from dh and what it kept of
+    gate and up.  dgate and dup (dh's shape and type) are computed always, the
+    others and h where given; dgate, dup and h may take dh's place, or that of
+    gate and up where these are tensors.  accumulate adds to what dw_gate and
+    dw_up hold."""
+    kind = _act_code(act)
+    rows, ff = _rows(dh, "dh")
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate: expected (ff, dim)")
+    if not dh.is_cuda:
+        raise ValueError("dh: expected a contiguous CUDA tensor")
+    ops = _setup()
+    dev = ops.device()
+    dim, t = w_gate.shape[1], dh.dtype
+    if isinstance(gate, Saved) != isinstance(up, Saved):
+        raise TypeError("gate, up: expected both Saved or both tensors")
+    gate_exps, gate_data = _kept(gate, "gate", dev, t, dh.shape, rows, ff)
+    up_exps, up_data = _kept(up, "up", dev, t, dh.shape, rows, ff)
+    dw = dw_gate if dw_gate is not None else dw_up if dw_up is not None else dh
+    dt, wide = dw.dtype, dh.shape[:-1] + (dim,)
+    _check(ops.lib.rra_gated_ff_grad(_op(dh, "dh", dev), _op(x, "x", dev, t, wide),
+                                     _op(w_gate, "w_gate", dev, t, (ff, dim)),
+                                     _op(w_up, "w_up", dev, t, (ff, dim)), gate_exps, gate_data,
+                                     up_exps, up_data, rows, dim, ff, _op_dtype(ops, dh), kind,
+                                     _op(dgate, "dgate", dev, t, dh.shape),
+                                     _op(dup, "dup", dev, t, dh.shape),
+                                     _op(h, "h", dev, t, dh.shape), _op(dx, "dx", dev, t, wide),
+                                     _op(dw_gate, "dw_gate", dev, dt, (ff, dim)),
+                                     _op(dw_up, "dw_up", dev, dt, (ff, dim)), _op_dtype(ops, dw),
+                                     1 if accumulate else 0,
+                                     stream.cuda_stream if stream is not None else ops.stream(dev)),
+           "rra_gated_ff_grad")

@@ -1,5 +1,5 @@
 // op_common.cuh -- what the training-step operators (grad_norm.cu,
-// embedding.cu, layer_norm.cu) share: packs of elements read and written by
+// embedding.cu, layer_norm.cu, layer_norm_saved.cu, gated_ff.cu) share: packs of elements read and written by
 // one instruction, block reductions, argument checks and the scratch memory
 // of a stream.
 #pragma once
@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
@@ -266,6 +267,20 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// An argument's bytes, for comparing several.
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+
+inline bool any_overlap(const Span &a, std::initializer_list<Span> others)
+{
+    for (const Span &b : others)
+        if (overlap(a.p, a.bytes, b.p, b.bytes))
+            return true;
+    return false;
 }
 
 __host__ __device__ inline bool aligned_to(const void *p, size_t n)

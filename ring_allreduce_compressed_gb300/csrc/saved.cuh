@@ -1,0 +1,172 @@
+// saved.cuh -- activations held in 8 bits between the two passes of a step.
+//
+// A row of D elements is cut into blocks of 128; a block has one exponent
+// e = floor(log2 max|v|) (-126 for a zero or subnormal maximum) and a code
+// m = clamp(rne(v 2^(6-e)), +-127) for each element, which stands for
+// m 2^(e-6): the block floating point of rra_bfp_encode, with every row's
+// blocks its own.  Codes lie in rows of whole blocks (zeros behind D), so a
+// pack of 8 is one 8-byte access in every row whatever D is.
+// A block with an infinity or NaN has the exponent byte -128 and codes 0: its
+// scale 2^e comes out as infinity, and 0 times that is NaN.
+//
+// Everywhere a lane holds packs of 8 elements and 16 neighbouring lanes a
+// block.
+#pragma once
+
+#include "bfp_group.cuh"
+#include "op_common.cuh"
+
+namespace rra {
+
+constexpr int kPack = 8;                     // elements
+constexpr int kBlockPacks = kBlock / kPack;  // packs that share an exponent
+
+__host__ __device__ inline long long blocks_of(long long dim) { return (dim + kBlock - 1) / kBlock; }
+
+struct Codes8 {
+    uint32_t w[2];
+};
+
+// Biased exponent of a block from the bits of its largest magnitude (an
+// infinity or NaN: 255), and the byte that is stored.
+__device__ __forceinline__ int block_exponent(uint32_t top_bits)
+{
+    return max((int)(top_bits >> 23), 1);
+}
+__device__ __forceinline__ int8_t exponent_byte(int E) { return (int8_t)(E - 127); }
+
+// Codes of 8 values in a block of biased exponent E (two's complement).  As in
+// BfpGroup: t = fma(v, 2^(6-e), 1.5 2^23 + 128) holds m + 128 in its low byte.
+__device__ __forceinline__ Codes8 encode8(const float v[8], int E)
+{
+    constexpr float kEnc = kMagic + 128.0f;
+    if (E == 255)
+        return {{0u, 0u}};
+    // 2^(6-e), a normal float unless E < 6: such blocks are first scaled by 2^64
+    int sb = 260 - E;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        x[j] = v[j];
+    if (E < 6) {
+        sb -= 64;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = __fmul_rn(x[j], 1.8446744073709552e19f);
+    }
+    const float s = __int_as_float(sb << 23);
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(s, s),
+                                    make_float2(kEnc, kEnc));
+        // m is at most 128 before it is clamped: 2^(6-e) max|v| < 128
+        u[j] = __float_as_uint(fminf(fmaxf(t.x, kEnc - 127.0f), kEnc + 127.0f));
+        u[j + 1] = __float_as_uint(fminf(fmaxf(t.y, kEnc - 127.0f), kEnc + 127.0f));
+    }
+    Codes8 c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        c.w[h] = __byte_perm(__byte_perm(u[4 * h], u[4 * h + 1], 0x0040),
+                             __byte_perm(u[4 * h + 2], u[4 * h + 3], 0x0040), 0x5410) ^
+                 0x80808080u;
+    return c;
+}
+
+// The 8 values of codes whose block's exponent byte is e.
+__device__ __forceinline__ void decode8(const Codes8 &c, int8_t e, float v[8])
+{
+    constexpr float kOff = -(kMagic + 128.0f) / 64.0f;
+    const float s = __uint_as_float(((uint32_t)(e + 127) & 255u) << 23);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = c.w[h] ^ 0x80808080u; // m + 128
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const float2 f = make_float2(__uint_as_float(__byte_perm(x, kMagicBits, 0x7640 + j)),
+                                         __uint_as_float(__byte_perm(x, kMagicBits, 0x7641 + j)));
+            // m 2^-6, exactly; times 2^e
+            const float2 r = __fmul2_rn(
+                __ffma2_rn(f, make_float2(1.0f / 64, 1.0f / 64), make_float2(kOff, kOff)),
+                make_float2(s, s));
+            v[4 * h + j] = r.x;
+            v[4 * h + j + 1] = r.y;
+        }
+    }
+}
+
+__device__ __forceinline__ Codes8 load_codes(const int8_t *p)
+{
+    const Pack<uint32_t, 2> q = load_pack<uint32_t, 2>(reinterpret_cast<const uint32_t *>(p));
+    return {{q.e[0], q.e[1]}};
+}
+__device__ __forceinline__ void store_codes(int8_t *p, const Codes8 &c)
+{
+    Pack<uint32_t, 2> q;
+    q.e[0] = c.w[0];
+    q.e[1] = c.w[1];
+    store_pack<uint32_t, 2>(reinterpret_cast<uint32_t *>(p), q);
+}
+
+// Largest magnitude's bits over each half of a warp; every lane takes part.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t bits)
+{
+    const bool low = threadIdx.x % 32 < 16;
+    const uint32_t a = __reduce_max_sync(kFull, low ? bits : 0u);
+    const uint32_t b = __reduce_max_sync(kFull, low ? 0u : bits);
+    return low ? a : b;
+}
+
+// Bits of the largest magnitude of 8 values: infinities and NaN are above all
+// finite ones.
+__device__ __forceinline__ uint32_t top_bits(const float v[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return m;
+}
+
+// n (0..8) elements at p, as fp32, zeros behind them; VEC: n is 0 or 8 and p a
+// multiple of 16 bytes.
+template <typename T, bool VEC> __device__ __forceinline__ void load8(const T *p, int n, float v[8])
+{
+    if (VEC) {
+        T t[8];
+        if (n == 8) {
+            load_values<T, 8>(p, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = to_f32(t[j]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = !VEC && j < n ? to_f32(p[j]) : 0.0f;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T *p, int n, const float v[8])
+{
+    if (VEC) {
+        T t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t[j] = from_f32<T>(v[j]);
+        if (n == 8)
+            store_values<T, 8>(p, t);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n)
+            p[j] = from_f32<T>(v[j]);
+}
+
+// Exponents and codes of an activation of `rows` rows.
+inline size_t exps_bytes(size_t rows, size_t dim) { return rows * (size_t)blocks_of(dim); }
+inline size_t codes_bytes(size_t rows, size_t dim) { return rows * (size_t)blocks_of(dim) * kBlock; }
+
+} // namespace rra
