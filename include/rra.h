@@ -603,8 +603,8 @@ rra_status rra_debug_withhold(rra_comm *comm, int rank, int step);
  *  - All sums and statistics are held in fp32 or more; every result is
  *    rounded to its type once, to nearest even.  Equal calls give equal bits.
  *  - Infinities and NaN are carried through as the formulas have it.
- *  - rra_grad_norm, rra_grad_clip, rra_embedding_grad and
- *    rra_layer_norm_grad use scratch memory that the library keeps per device
+ *  - rra_grad_norm, rra_grad_clip, rra_embedding_grad, rra_layer_norm_grad,
+ *    rra_layer_norm_saved_grad, rra_gated_ff and rra_gated_ff_grad use scratch memory that the library keeps per device
  *    and stream (cudaStreamPerThread: per thread) and allocates with
  *    cudaMalloc when a call needs more than it holds (it at least doubles when
  *    it grows).  What it replaces, then or when a destroyed stream's handle
@@ -796,8 +796,10 @@ typedef enum {
  * Arrays of 16-byte alignment with dim a multiple of 16 bytes run fastest;
  * others of 16-bit types are laid out anew in scratch memory first.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, dim or ff 0, rows, dim or ff above
- * 2^31 - 1, an array of more than 64 TB, an output that overlaps an input or
- * another output), RRA_ERR_NOMEM, RRA_ERR_CUDA.
+ * 2^30, an array of more than 64 TB, an output that overlaps an input or another
+ * output), RRA_ERR_NOMEM, RRA_ERR_CUDA; RRA_ERR_TIMEOUT (this call did nothing): a
+ * wait inside a kernel of an earlier call of these two ran out of time (4 s), and
+ * that call's outputs are not complete.
  */
 rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, size_t rows,
                         size_t dim, size_t ff, rra_dtype dtype, rra_act act, void *h,

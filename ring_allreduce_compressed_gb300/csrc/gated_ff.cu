@@ -238,10 +238,136 @@ template <typename T> cudaError_t act_grad(const FfGradArgs &a, cudaStream_t st)
     return launch_chained(fn, grid, kActThreads, st, a, lanes);
 }
 
+// ---------------------------------------------------------------- operands for tensor maps
+
+// A matrix whose rows do not begin on 16-byte boundaries, copied to rows that do.
+template <typename T>
+__global__ void __launch_bounds__(kActThreads) align_kernel(const T *from, T *to, long long rows,
+                                                            long long cols, long long ld)
+{
+    const long long packs = ld / kPack, total = rows * packs;
+    dependents_wait();
+    dependents_launch();
+    for (long long i = (long long)blockIdx.x * kActThreads + threadIdx.x; i < total;
+         i += (long long)gridDim.x * kActThreads) {
+        const long long r = i / packs, c = (i - r * packs) * kPack;
+        const int there = (int)min((long long)kPack, cols - c);
+        Pack<T, kPack> v;
+#pragma unroll
+        for (int j = 0; j < kPack; ++j)
+            v.e[j] = j < there ? from[r * cols + c + j] : from_f32<T>(0.0f);
+        store_pack<T, kPack>(to + r * ld + c, v);
+    }
+}
+
+// Operands as tensor maps can read them: where they are, or in the stream's scratch.
+template <typename T, int N> class Aligned {
+public:
+    Matrix16 m[N];
+
+    // Plans copies of those that need one; their places follow from take().
+    explicit Aligned(const Matrix16 (&given)[N])
+    {
+        for (int i = 0; i < N; ++i) {
+            m[i] = given[i];
+            copy_[i] = m[i].p && m[i].rows > 0 && !gemm_takes(m[i]);
+            if (copy_[i]) {
+                m[i].ld = (m[i].cols + kPack - 1) / kPack * kPack;
+                at_[i] = bytes_;
+                bytes_ += (size_t)m[i].rows * m[i].ld * sizeof(T) + 255 & ~(size_t)255;
+            }
+        }
+    }
+    size_t bytes() const { return bytes_; }
+    rra_status take(cudaStream_t st)
+    {
+        if (!bytes_)
+            return RRA_OK;
+        const rra_status r = op_scratch(st, kScratchHead + bytes_, lk_, &ws_);
+        return r;
+    }
+    // Copies operand i, once what it holds is there.
+    cudaError_t fill(int i, cudaStream_t st)
+    {
+        if (!copy_[i])
+            return cudaSuccess;
+        T *const to = reinterpret_cast<T *>(ws_ + kScratchHead + at_[i]);
+        const long long packs = m[i].rows * (m[i].ld / kPack);
+        const unsigned grid = (unsigned)std::min((packs + kActThreads - 1) / kActThreads,
+                                                 (long long)num_sms() * 32);
+        const cudaError_t e =
+            launch_chained(align_kernel<T>, dim3(grid), kActThreads, st,
+                           static_cast<const T *>(m[i].p), to, m[i].rows, m[i].cols, m[i].ld);
+        m[i].p = to;
+        return e;
+    }
+
+private:
+    bool copy_[N];
+    size_t at_[N], bytes_ = 0;
+    unsigned char *ws_ = nullptr;
+    std::unique_lock<std::mutex> lk_; // until the call's launches are queued
+};
+
 // ---------------------------------------------------------------- calls
+
+// Has a kernel given up waiting since the last call?
+rra_status stalled_status()
+{
+    unsigned *word = nullptr;
+    if (stalled_word(&word) != cudaSuccess)
+        return RRA_ERR_CUDA;
+    volatile unsigned *const w = word;
+    if (!*w)
+        return RRA_OK;
+    *w = 0;
+    return RRA_ERR_TIMEOUT;
+}
+
+template <typename T> rra_status ff_tensor(const FfArgs &a, cudaStream_t st)
+{
+    rra_status s = stalled_status();
+    if (s != RRA_OK)
+        return s;
+    Aligned<T, 3> in({{a.x, a.rows, a.dim, a.dim}, {a.wg, a.ff, a.dim, a.dim},
+                      {a.wu, a.ff, a.dim, a.dim}});
+    if ((s = in.take(st)) != RRA_OK)
+        return s;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+        e = in.fill(i, st);
+    return launched(e == cudaSuccess ? gemm_forward<T>(a, in.m[0], in.m[1], in.m[2], st) : e);
+}
+
+template <typename T, typename O> rra_status ff_grad_tensor(const FfGradArgs &a, cudaStream_t st)
+{
+    rra_status s = stalled_status();
+    if (s != RRA_OK)
+        return s;
+    const bool weights = a.dwg || a.dwu;
+    Aligned<T, 5> in({{a.dgate, a.rows, a.ff, a.ff},
+                      {a.dup, a.rows, a.ff, a.ff},
+                      {a.dx ? a.wg : nullptr, a.ff, a.dim, a.dim},
+                      {a.dx ? a.wu : nullptr, a.ff, a.dim, a.dim},
+                      {weights ? a.x : nullptr, a.rows, a.dim, a.dim}});
+    if (!a.dx && !weights)
+        return launched(act_grad<T>(a, st));
+    if ((s = in.take(st)) != RRA_OK)
+        return s;
+    cudaError_t e = act_grad<T>(a, st);
+    for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+        e = in.fill(i, st);
+    if (e == cudaSuccess && a.dx)
+        e = gemm_dx<T>(a, in.m[0], in.m[1], in.m[2], in.m[3], st);
+    if (e == cudaSuccess && weights)
+        e = gemm_dw<T, O>(a, in.m[0], in.m[1], in.m[4], st);
+    return launched(e);
+}
 
 template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
 {
+    if constexpr (sizeof(T) == 2)
+        return ff_tensor<T>(a, st);
     const long long tiles = (a.ff + kTileN - 1) / kTileN * ((a.rows + kTileM - 1) / kTileM);
     return launched(launch_chained(ff_plain_kernel<T>, dim3((unsigned)std::min(tiles, 1LL << 20)),
                                    kTileThreads, st, a));
@@ -249,6 +375,9 @@ template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
 
 template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaStream_t st)
 {
+    if constexpr (sizeof(T) == 2)
+        if (a.rows > 0)
+            return ff_grad_tensor<T, O>(a, st);
     cudaError_t e = a.rows > 0 ? act_grad<T>(a, st) : cudaSuccess;
     if (e == cudaSuccess && a.dx && a.rows > 0) {
         const Product p{{{a.dgate, a.ff}, {a.dup, a.ff}},
@@ -278,7 +407,7 @@ template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaSt
     return launched(e);
 }
 
-constexpr size_t kMost = ((size_t)1 << 31) - 1; // rows, dim, ff
+constexpr size_t kMost = (size_t)1 << 30; // rows, dim, ff
 
 bool valid_ff(size_t rows, size_t dim, size_t ff, rra_dtype t, rra_act act)
 {

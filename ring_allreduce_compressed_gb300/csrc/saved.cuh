@@ -157,12 +157,12 @@ __device__ __forceinline__ void store8(T *p, int n, const float v[8])
             t[j] = from_f32<T>(v[j]);
         if (n == 8)
             store_values<T, 8>(p, t);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n)
-            p[j] = from_f32<T>(v[j]);
+        for (int j = 0; j < 8; ++j)
+            if (j < n)
+                p[j] = from_f32<T>(v[j]);
+    }
 }
 
 // Exponents and codes of an activation of `rows` rows.
