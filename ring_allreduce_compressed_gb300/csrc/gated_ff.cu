@@ -74,13 +74,13 @@ __device__ __forceinline__ void keep_row(const Kept &to, long long r, long long 
             w[j] = c0 + c + j < ff ? v[j] : 0.0f;
             top = max(top, __float_as_uint(w[j]) & 0x7fffffffu);
         }
-        const int E = block_exponent(__reduce_max_sync(kFull, top));
-        const Codes8 q = encode8(w, E);
+        top = __reduce_max_sync(kFull, top);
+        const Codes8 q = encode8(w, top);
         const long long nb = blocks_of(ff), b = c0 / kBlock;
         *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(to.data) + (r * nb + b) * kBlock + c) =
             q.w[0];
         if (c == 0)
-            to.exps[r * nb + b] = exponent_byte(E);
+            to.exps[r * nb + b] = exponent_byte(block_exponent(top));
     } else if (to.data) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -103,12 +103,12 @@ __device__ __forceinline__ uint32_t row_top(uint32_t at)
 
 // One of gate and up, 8 columns from c on of row r.
 template <typename T>
-__device__ __forceinline__ void keep8(const Kept &to, int E, long long r, long long c, long long ff,
+__device__ __forceinline__ void keep8(const Kept &to, uint32_t top, long long r, long long c, long long ff,
                                       bool whole, const float v[8])
 {
     if (to.exps) {
         const long long nb = blocks_of(ff);
-        store_codes(static_cast<int8_t *>(to.data) + r * nb * kBlock + c, encode8(v, E));
+        store_codes(static_cast<int8_t *>(to.data) + r * nb * kBlock + c, encode8(v, top));
     } else if (to.data) {
         put8(static_cast<T *>(to.data) + r * ff + c, (int)max(0LL, min(8LL, ff - c)), whole, v);
     }
@@ -119,17 +119,17 @@ template <typename T>
 __device__ __forceinline__ void write_forward(const Gemm &g, uint32_t at, long long r, long long n0,
                                               bool whole)
 {
-    int eg = 0, eu = 0;
+    uint32_t eg = 0, eu = 0; // bits of the blocks' largest magnitudes
     if (g.gate.exps)
-        eg = block_exponent(row_top(at));
+        eg = row_top(at);
     if (g.up.exps)
-        eu = block_exponent(row_top(at + kHalf));
+        eu = row_top(at + kHalf);
     const bool on = r < g.m;
     const long long nb = blocks_of(g.n);
     if (on && g.gate.exps)
-        g.gate.exps[r * nb + n0 / kBlock] = exponent_byte(eg);
+        g.gate.exps[r * nb + n0 / kBlock] = exponent_byte(block_exponent(eg));
     if (on && g.up.exps)
-        g.up.exps[r * nb + n0 / kBlock] = exponent_byte(eu);
+        g.up.exps[r * nb + n0 / kBlock] = exponent_byte(block_exponent(eu));
     for (int c = 0; c < kHalf; c += 32) {
         uint32_t rg[32], ru[32];
         tmem_load(at + c, rg);

@@ -13,6 +13,7 @@
 // Bound by memory: one pass over what is read and written, 8 bits of the saved
 // row among it.
 #include "op_common.cuh"
+#include "ragged.cuh"
 #include "row_group.cuh"
 #include "saved.cuh"
 
@@ -38,6 +39,13 @@ __device__ __forceinline__ int in_pack(long long dim, long long u)
     return (int)max(0LL, min((long long)kPack, dim - u * kPack));
 }
 
+// The pairs of a pack.
+template <typename T>
+__device__ __forceinline__ Pair pair_in(const uint32_t (&w)[kPackWords<T>], int j)
+{
+    return pair_of(element<T>(w, 2 * j), element<T>(w, 2 * j + 1));
+}
+
 // ---------------------------------------------------------------- save
 
 struct Save {
@@ -50,23 +58,26 @@ struct Save {
     Group g;
 };
 
+// Threads of a block, wide rows apart: 80 registers a thread hold a row without
+// spilling, 64 do not.
 constexpr int kSaveThreads = 256;
 constexpr int kSaveHeld = 4; // packs of a lane
 
 // A row in the registers of a group of lanes, as in norm_kernel: lane i holds
 // packs i, i + lanes, ..., and 16 lanes of a warp a block of codes.
-// VEC: every pack is whole and on a 16-byte boundary.
-template <typename T, typename W, int K, bool MULTI, bool VEC>
-__global__ void __launch_bounds__(MULTI ? 1024 : kSaveThreads) save_kernel(const Save a)
+// WHOLE: every pack is whole and on a 16-byte boundary.
+template <typename T, typename W, int K, bool MULTI, bool WHOLE, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 3 : 1)
+    save_kernel(const Save a)
 {
     __shared__ __align__(16) float sm[MULTI ? 2 * 32 : 4];
-    const T *const x = static_cast<const T *>(a.x);
+    const T *const x = static_cast<const T *>(a.x), *const x_end = x + a.rows * a.dim;
     T *const y = static_cast<T *>(a.y);
     const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
                                                                 static_cast<const W *>(a.beta);
     const int lanes = a.g.lanes(), li = threadIdx.x % lanes, groups = blockDim.x / lanes;
-    const int nb = (int)blocks_of(a.dim), packs = nb * kBlockPacks;
-    const float n = (float)a.dim, inverse = 1.0f / n;
+    const int dim = (int)a.dim, nb = (int)blocks_of(dim), packs = nb * kBlockPacks;
+    const float n = (float)dim, inverse = 1.0f / n;
     GroupOf group = group_of(a.g, sm, 1);
     if (MULTI) {
         if (threadIdx.x < 64)
@@ -74,6 +85,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : kSaveThreads) save_kernel(const
         __syncthreads();
     }
     const int first = threadIdx.x / lanes;
+    const auto there = [&](int u) { return max(0, min(kPack, dim - u * kPack)); };
     dependents_wait();
     dependents_launch();
     for (long long base = (long long)blockIdx.x * groups; base < a.rows;
@@ -81,44 +93,70 @@ __global__ void __launch_bounds__(MULTI ? 1024 : kSaveThreads) save_kernel(const
         // every lane takes part in the sums, some in vain: they read the last row
         const long long r = MULTI ? base : min(base + first, a.rows - 1);
         const bool on = MULTI || base + first < a.rows;
-        float v[K][8];
-        Sums<1> s{{0.0f}};
+        uint32_t w[K][kPackWords<T>];
+        const T *const p = x + r * dim;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int u = li + k * lanes;
-            load8<T, VEC>(x + r * a.dim + (long long)u * kPack, in_pack(a.dim, u), v[k]);
+        for (int k = 0; k < K; ++k)
+            load_words<T, WHOLE>(p + (li + k * lanes) * kPack, there(li + k * lanes), x, x_end,
+                                 w[k]);
+        Pair sum = pair_of(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s.v[0] += v[k][j];
-        }
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum = add(sum, pair_in<T>(w[k], j));
+        Sums<1> s{{sum_of(sum)}};
         const float mu = quotient(group_sum<MULTI, 1>(s, group).v[0], n, inverse);
-        s.v[0] = 0.0f;
+        const Pair minus = pair_of(-mu, -mu);
+        sum = pair_of(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int there = in_pack(a.dim, li + k * lanes);
+            const int c = there(li + k * lanes);
+            if (c == kPack) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = j < there ? v[k][j] - mu : 0.0f;
-                s.v[0] = fmaf(d, d, s.v[0]);
+                for (int j = 0; j < 4; ++j) {
+                    const Pair d = add(pair_in<T>(w[k], j), minus);
+                    sum = fma(d, d, sum);
+                }
+            } else if (!WHOLE && c > 0) {
+                float t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float d = j < c ? element<T>(w[k], j) - mu : 0.0f;
+                    t = fmaf(d, d, t);
+                }
+                sum = add(sum, pair_of(t, 0.0f));
             }
         }
+        s.v[0] = sum_of(sum);
         const float rs = rsqrtf(quotient(group_sum<MULTI, 1>(s, group).v[0], n, inverse) + a.eps);
+        const Pair scale = pair_of(rs, rs);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int u = li + k * lanes, there = in_pack(a.dim, u);
-            const int E = block_exponent(half_warp_max(top_bits(v[k])));
-            if (!on || u >= packs)
-                continue;
-            store_codes(a.codes + (r * packs + u) * kPack, encode8(v[k], E));
-            if (u % kBlockPacks == 0)
-                a.exps[r * nb + u / kBlockPacks] = exponent_byte(E);
-            float g[8], b[8];
-            weights8<W, VEC>(gamma, (long long)u * kPack, there, 1.0f, g);
-            weights8<W, VEC>(beta, (long long)u * kPack, there, 0.0f, b);
+            const int u = li + k * lanes, c = there(u);
+            if (MULTI && k * lanes >= packs) // (of all lanes)
+                break;
+            float v[8], g[8], b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[k][j] = fmaf((v[k][j] - mu) * rs, g[j], b[j]);
-            store8<T, VEC>(y + r * a.dim + (long long)u * kPack, there, v[k]);
+                v[j] = element<T>(w[k], j);
+            const uint32_t top = half_warp_max(top_bits(v));
+            if (on && u < packs) {
+                store_codes(a.codes + (r * packs + u) * kPack, encode8(v, top));
+                if (u % kBlockPacks == 0)
+                    a.exps[r * nb + u / kBlockPacks] = exponent_byte(block_exponent(top));
+            }
+            weights8<W, WHOLE>(gamma, u * kPack, c, 1.0f, g);
+            weights8<W, WHOLE>(beta, u * kPack, c, 0.0f, b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Pair q = fma(mul(add(pair_of(v[2 * j], v[2 * j + 1]), minus), scale),
+                                   pair_of(g[2 * j], g[2 * j + 1]), pair_of(b[2 * j], b[2 * j + 1]));
+                halves(q, v[2 * j], v[2 * j + 1]);
+            }
+            uint32_t o[kPackWords<T>];
+            to_words<T>(v, o);
+            store_words<T, WHOLE>(y + r * dim + u * kPack, c, there(u + 1), on, min(lanes, 32), o);
         }
         if (on && li == 0) {
             a.mean[r] = mu;
@@ -159,12 +197,12 @@ __global__ void __launch_bounds__(kLongThreads) save_long_kernel(const Save a)
             const int there = in_pack(a.dim, u);
             float v[8], g[8], b[8];
             load8<T, false>(p + u * kPack, there, v);
-            const int E = block_exponent(half_warp_max(top_bits(v)));
+            const uint32_t top = half_warp_max(top_bits(v));
             if (u >= packs)
                 continue;
-            store_codes(a.codes + (r * packs + u) * kPack, encode8(v, E));
+            store_codes(a.codes + (r * packs + u) * kPack, encode8(v, top));
             if (u % kBlockPacks == 0)
-                a.exps[r * nb + u / kBlockPacks] = exponent_byte(E);
+                a.exps[r * nb + u / kBlockPacks] = exponent_byte(block_exponent(top));
             weights8<W, false>(gamma, u * kPack, there, 1.0f, g);
             weights8<W, false>(beta, u * kPack, there, 0.0f, b);
 #pragma unroll
@@ -196,14 +234,19 @@ template <typename T, typename W, bool VEC> cudaError_t save_rows(Save a, cudaSt
     a.g = save_group(packs, few ? 1 : kSaveHeld);
     if (a.g.warps > 1) {
         const int threads = 32 * a.g.warps;
-        return launch_chained(save_kernel<T, W, kSaveHeld, true, VEC>,
-                              dim3(grid_of(a.rows, 2048 / threads)), threads, st, a);
+        const dim3 grid(grid_of(a.rows, 2048 / threads));
+        return threads <= kSaveThreads
+                   ? launch_chained(save_kernel<T, W, kSaveHeld, true, VEC, kSaveThreads>, grid,
+                                    threads, st, a)
+                   : launch_chained(save_kernel<T, W, kSaveHeld, true, VEC, 1024>, grid, threads,
+                                    st, a);
     }
     const int per_block = kSaveThreads / a.g.lanes();
     const unsigned grid = grid_of((a.rows + per_block - 1) / per_block, 16);
-    return few ? launch_chained(save_kernel<T, W, 1, false, VEC>, dim3(grid), kSaveThreads, st, a)
-               : launch_chained(save_kernel<T, W, kSaveHeld, false, VEC>, dim3(grid), kSaveThreads,
-                                st, a);
+    return few ? launch_chained(save_kernel<T, W, 1, false, VEC, kSaveThreads>, dim3(grid),
+                                kSaveThreads, st, a)
+               : launch_chained(save_kernel<T, W, kSaveHeld, false, VEC, kSaveThreads>, dim3(grid),
+                                kSaveThreads, st, a);
 }
 
 // Is every pack of 8 elements of these rows, and of the weights, whole and on
@@ -234,34 +277,87 @@ struct Restore {
     const void *gamma, *beta;
     long long rows, dim;
     void *y;
-    int lanes; // of a row
+    int lanes; // of a row's stretch of columns
 };
 
 constexpr int kRestoreThreads = 256;
+constexpr int kRestorePacks = 2, kRestoreRows = 2; // of a thread at a time
+constexpr int kRestoreCols = kRestoreThreads * kRestorePacks * kPack; // of a block, blockIdx.y each
 
-template <typename T, typename W, bool VEC>
+// A thread keeps its columns' weights in registers over all of its rows, and has the
+// codes of several rows on their way at a time.
+template <typename T, typename W, bool WHOLE>
 __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const Restore a)
 {
+    constexpr int K = kRestorePacks, R = kRestoreRows;
     const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
                                                                 static_cast<const W *>(a.beta);
-    const long long nb = blocks_of(a.dim), packs = (a.dim + kPack - 1) / kPack;
+    T *const y = static_cast<T *>(a.y);
+    const long long nb = blocks_of(a.dim), width = nb * kBlock;
     const int li = threadIdx.x % a.lanes, groups = kRestoreThreads / a.lanes;
+    const long long u0 = (long long)blockIdx.y * (kRestoreCols / kPack) + li;
+    const long long step = (long long)gridDim.x * groups, first = (long long)blockIdx.x * groups;
     dependents_wait();
     dependents_launch();
-    for (long long r = (long long)blockIdx.x * groups + threadIdx.x / a.lanes; r < a.rows;
-         r += (long long)gridDim.x * groups) {
-        const float mu = a.mean ? a.mean[r] : 0.0f, rs = a.rstd ? a.rstd[r] : 1.0f;
-        for (long long u = li; u < packs; u += a.lanes) {
-            const int there = in_pack(a.dim, u);
-            float v[8], g[8], b[8];
-            decode8(load_codes(a.codes + (r * nb * kBlockPacks + u) * kPack),
-                    a.exps[r * nb + u / kBlockPacks], v);
-            weights8<W, VEC>(gamma, u * kPack, there, 1.0f, g);
-            weights8<W, VEC>(beta, u * kPack, there, 0.0f, b);
+    int there[K], next[K];
+    Pair g[K][4], b[K][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = fmaf((v[j] - mu) * rs, g[j], b[j]);
-            store8<T, VEC>(static_cast<T *>(a.y) + r * a.dim + u * kPack, there, v);
+    for (int k = 0; k < K; ++k) {
+        const long long u = u0 + k * a.lanes;
+        there[k] = in_pack(a.dim, u);
+        next[k] = in_pack(a.dim, u + 1);
+        float t[8];
+        weights8<W, WHOLE>(gamma, u * kPack, there[k], 1.0f, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            g[k][j] = pair_of(t[2 * j], t[2 * j + 1]);
+        weights8<W, WHOLE>(beta, u * kPack, there[k], 0.0f, t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[k][j] = pair_of(t[2 * j], t[2 * j + 1]);
+    }
+    // the rows of a block's groups go on together: whole warps store
+    for (long long base = first; base < a.rows; base += R * step) {
+        Codes8 c[R][K];
+        int8_t e[R][K];
+        float mu[R], rs[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const long long r = base + i * step + threadIdx.x / a.lanes;
+            const bool on = r < a.rows;
+            mu[i] = on && a.mean ? a.mean[r] : 0.0f;
+            rs[i] = on && a.rstd ? a.rstd[r] : 1.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const long long u = u0 + k * a.lanes;
+                c[i][k] = {{0u, 0u}};
+                e[i][k] = 0;
+                if (on && there[k] > 0) {
+                    c[i][k] = load_codes(a.codes + r * width + u * kPack);
+                    e[i][k] = a.exps[r * nb + u / kBlockPacks];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const long long r = base + i * step + threadIdx.x / a.lanes;
+            const Pair minus = pair_of(-mu[i], -mu[i]), scale = pair_of(rs[i], rs[i]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float2 f[4];
+                fractions8(c[i][k], f);
+                const float s = block_scale(e[i][k]);
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    halves(fma(mul(fma(pair_of(f[j].x, f[j].y), pair_of(s, s), minus), scale),
+                               g[k][j], b[k][j]),
+                           v[2 * j], v[2 * j + 1]);
+                uint32_t o[kPackWords<T>];
+                to_words<T>(v, o);
+                store_words<T, WHOLE>(y + r * a.dim + (u0 + k * a.lanes) * kPack, there[k], next[k],
+                                      r < a.rows, min(a.lanes, 32), o);
+            }
         }
     }
 }
@@ -269,10 +365,14 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const Restore 
 template <typename T, typename W> rra_status restore(Restore a, cudaStream_t st)
 {
     a.lanes = 1;
-    while (a.lanes < kRestoreThreads && a.lanes * kPack < a.dim)
+    while (a.lanes < kRestoreThreads && a.lanes * kRestorePacks * kPack < a.dim)
         a.lanes *= 2;
     const int groups = kRestoreThreads / a.lanes;
-    const dim3 grid(grid_of((a.rows + groups - 1) / groups, 8));
+    const long long cols = (a.dim + kRestoreCols - 1) / kRestoreCols;
+    const long long blocks = std::max(1LL, num_sms() * 8LL / cols);
+    if (cols > 65535) // (rows of 2^28 elements and more)
+        return RRA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)std::min((a.rows + groups - 1) / groups, blocks), (unsigned)cols);
     return launched(whole_packs<T>(a.dim, {a.y, a.gamma, a.beta})
                         ? launch_chained(restore_kernel<T, W, true>, grid, kRestoreThreads, st, a)
                         : launch_chained(restore_kernel<T, W, false>, grid, kRestoreThreads, st,
@@ -291,8 +391,269 @@ struct SavedGrad {
     int accumulate;
     float *part; // [parts][2][dim]
     int parts;
-    long long stretch; // rows of a partial row
+    long long stretch; // long rows: rows of a partial row
+    Group g;
 };
+
+// A row's packs in the registers and shared memory of a group of lanes, as in
+// norm_grad_kernel: a lane keeps its columns' sums of dgamma and dbeta over all rows
+// of its group in registers, the packs of the next row are on their way to shared
+// memory while a row is worked on, each lane's to slots of its own, and every block
+// leaves one partial row of the sums, which join_kernel adds.  A pack of dy that does
+// not begin on a 16-byte boundary comes with the chunks that it touches.
+constexpr int kGradHeld = 4; // packs of a lane
+constexpr int kGradThreads = 384, kGradWide = 512;
+constexpr int kGradSums = 2 * 2 * 32; // floats of a group for its rows' sums
+constexpr int kMostBarriers = 15;     // of groups: a block has 16, __syncthreads takes one
+constexpr int kGradStages = 2;
+
+// 16-byte chunks that a pack's slot has.
+template <typename T, bool WHOLE>
+constexpr int kChunks = (int)sizeof(T) / 2 + (WHOLE ? 0 : 1);
+
+__device__ __forceinline__ void stage16(void *to, const void *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+}
+
+template <typename T, typename W, bool MULTI, int THREADS, bool WHOLE>
+__global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad a)
+{
+    constexpr int K = kGradHeld, C = kChunks<T, WHOLE>, N = kPackWords<T>;
+    // gamma as fp32, the groups' sums, the stages; after the last row: the
+    // holders' [2][width]
+    extern __shared__ __align__(16) float smem[];
+    const T *const dy = static_cast<const T *>(a.dy), *const dy_end = dy + a.rows * a.dim;
+    T *const dx = static_cast<T *>(a.dx);
+    const W *const gamma = static_cast<const W *>(a.gamma);
+    const int lanes = a.g.lanes(), li = threadIdx.x % lanes, group = threadIdx.x / lanes,
+              groups = blockDim.x / lanes;
+    const int dim = (int)a.dim, nb = (int)blocks_of(dim), packs = (dim + kPack - 1) / kPack,
+              width = packs * kPack;
+    const long long step = (long long)gridDim.x * groups;
+    const float n = (float)dim, inverse = 1.0f / n;
+    float *const weights = smem, *const sums = weights + width;
+    GroupOf mine = group_of(a.g, sums + group * kGradSums, 1 + group);
+    unsigned char *const stages =
+        reinterpret_cast<unsigned char *>(sums + (MULTI ? groups * kGradSums : 0));
+    // a stage: chunk c of every thread's k-th pack, then every thread's k-th codes
+    constexpr int kRow = THREADS * 16, kCodes = K * C * kRow, kStage = kCodes + K * THREADS * 8;
+    unsigned char *const slots = stages + threadIdx.x * 16;
+    unsigned char *const codes = stages + kCodes + threadIdx.x * 8;
+    const auto there = [&](int u) { return max(0, min(kPack, dim - u * kPack)); };
+    dependents_wait();
+
+    const auto stage_row = [&](int stage, long long r) {
+        unsigned char *const to = slots + stage * kStage;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = li + k * lanes, in = r < a.rows ? there(u) : 0;
+            if (in == 0)
+                continue;
+            const T *const p = dy + r * dim + u * kPack;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                             smem_u32(codes + stage * kStage + k * THREADS * 8)),
+                         "l"(a.codes + (r * nb * kBlockPacks + u) * kPack)
+                         : "memory");
+            if (WHOLE) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    stage16(to + (k * C + c) * kRow, reinterpret_cast<const uint4 *>(p) + c);
+                continue;
+            }
+            const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+            const uint4 *const from =
+                reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
+            if (in == kPack && reinterpret_cast<const T *>(from) >= dy &&
+                reinterpret_cast<const T *>(from + C) <= dy_end) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    stage16(to + (k * C + c) * kRow, from + c);
+            } else { // an end of the row or the array: what is there, zeros behind it
+                for (int j = 0; j < kPack; ++j) {
+                    const int at = m + j * (int)sizeof(T);
+                    *reinterpret_cast<T *>(to + (k * C + at / 16) * kRow + at % 16) =
+                        j < in ? p[j] : from_f32<T>(0.0f);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    Pair dg[K][4], db[K][4];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dg[k][j] = db[k][j] = pair_of(0.0f, 0.0f);
+    long long r = (long long)blockIdx.x * groups + group;
+    int stage = 0;
+    stage_row(0, r);
+    float next_mu = 0.0f, next_rs = 0.0f;
+    int8_t next_e[K] = {};
+    const auto next_row = [&](long long q) {
+        if (q >= a.rows)
+            return;
+        next_mu = a.mean[q];
+        next_rs = a.rstd[q];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (li + k * lanes < packs)
+                next_e[k] = a.exps[q * nb + (li + k * lanes) / kBlockPacks];
+    };
+    next_row(r);
+    for (int i = threadIdx.x; i < width; i += blockDim.x)
+        weights[i] = i >= dim ? 0.0f : gamma ? to_f32(gamma[i]) : 1.0f;
+    if (MULTI)
+        for (int i = threadIdx.x; i < groups * kGradSums; i += blockDim.x)
+            sums[i] = 0.0f;
+    __syncthreads();
+    // a group of several warps has barriers of its own: it ends with its last
+    // row; the groups of a warp go on together
+    const long long end = MULTI ? a.rows : a.rows + (group - (group & -(32 / lanes)));
+    for (; r < end; r += step) {
+        const bool on = MULTI || r < a.rows;
+        stage_row(stage ^ 1, r + step);
+        const int now = stage;
+        stage ^= 1;
+        const float rs = next_rs;
+        const Pair minus = pair_of(-next_mu, -next_mu), scale = pair_of(rs, rs);
+        float s_e[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            s_e[k] = block_scale(next_e[k]);
+        next_row(r + step);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        // dy and xh of the k-th pack, out of its slot
+        const auto take = [&](int k, Pair (&d)[4], Pair (&xh)[4]) {
+            const unsigned char *const at = slots + now * kStage;
+            const int u = li + k * lanes;
+            uint32_t w[N];
+            if (WHOLE) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(at + (k * C + c) * kRow);
+                    w[4 * c] = q.x, w[4 * c + 1] = q.y, w[4 * c + 2] = q.z, w[4 * c + 3] = q.w;
+                }
+            } else {
+                uint32_t in[N + 4];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(at + (k * C + c) * kRow);
+                    in[4 * c] = q.x, in[4 * c + 1] = q.y, in[4 * c + 2] = q.z, in[4 * c + 3] = q.w;
+                }
+                shift_bytes(in, (int)(reinterpret_cast<uintptr_t>(dy + r * dim + u * kPack) & 15),
+                            w);
+            }
+            const Codes8 q = load_codes(
+                reinterpret_cast<const int8_t *>(codes + now * kStage + k * THREADS * 8));
+            float2 f[4];
+            fractions8(q, f);
+            const Pair s = pair_of(s_e[k], s_e[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[j] = pair_in<T>(w, j);
+                xh[j] = mul(fma(pair_of(f[j].x, f[j].y), s, minus), scale);
+            }
+        };
+        const auto weight = [&](int k, Pair (&g)[4]) {
+            const float4 *const p =
+                reinterpret_cast<const float4 *>(weights + (li + k * lanes) * kPack);
+            const float4 lo = p[0], hi = p[1];
+            g[0] = pair_of(lo.x, lo.y), g[1] = pair_of(lo.z, lo.w);
+            g[2] = pair_of(hi.x, hi.y), g[3] = pair_of(hi.z, hi.w);
+        };
+        Pair s0 = pair_of(0.0f, 0.0f), s1 = s0;
+        if (on) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (li + k * lanes >= packs)
+                    continue;
+                Pair d[4], xh[4], g[4];
+                take(k, d, xh);
+                weight(k, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Pair w = mul(d[j], g[j]);
+                    s0 = add(s0, w);
+                    s1 = fma(w, xh[j], s1);
+                    dg[k][j] = fma(d[j], xh[j], dg[k][j]);
+                    db[k][j] = add(db[k][j], d[j]);
+                }
+            }
+        }
+        if (!dx)
+            continue;
+        Sums<2> s{{sum_of(s0), sum_of(s1)}};
+        s = group_sum<MULTI, 2>(s, mine);
+        // dx = rs w - rs mean(w) - xh rs mean(w xh)
+        const float t0 = -rs * quotient(s.v[0], n, inverse), t1 = -rs * quotient(s.v[1], n, inverse);
+        const Pair m0 = pair_of(t0, t0), m1 = pair_of(t1, t1);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = li + k * lanes;
+            uint32_t o[N] = {};
+            if (on && u < packs) {
+                Pair d[4], xh[4], g[4];
+                float v[8];
+                take(k, d, xh);
+                weight(k, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    halves(fma(xh[j], m1, fma(mul(d[j], g[j]), scale, m0)), v[2 * j], v[2 * j + 1]);
+                to_words<T>(v, o);
+            }
+            store_words<T, WHOLE>(dx + r * dim + u * kPack, there(u), there(u + 1), on,
+                                  min(lanes, 32), o);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    dependents_launch();
+    if (!a.dgamma && !a.dbeta)
+        return;
+
+    float *const out = a.part + 2LL * blockIdx.x * a.dim;
+    float fg[K][8], fb[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            halves(dg[k][j], fg[k][2 * j], fg[k][2 * j + 1]);
+            halves(db[k][j], fb[k][2 * j], fb[k][2 * j + 1]);
+        }
+    if constexpr (!MULTI) { // the warp's groups first
+        for (int o = lanes; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    fg[k][j] += __shfl_xor_sync(kFull, fg[k][j], o);
+                    fb[k][j] += __shfl_xor_sync(kFull, fb[k][j], o);
+                }
+    }
+    const int holders = MULTI ? groups : blockDim.x / 32, me = MULTI ? group : threadIdx.x / 32;
+    const bool holds = MULTI || threadIdx.x % 32 < lanes;
+    __syncthreads(); // (gamma and the stages are done with)
+    float *const own = smem + me * 2 * width;
+    if (holds)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (li + k * lanes < packs) {
+                store_values<float, 8>(own + (li + k * lanes) * kPack, fg[k]);
+                store_values<float, 8>(own + width + (li + k * lanes) * kPack, fb[k]);
+            }
+    __syncthreads();
+    for (int c = threadIdx.x; c < dim; c += blockDim.x) {
+        float g = 0.0f, b = 0.0f;
+        for (int h = 0; h < holders; ++h) {
+            g += smem[h * 2 * width + c];
+            b += smem[(h * 2 + 1) * width + c];
+        }
+        out[c] = g;
+        out[dim + c] = b;
+    }
+}
 
 // xh of pack u of row r.
 __device__ __forceinline__ void normal8(const SavedGrad &a, long long r, long long u, float mu,
@@ -306,7 +667,7 @@ __device__ __forceinline__ void normal8(const SavedGrad &a, long long r, long lo
         xh[j] = (xh[j] - mu) * rs;
 }
 
-// dx by two passes over a row, the second from L2.
+// Rows that no block holds: dx by two passes over a row, the second from L2.
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) saved_dx_kernel(const SavedGrad a)
 {
@@ -378,25 +739,90 @@ __global__ void __launch_bounds__(kThreads) saved_weights_kernel(const SavedGrad
 }
 
 template <typename T, typename W, bool VEC>
-cudaError_t saved_grad_rows(const SavedGrad &a, cudaStream_t st)
+cudaError_t saved_grad_long(const SavedGrad &a, cudaStream_t st)
 {
-    if (a.rows > 0 && (a.dgamma || a.dbeta)) {
+    if (a.dgamma || a.dbeta) {
         const unsigned cols = (unsigned)std::min((a.dim / kPack + kThreads) / kThreads, 1LL << 16);
         saved_weights_kernel<T, VEC><<<dim3(cols, a.parts), kThreads, 0, st>>>(a);
     }
-    if (a.rows > 0 && a.dx) // last: dx may be dy
+    if (a.dx) // last: dx may be dy
         saved_dx_kernel<T, W, VEC><<<grid_of(a.rows, 8), kThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && (a.dgamma || a.dbeta))
-        e = join_parts<W>(Join{a.part, a.parts, a.dim, a.dgamma, a.dbeta, a.accumulate}, false,
-                          st);
-    return e;
+    return cudaGetLastError();
+}
+
+// Launch shape of the gradient, from which its scratch follows.
+struct GradShape {
+    Group g;
+    int groups;  // of a block
+    int parts;   // partial rows
+    int threads; // kGradThreads, kGradWide, or 0: rows that no block holds
+    bool whole;
+};
+
+template <typename T> GradShape grad_shape(const SavedGrad &a)
+{
+    GradShape s;
+    s.whole = whole_packs<T>(a.dim, {a.dy, a.dx, a.gamma});
+    const long long packs = (a.dim + kPack - 1) / kPack;
+    s.threads = packs <= kGradThreads * kGradHeld ? kGradThreads
+                // (fp32 rows off 16-byte boundaries: 512 threads' slots are too many)
+                : packs <= kGradWide * kGradHeld && (s.whole || sizeof(T) == 2) ? kGradWide
+                                                                                : 0;
+    if (!s.threads) {
+        const long long stretch = std::max(16LL, (a.rows + 127) / 128);
+        s.groups = 1;
+        s.parts = (int)((a.rows + stretch - 1) / stretch);
+        return s;
+    }
+    s.g = group_for(packs, kGradHeld);
+    // one block per SM; groups of a block only where rows are many
+    const long long most = std::min(std::max(1, s.threads / s.g.lanes()),
+                                    s.g.warps > 1 ? kMostBarriers : s.threads);
+    s.groups = (int)std::max(1LL, std::min(most, a.rows / num_sms()));
+    if (s.g.warps == 1) { // whole warps
+        const int in_warp = 32 / s.g.lanes();
+        s.groups = std::max(1, s.groups / in_warp) * in_warp;
+    }
+    s.parts = (int)std::min((a.rows + s.groups - 1) / s.groups, (long long)num_sms());
+    return s;
+}
+
+template <typename T, typename W, bool MULTI, int THREADS, bool WHOLE>
+cudaError_t saved_grad_held(const SavedGrad &a, const GradShape &s, cudaStream_t st)
+{
+    // the slots of a whole block, whatever its size: their distance is a constant
+    const size_t stages =
+                     (size_t)kGradStages * kGradHeld * (kChunks<T, WHOLE> * 16 + 8) * THREADS,
+                 sums = MULTI ? sizeof(float) * kGradSums * s.groups : 0,
+                 weights = sizeof(float) * ((a.dim + kPack - 1) / kPack * kPack);
+    // at the end: the sums of every holder (a group, or a warp of groups)
+    const int holders = MULTI ? s.groups : s.groups * s.g.lanes() / 32;
+    const int smem = (int)std::max(weights + sums + stages, 2 * weights * holders);
+    const auto fn = saved_grad_kernel<T, W, MULTI, THREADS, WHOLE>;
+    const cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess)
+        return e;
+    return launch_chained_smem(fn, dim3(s.parts), s.groups * s.g.lanes(), smem, st, a);
+}
+
+template <typename T, typename W, bool WHOLE>
+cudaError_t saved_grad_rows(const SavedGrad &a, const GradShape &s, cudaStream_t st)
+{
+    if (s.threads == kGradThreads)
+        return s.g.warps > 1 ? saved_grad_held<T, W, true, kGradThreads, WHOLE>(a, s, st)
+                             : saved_grad_held<T, W, false, kGradThreads, WHOLE>(a, s, st);
+    if constexpr (WHOLE || sizeof(T) == 2)
+        if (s.threads == kGradWide)
+            return saved_grad_held<T, W, true, kGradWide, WHOLE>(a, s, st);
+    return saved_grad_long<T, W, WHOLE>(a, st);
 }
 
 template <typename T, typename W> rra_status saved_grad(SavedGrad a, cudaStream_t st)
 {
+    const GradShape s = grad_shape<T>(a);
+    a.g = s.g;
+    a.parts = s.parts;
     a.stretch = std::max(16LL, (a.rows + 127) / 128);
-    a.parts = (int)((a.rows + a.stretch - 1) / a.stretch);
     std::unique_lock<std::mutex> lk;
     if (a.dgamma || a.dbeta) {
         unsigned char *ws = nullptr;
@@ -406,9 +832,13 @@ template <typename T, typename W> rra_status saved_grad(SavedGrad a, cudaStream_
             return r;
         a.part = reinterpret_cast<float *>(ws + kScratchHead);
     }
-    return launched(whole_packs<T>(a.dim, {a.dy, a.dx, a.gamma})
-                        ? saved_grad_rows<T, W, true>(a, st)
-                        : saved_grad_rows<T, W, false>(a, st));
+    cudaError_t e = cudaSuccess;
+    if (a.rows > 0)
+        e = s.whole ? saved_grad_rows<T, W, true>(a, s, st) : saved_grad_rows<T, W, false>(a, s, st);
+    if (e == cudaSuccess && (a.dgamma || a.dbeta))
+        e = join_parts<W>(Join{a.part, a.parts, a.dim, a.dgamma, a.dbeta, a.accumulate},
+                          a.rows > 0 && s.threads, st);
+    return launched(e);
 }
 
 // ---------------------------------------------------------------- calls
@@ -555,6 +985,6 @@ extern "C" rra_status rra_layer_norm_saved_grad(const void *dy, const int8_t *ex
     if (weight_t != dtype && weight_t != RRA_F32)
         return RRA_ERR_UNSUPPORTED;
     const SavedGrad a{dy, exps,   codes, gamma,      mean,    rstd, (long long)rows, (long long)dim,
-                      dx, dgamma, dbeta, accumulate, nullptr, 0,    0};
+                      dx, dgamma, dbeta, accumulate, nullptr, 0,    0,  {}};
     return by_types<SavedGradCall>(dtype, weight_t, a, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -35,63 +35,83 @@ __device__ __forceinline__ int block_exponent(uint32_t top_bits)
 }
 __device__ __forceinline__ int8_t exponent_byte(int E) { return (int8_t)(E - 127); }
 
-// Codes of 8 values in a block of biased exponent E (two's complement).  As in
-// BfpGroup: t = fma(v, 2^(6-e), 1.5 2^23 + 128) holds m + 128 in its low byte.
-__device__ __forceinline__ Codes8 encode8(const float v[8], int E)
+// Codes of 8 values in a block whose largest magnitude has these bits (two's
+// complement).  As in BfpGroup: t = fma(v, 2^(6-e), 1.5 2^23 + 128) holds m + 128 in
+// its low byte.
+__device__ __forceinline__ Codes8 encode8(const float v[8], uint32_t top)
 {
     constexpr float kEnc = kMagic + 128.0f;
+    const int E = block_exponent(top);
     if (E == 255)
         return {{0u, 0u}};
     // 2^(6-e), a normal float unless E < 6: such blocks are first scaled by 2^64
-    int sb = 260 - E;
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        x[j] = v[j];
+    const float s = __int_as_float((E < 6 ? 196 - E : 260 - E) << 23);
+    const float2 s2 = make_float2(s, s), c2 = make_float2(kEnc, kEnc);
+    float2 t[4];
     if (E < 6) {
-        sb -= 64;
+        const float2 up = make_float2(1.8446744073709552e19f, 1.8446744073709552e19f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = __fmul_rn(x[j], 1.8446744073709552e19f);
+        for (int j = 0; j < 4; ++j)
+            t[j] = __ffma2_rn(__fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), up), s2, c2);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            t[j] = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), s2, c2);
     }
-    const float s = __int_as_float(sb << 23);
-    uint32_t u[8];
+    // m is at most 128, and above 127 only where the block's largest value is 127.5
+    // of 128 or more (a subnormal one, which is none, may look like it)
+    if ((top & 0x7fffffu) >= 0x7f0000u) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float2 t = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(s, s),
-                                    make_float2(kEnc, kEnc));
-        // m is at most 128 before it is clamped: 2^(6-e) max|v| < 128
-        u[j] = __float_as_uint(fminf(fmaxf(t.x, kEnc - 127.0f), kEnc + 127.0f));
-        u[j + 1] = __float_as_uint(fminf(fmaxf(t.y, kEnc - 127.0f), kEnc + 127.0f));
+        for (int j = 0; j < 4; ++j) {
+            t[j].x = fminf(fmaxf(t[j].x, kEnc - 127.0f), kEnc + 127.0f);
+            t[j].y = fminf(fmaxf(t[j].y, kEnc - 127.0f), kEnc + 127.0f);
+        }
     }
     Codes8 c;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        c.w[h] = __byte_perm(__byte_perm(u[4 * h], u[4 * h + 1], 0x0040),
-                             __byte_perm(u[4 * h + 2], u[4 * h + 3], 0x0040), 0x5410) ^
+    for (int h = 0; h < 2; ++h) {
+        const float2 a = t[2 * h], b = t[2 * h + 1];
+        c.w[h] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                             __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040),
+                             0x5410) ^
                  0x80808080u;
+    }
     return c;
+}
+
+// 2^e of a block's exponent byte (an infinity for a block that is not finite).
+__device__ __forceinline__ float block_scale(int8_t e)
+{
+    return __uint_as_float(((uint32_t)(e + 127) & 255u) << 23);
+}
+
+// m / 64 of 8 codes, exactly; a value is that times the block's scale.
+__device__ __forceinline__ void fractions8(const Codes8 &c, float2 f[4])
+{
+    constexpr float kOff = -(kMagic + 128.0f) / 64.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = c.w[h] ^ 0x80808080u; // m + 128
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            f[2 * h + j] = __ffma2_rn(
+                make_float2(__uint_as_float(__byte_perm(x, kMagicBits, 0x7640 + 2 * j)),
+                            __uint_as_float(__byte_perm(x, kMagicBits, 0x7641 + 2 * j))),
+                make_float2(1.0f / 64, 1.0f / 64), make_float2(kOff, kOff));
+    }
 }
 
 // The 8 values of codes whose block's exponent byte is e.
 __device__ __forceinline__ void decode8(const Codes8 &c, int8_t e, float v[8])
 {
-    constexpr float kOff = -(kMagic + 128.0f) / 64.0f;
-    const float s = __uint_as_float(((uint32_t)(e + 127) & 255u) << 23);
+    float2 f[4];
+    fractions8(c, f);
+    const float s = block_scale(e);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t x = c.w[h] ^ 0x80808080u; // m + 128
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            const float2 f = make_float2(__uint_as_float(__byte_perm(x, kMagicBits, 0x7640 + j)),
-                                         __uint_as_float(__byte_perm(x, kMagicBits, 0x7641 + j)));
-            // m 2^-6, exactly; times 2^e
-            const float2 r = __fmul2_rn(
-                __ffma2_rn(f, make_float2(1.0f / 64, 1.0f / 64), make_float2(kOff, kOff)),
-                make_float2(s, s));
-            v[4 * h + j] = r.x;
-            v[4 * h + j + 1] = r.y;
-        }
+    for (int j = 0; j < 4; ++j) {
+        const float2 r = __fmul2_rn(f[j], make_float2(s, s));
+        v[2 * j] = r.x;
+        v[2 * j + 1] = r.y;
     }
 }
 
