@@ -21,7 +21,8 @@ LIB = os.path.join(LIBDIR, "librra.so")
 
 SOURCES = ["rra_host.cu", "ring_none.cu", "ring_bfp8.cu", "ring_bfp4.cu", "ring_bfp8_ef.cu", "ring_bfp4_ef.cu", "ring_sparse.cu", "ring_sparse_chunk.cu", "coll_kernels.cu",
            "codec_kernels.cu", "noalloc.cu", "op_scratch.cu", "grad_norm.cu", "embedding.cu", "layer_norm.cu",
-           "layer_norm_saved.cu", "gated_ff.cu", "gated_gemm.cu"]
+           "layer_norm_saved.cu", "gated_ff.cu", "gated_gemm.cu",
+           "gated_rows.cu"]
 HEADERS = ["rra_device.cuh", "rra_kernels.h", "bfp_group.cuh", "ring_kernel.cuh", "wire_sparse.cuh",
            "op_common.cuh", "row_group.cuh", "saved.cuh", "ragged.cuh", "gated_act.cuh", "gated_ff.h", "tc.cuh",
            "token_sort.cuh", "stream_slot.h"]

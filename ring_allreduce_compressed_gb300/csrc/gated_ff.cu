@@ -10,167 +10,11 @@
 
 #include "gated_act.cuh"
 #include "op_common.cuh"
+#include "ragged.cuh"
 #include "saved.cuh"
 
 namespace rra {
 namespace {
-
-// ---------------------------------------------------------------- products without tensor cores
-
-// out[m, n] = sum over k of a(m, k) b(k, n), over one or two pairs of operands
-// (their sums added), or two outputs of one a.  An operand is read along k or along
-// its rows, whichever is next to each other in memory.
-//
-// A block makes 32 x 128 results, a warp 4 rows of 128 (one block of codes), a
-// lane 4 x 4 of each; the operands come in slices of 16 along k.
-constexpr int kTileM = 32, kTileN = 128, kTileK = 16, kTileThreads = 256;
-
-struct Operand {
-    const void *p;
-    long long ld;
-};
-
-// A slice of R rows of an operand, [k][row], as fp32.  ALONG: k is next to each other.
-template <typename T, int R, bool ALONG>
-__device__ __forceinline__ void load_slice(float (&to)[kTileK][R + 4], const Operand &o,
-                                           long long row0, long long rows, long long k0,
-                                           long long depth)
-{
-    const T *const p = static_cast<const T *>(o.p);
-#pragma unroll
-    for (int i = threadIdx.x; i < R * kTileK; i += kTileThreads) {
-        const int k = ALONG ? i % kTileK : i / R, r = ALONG ? i / kTileK : i % R;
-        const bool there = row0 + r < rows && k0 + k < depth;
-        to[k][r] = there ? to_f32(ALONG ? p[(row0 + r) * o.ld + k0 + k] : p[(k0 + k) * o.ld + row0 + r])
-                         : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void add_products(const float (&a)[kTileK][kTileM + 4],
-                                             const float (&b)[kTileK][kTileN + 4],
-                                             float (&acc)[4][4])
-{
-    const int m = threadIdx.x / 32 * 4, n = threadIdx.x % 32 * 4;
-#pragma unroll
-    for (int k = 0; k < kTileK; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = fmaf(a[k][m + i], b[k][n + j], acc[i][j]);
-}
-
-// Gate or up: the values, or their codes.
-template <typename T>
-__device__ __forceinline__ void keep_row(const Kept &to, long long r, long long c0, long long ff,
-                                         const float v[4])
-{
-    const int c = threadIdx.x % 32 * 4;
-    if (to.exps) { // every lane of the warp is here
-        uint32_t top = 0;
-        float w[8] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[j] = c0 + c + j < ff ? v[j] : 0.0f;
-            top = max(top, __float_as_uint(w[j]) & 0x7fffffffu);
-        }
-        top = __reduce_max_sync(kFull, top);
-        const Codes8 q = encode8(w, top);
-        const long long nb = blocks_of(ff), b = c0 / kBlock;
-        *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(to.data) + (r * nb + b) * kBlock + c) =
-            q.w[0];
-        if (c == 0)
-            to.exps[r * nb + b] = exponent_byte(block_exponent(top));
-    } else if (to.data) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c0 + c + j < ff)
-                static_cast<T *>(to.data)[r * ff + c0 + c + j] = from_f32<T>(v[j]);
-    }
-}
-
-template <typename T> __global__ void __launch_bounds__(kTileThreads) ff_plain_kernel(const FfArgs a)
-{
-    __shared__ float sx[kTileK][kTileM + 4], sg[kTileK][kTileN + 4], su[kTileK][kTileN + 4];
-    dependents_wait();
-    dependents_launch();
-    const long long tn = (a.ff + kTileN - 1) / kTileN, tm = (a.rows + kTileM - 1) / kTileM;
-    for (long long t = blockIdx.x; t < tn * tm; t += gridDim.x) {
-        const long long m0 = t / tn * kTileM, n0 = t % tn * kTileN;
-        float g[4][4] = {}, u[4][4] = {};
-        for (long long k0 = 0; k0 < a.dim; k0 += kTileK) {
-            __syncthreads();
-            load_slice<T, kTileM, true>(sx, {a.x, a.dim}, m0, a.rows, k0, a.dim);
-            load_slice<T, kTileN, true>(sg, {a.wg, a.dim}, n0, a.ff, k0, a.dim);
-            load_slice<T, kTileN, true>(su, {a.wu, a.dim}, n0, a.ff, k0, a.dim);
-            __syncthreads();
-            add_products(sx, sg, g);
-            add_products(sx, su, u);
-        }
-        constexpr bool exact = sizeof(T) == 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long r = m0 + threadIdx.x / 32 * 4 + i, c = n0 + threadIdx.x % 32 * 4;
-            if (r >= a.rows) // (all of a warp or none)
-                continue;
-            keep_row<T>(a.gate, r, n0, a.ff, g[i]);
-            keep_row<T>(a.up, r, n0, a.ff, u[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + j < a.ff)
-                    static_cast<T *>(a.h)[r * a.ff + c + j] =
-                        from_f32<T>(act_value<exact>(a.act, g[i][j]) * u[i][j]);
-        }
-    }
-}
-
-// out (rows x cols) = a1 b1 (+ a2 b2), or += where it accumulates.
-struct Product {
-    Operand a[2], b[2];
-    int pairs;
-    long long rows, cols, depth;
-    void *out;
-    int accumulate;
-};
-
-// AK, BK: is a, b next to each other along k?
-template <typename T, typename O, bool AK, bool BK>
-__global__ void __launch_bounds__(kTileThreads) product_kernel(const Product p)
-{
-    __shared__ float sa[kTileK][kTileM + 4], sb[kTileK][kTileN + 4];
-    const long long tn = (p.cols + kTileN - 1) / kTileN, tm = (p.rows + kTileM - 1) / kTileM;
-    for (long long t = blockIdx.x; t < tn * tm; t += gridDim.x) {
-        const long long m0 = t / tn * kTileM, n0 = t % tn * kTileN;
-        float acc[4][4] = {};
-        for (int i = 0; i < p.pairs; ++i)
-            for (long long k0 = 0; k0 < p.depth; k0 += kTileK) {
-                __syncthreads();
-                load_slice<T, kTileM, AK>(sa, p.a[i], m0, p.rows, k0, p.depth);
-                load_slice<T, kTileN, BK>(sb, p.b[i], n0, p.cols, k0, p.depth);
-                __syncthreads();
-                add_products(sa, sb, acc);
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long r = m0 + threadIdx.x / 32 * 4 + i, c = n0 + threadIdx.x % 32 * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r < p.rows && c + j < p.cols) {
-                    O *const to = static_cast<O *>(p.out) + r * p.cols + c + j;
-                    *to = from_f32<O>(p.accumulate ? to_f32(*to) + acc[i][j] : acc[i][j]);
-                }
-        }
-    }
-}
-
-template <typename T, typename O, bool AK, bool BK>
-cudaError_t product(const Product &p, cudaStream_t st)
-{
-    const long long tiles = (p.cols + kTileN - 1) / kTileN * ((p.rows + kTileM - 1) / kTileM);
-    product_kernel<T, O, AK, BK>
-        <<<(unsigned)std::min(tiles, 1LL << 20), kTileThreads, 0, st>>>(p);
-    return cudaGetLastError();
-}
 
 // ---------------------------------------------------------------- elementwise part of the gradient
 
@@ -178,7 +22,7 @@ constexpr int kActThreads = 256;
 
 // Packs of 8 elements of a row; SAVED: gate and up in 8 bits.  Every element is read
 // before it is written, so outputs may take inputs' places.
-template <typename T, bool SAVED, bool VEC>
+template <typename T, bool SAVED, bool VEC, int ACT>
 __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs a, int lanes)
 {
     constexpr bool exact = sizeof(T) == 4;
@@ -207,7 +51,7 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float slope;
-                const float value = act_both<exact>(a.act, g[j], &slope);
+                const float value = act_both<ACT, exact>(g[j], &slope);
                 dg[j] = d[j] * v[j] * slope;
                 h[j] = value * v[j];
                 d[j] *= value;
@@ -232,18 +76,26 @@ template <typename T> cudaError_t act_grad(const FfGradArgs &a, cudaStream_t st)
     const int groups = kActThreads / lanes;
     const dim3 grid((unsigned)std::max(
         1LL, std::min((a.rows + groups - 1) / groups, (long long)num_sms() * 8)));
-    const auto fn = a.gate.exps ? (vec ? act_grad_kernel<T, true, true> : act_grad_kernel<T, true, false>)
-                                : (vec ? act_grad_kernel<T, false, true>
-                                       : act_grad_kernel<T, false, false>);
-    return launch_chained(fn, grid, kActThreads, st, a, lanes);
+    return host_by_act(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        const auto fn = a.gate.exps ? (vec ? act_grad_kernel<T, true, true, ACT>
+                                           : act_grad_kernel<T, true, false, ACT>)
+                                    : (vec ? act_grad_kernel<T, false, true, ACT>
+                                           : act_grad_kernel<T, false, false, ACT>);
+        return launch_chained(fn, grid, kActThreads, st, a, lanes);
+    });
 }
 
 // ---------------------------------------------------------------- operands for tensor maps
 
-// A matrix whose rows do not begin on 16-byte boundaries, copied to rows that do.
+// A matrix whose rows do not begin on 16-byte boundaries, copied to rows that do; one
+// of fp32 numbers cut into three planes of bf16, 8 bits of each number in the first,
+// the next 8 in the second and the rest in the third.  (Cut, not rounded: the three
+// add up to the number exactly, and none is larger.)
 template <typename T>
-__global__ void __launch_bounds__(kActThreads) align_kernel(const T *from, T *to, long long rows,
-                                                            long long cols, long long ld)
+__global__ void __launch_bounds__(kActThreads) operand_kernel(const T *from, uint32_t *to,
+                                                              long long rows, long long cols,
+                                                              long long ld)
 {
     const long long packs = ld / kPack, total = rows * packs;
     dependents_wait();
@@ -251,52 +103,80 @@ __global__ void __launch_bounds__(kActThreads) align_kernel(const T *from, T *to
     for (long long i = (long long)blockIdx.x * kActThreads + threadIdx.x; i < total;
          i += (long long)gridDim.x * kActThreads) {
         const long long r = i / packs, c = (i - r * packs) * kPack;
-        const int there = (int)min((long long)kPack, cols - c);
-        Pack<T, kPack> v;
+        uint32_t w[kPackWords<T>];
+        load_words<T, false>(from + r * cols + c, (int)min((long long)kPack, cols - c), from,
+                             from + rows * cols, w);
+        uint4 *const at = reinterpret_cast<uint4 *>(to) + i;
+        if constexpr (sizeof(T) == 2) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            uint32_t q[3][4];
 #pragma unroll
-        for (int j = 0; j < kPack; ++j)
-            v.e[j] = j < there ? from[r * cols + c + j] : from_f32<T>(0.0f);
-        store_pack<T, kPack>(to + r * ld + c, v);
+            for (int j = 0; j < 8; ++j) {
+                float v = __uint_as_float(w[j]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+                    q[p][j / 2] = j % 2 ? q[p][j / 2] | top : top >> 16;
+                    // (what is not finite is all in the first plane; a NaN of the low bits
+                    // alone keeps being one)
+                    const float rest = v - __uint_as_float(top);
+                    if (p == 0 && (w[j] & 0x7f800000u) == 0x7f800000u) {
+                        if (w[j] & 0x007fffffu)
+                            q[0][j / 2] |= j % 2 ? 0x00400000u : 0x00000040u;
+                        v = 0.0f;
+                    } else {
+                        v = rest;
+                    }
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                at[p * total] = make_uint4(q[p][0], q[p][1], q[p][2], q[p][3]);
+        }
     }
 }
 
-// Operands as tensor maps can read them: where they are, or in the stream's scratch.
-template <typename T, int N> class Aligned {
+// Operands as tensor maps can read them: where they are, or in the stream's scratch,
+// where the products' own parts are, too.
+template <typename T, int N> class Operands {
 public:
     Matrix16 m[N];
+    unsigned char *scratch = nullptr;
+    size_t parts_at = 0;
 
-    // Plans copies of those that need one; their places follow from take().
-    explicit Aligned(const Matrix16 (&given)[N])
+    explicit Operands(const Matrix16 (&given)[N])
     {
+        size_t at = kScratchHead;
         for (int i = 0; i < N; ++i) {
             m[i] = given[i];
-            copy_[i] = m[i].p && m[i].rows > 0 && !gemm_takes(m[i]);
+            m[i].planes = sizeof(T) == 4 ? 3 : 1;
+            copy_[i] = m[i].p && (sizeof(T) == 4 || !gemm_takes(m[i]));
             if (copy_[i]) {
                 m[i].ld = (m[i].cols + kPack - 1) / kPack * kPack;
-                at_[i] = bytes_;
-                bytes_ += (size_t)m[i].rows * m[i].ld * sizeof(T) + 255 & ~(size_t)255;
+                at_[i] = at;
+                at += ((size_t)m[i].planes * m[i].rows * m[i].ld * 2 + 255) & ~(size_t)255;
             }
         }
+        parts_at = at;
     }
-    size_t bytes() const { return bytes_; }
-    rra_status take(cudaStream_t st)
+    rra_status take(size_t parts, cudaStream_t st)
     {
-        if (!bytes_)
+        if (parts_at + parts == kScratchHead)
             return RRA_OK;
-        const rra_status r = op_scratch(st, kScratchHead + bytes_, lk_, &ws_);
-        return r;
+        return op_scratch(st, parts_at + parts, lk_, &scratch);
     }
     // Copies operand i, once what it holds is there.
     cudaError_t fill(int i, cudaStream_t st)
     {
         if (!copy_[i])
             return cudaSuccess;
-        T *const to = reinterpret_cast<T *>(ws_ + kScratchHead + at_[i]);
+        uint32_t *const to = reinterpret_cast<uint32_t *>(scratch + at_[i]);
         const long long packs = m[i].rows * (m[i].ld / kPack);
         const unsigned grid = (unsigned)std::min((packs + kActThreads - 1) / kActThreads,
                                                  (long long)num_sms() * 32);
         const cudaError_t e =
-            launch_chained(align_kernel<T>, dim3(grid), kActThreads, st,
+            launch_chained(operand_kernel<T>, dim3(grid), kActThreads, st,
                            static_cast<const T *>(m[i].p), to, m[i].rows, m[i].cols, m[i].ld);
         m[i].p = to;
         return e;
@@ -304,8 +184,7 @@ public:
 
 private:
     bool copy_[N];
-    size_t at_[N], bytes_ = 0;
-    unsigned char *ws_ = nullptr;
+    size_t at_[N];
     std::unique_lock<std::mutex> lk_; // until the call's launches are queued
 };
 
@@ -321,89 +200,56 @@ rra_status stalled_status()
     if (!*w)
         return RRA_OK;
     *w = 0;
+    op_scratch_spoilt();
     return RRA_ERR_TIMEOUT;
 }
 
-template <typename T> rra_status ff_tensor(const FfArgs &a, cudaStream_t st)
+template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
 {
+    if (few_rows<T>(a))
+        return rows_forward<T>(a, st);
     rra_status s = stalled_status();
     if (s != RRA_OK)
         return s;
-    Aligned<T, 3> in({{a.x, a.rows, a.dim, a.dim}, {a.wg, a.ff, a.dim, a.dim},
-                      {a.wu, a.ff, a.dim, a.dim}});
-    if ((s = in.take(st)) != RRA_OK)
+    Operands<T, 3> in({{a.x, a.rows, a.dim, a.dim, 1},
+                       {a.wg, a.ff, a.dim, a.dim, 1},
+                       {a.wu, a.ff, a.dim, a.dim, 1}});
+    if ((s = in.take(gemm_parts(a, sizeof(T) == 4), st)) != RRA_OK)
         return s;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i)
         e = in.fill(i, st);
-    return launched(e == cudaSuccess ? gemm_forward<T>(a, in.m[0], in.m[1], in.m[2], st) : e);
+    return launched(e == cudaSuccess ? gemm_forward<T>(a, in.m, in.scratch, in.parts_at, st) : e);
 }
 
-template <typename T, typename O> rra_status ff_grad_tensor(const FfGradArgs &a, cudaStream_t st)
+template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaStream_t st)
 {
+    const bool weights = a.dwg || a.dwu;
+    if (a.rows == 0) { // sums over nothing
+        cudaError_t e = cudaSuccess;
+        for (void *out : {a.dwg, a.dwu})
+            if (e == cudaSuccess && out && !a.accumulate)
+                e = cudaMemsetAsync(out, 0, (size_t)a.ff * a.dim * sizeof(O), st);
+        return launched(e);
+    }
     rra_status s = stalled_status();
     if (s != RRA_OK)
         return s;
-    const bool weights = a.dwg || a.dwu;
-    Aligned<T, 5> in({{a.dgate, a.rows, a.ff, a.ff},
-                      {a.dup, a.rows, a.ff, a.ff},
-                      {a.dx ? a.wg : nullptr, a.ff, a.dim, a.dim},
-                      {a.dx ? a.wu : nullptr, a.ff, a.dim, a.dim},
-                      {weights ? a.x : nullptr, a.rows, a.dim, a.dim}});
-    if (!a.dx && !weights)
-        return launched(act_grad<T>(a, st));
-    if ((s = in.take(st)) != RRA_OK)
+    const bool products = a.dx || weights;
+    Operands<T, 5> in({{products ? a.dgate : nullptr, a.rows, a.ff, a.ff, 1},
+                       {products ? a.dup : nullptr, a.rows, a.ff, a.ff, 1},
+                       {a.dx ? a.wg : nullptr, a.ff, a.dim, a.dim, 1},
+                       {a.dx ? a.wu : nullptr, a.ff, a.dim, a.dim, 1},
+                       {weights ? a.x : nullptr, a.rows, a.dim, a.dim, 1}});
+    if (products && (s = in.take(gemm_parts(a, sizeof(T) == 4), st)) != RRA_OK)
         return s;
     cudaError_t e = act_grad<T>(a, st);
     for (int i = 0; i < 5 && e == cudaSuccess; ++i)
         e = in.fill(i, st);
     if (e == cudaSuccess && a.dx)
-        e = gemm_dx<T>(a, in.m[0], in.m[1], in.m[2], in.m[3], st);
+        e = gemm_dx<T>(a, in.m, in.scratch, in.parts_at, st);
     if (e == cudaSuccess && weights)
-        e = gemm_dw<T, O>(a, in.m[0], in.m[1], in.m[4], st);
-    return launched(e);
-}
-
-template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
-{
-    if constexpr (sizeof(T) == 2)
-        return ff_tensor<T>(a, st);
-    const long long tiles = (a.ff + kTileN - 1) / kTileN * ((a.rows + kTileM - 1) / kTileM);
-    return launched(launch_chained(ff_plain_kernel<T>, dim3((unsigned)std::min(tiles, 1LL << 20)),
-                                   kTileThreads, st, a));
-}
-
-template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaStream_t st)
-{
-    if constexpr (sizeof(T) == 2)
-        if (a.rows > 0)
-            return ff_grad_tensor<T, O>(a, st);
-    cudaError_t e = a.rows > 0 ? act_grad<T>(a, st) : cudaSuccess;
-    if (e == cudaSuccess && a.dx && a.rows > 0) {
-        const Product p{{{a.dgate, a.ff}, {a.dup, a.ff}},
-                        {{a.wg, a.dim}, {a.wu, a.dim}},
-                        2,
-                        a.rows,
-                        a.dim,
-                        a.ff,
-                        a.dx,
-                        0};
-        e = product<T, T, true, false>(p, st);
-    }
-    for (int i = 0; i < 2; ++i) {
-        void *const out = i == 0 ? a.dwg : a.dwu;
-        if (e != cudaSuccess || !out || (a.rows == 0 && a.accumulate))
-            continue;
-        const Product p{{{i == 0 ? a.dgate : a.dup, a.ff}},
-                        {{a.x, a.dim}},
-                        1,
-                        a.ff,
-                        a.dim,
-                        a.rows,
-                        out,
-                        a.accumulate};
-        e = product<T, O, false, false>(p, st);
-    }
+        e = gemm_dw<T, O>(a, in.m, in.scratch, in.parts_at, st);
     return launched(e);
 }
 

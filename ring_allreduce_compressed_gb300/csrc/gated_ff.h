@@ -32,25 +32,35 @@ struct FfGradArgs {
     int accumulate;
 };
 
-// A matrix of 16-bit elements, next to each other along its columns.
+// A matrix of 16-bit elements, next to each other along its columns; fp32 ones as three
+// planes of bf16, one behind the other.
 struct Matrix16 {
     const void *p;
     long long rows, cols, ld;
+    int planes;
 };
 
 // Can tensor maps read it?  (16-byte aligned rows)
 bool gemm_takes(const Matrix16 &x);
 
 // The products on the tensor cores (gated_gemm.cu); operands as gemm_takes has them.
+// in: x, w_gate, w_up; dgate, dup, w_gate, w_up, x.  gemm_parts: bytes that a call
+// needs `parts_at` bytes from the stream's scratch on.
+size_t gemm_parts(const FfArgs &a, bool f32);
+size_t gemm_parts(const FfGradArgs &a, bool f32);
 template <typename T>
-cudaError_t gemm_forward(const FfArgs &a, const Matrix16 &x, const Matrix16 &wg,
-                         const Matrix16 &wu, cudaStream_t st);
+cudaError_t gemm_forward(const FfArgs &a, const Matrix16 (&in)[3], unsigned char *scratch,
+                         size_t parts_at, cudaStream_t st);
 template <typename T>
-cudaError_t gemm_dx(const FfGradArgs &a, const Matrix16 &dgate, const Matrix16 &dup,
-                    const Matrix16 &wg, const Matrix16 &wu, cudaStream_t st);
+cudaError_t gemm_dx(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
+                    size_t parts_at, cudaStream_t st);
 template <typename T, typename O>
-cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 &dgate, const Matrix16 &dup,
-                    const Matrix16 &x, cudaStream_t st);
+cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
+                    size_t parts_at, cudaStream_t st);
+
+// Few rows (gated_rows.cu): is the call one of those, and its kernel.
+template <typename T> bool few_rows(const FfArgs &a);
+template <typename T> rra_status rows_forward(const FfArgs &a, cudaStream_t st);
 
 // Host word that a kernel sets when a wait of its has run out of time.
 cudaError_t stalled_word(unsigned **word);

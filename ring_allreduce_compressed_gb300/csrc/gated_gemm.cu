@@ -1,5 +1,4 @@
-// gated_gemm.cu -- the products of the gated feed-forward block on the tensor cores
-// (16-bit types).
+// gated_gemm.cu -- the products of the gated feed-forward block on the tensor cores.
 //
 // A pair of blocks makes 256 x 256 results at a time: each block has 128 of the rows
 // and half of the other operand's 256 columns in its shared memory, and one
@@ -23,8 +22,21 @@ constexpr int kSlice = 64;      // elements of k: 128 bytes
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kHalf * kSlice * 2, kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = kSlice * kSlice * 2; // 64 rows for 64 elements of k
-constexpr int kGemmThreads = 192; // copies, instructions, four warps that write
+constexpr int kWriters = 8;                    // warps that write results
+constexpr int kGemmThreads = 64 + 32 * kWriters; // copies, instructions, and those
 constexpr int kGroup = 8;         // tiles along m that share their columns' slices in L2
+
+// fp32 operands come as three planes of bf16, each the next 8 bits of a number, which
+// add up to it exactly.  Of the nine products of planes the six largest count (what is
+// left out is below 2^-21 of a product, 2^-24 in the mean), the small ones first.  Sums
+// in tensor memory are cut off at each step of 16 along k, not rounded: half a unit
+// of the last place a step, always towards zero (measured: 4.8e-7 of the result after
+// 512 elements of k, 4.4e-6 after 4096).  For fp32 results they are therefore taken out
+// after kRun slices and added up there.
+constexpr int kRun = 4;
+template <bool F32> constexpr int kProducts = F32 ? 6 : 1;
+__device__ __forceinline__ int plane_a(int q) { return q == 0 ? 2 : q == 2 || q == 3 ? 1 : 0; }
+__device__ __forceinline__ int plane_b(int q) { return q == 1 ? 2 : q == 2 || q == 4 ? 1 : 0; }
 
 // What the products are:
 //  kForward: columns 0..127 are gate, 128..255 up, of the same 128 of ff.
@@ -39,12 +51,15 @@ struct Gemm {
     CUtensorMap a[2], b[2];
     int tiles_m, tiles_n, tiles; // tiles: of all outputs
     int slices;                  // of one pair of operands
+    int splits, per_split;       // parts of the slices, each an item of work; slices of one
     long long m, n;              // of an output
     int act;
     void *out[2]; // h; dx; dw_gate, dw_up
     Kept gate, up;
     int accumulate;
-    int first_out; // kDw: the output of the first tiles
+    int first_out;      // kDw: the output of the first tiles
+    float *parts;       // more than one split: [tile][split][block of the pair][64][128][4]
+    unsigned *arrivals; // [tile][block of the pair], zero before and after
     unsigned *stalled;
 };
 
@@ -68,6 +83,25 @@ template <int MODE> __device__ __forceinline__ TilePlace tile_place(const Gemm &
     return p;
 }
 
+// An item of work: a tile and a stretch of its slices.
+struct Item {
+    int tile, split, lo, hi;
+};
+
+template <int MODE> __device__ __forceinline__ Item item_of(const Gemm &g, int i)
+{
+    const int all = MODE == kDx ? 2 * g.slices : g.slices;
+    Item t;
+    t.split = i / g.tiles;
+    t.tile = i - t.split * g.tiles;
+    t.lo = t.split * g.per_split;
+    t.hi = min(t.lo + g.per_split, all);
+    return t;
+}
+
+// Slices whose sums stay in tensor memory.
+template <bool F32> __device__ __forceinline__ int run_of(const Item &t) { return F32 ? kRun : t.hi - t.lo; }
+
 // Eight values next to each other, of which `there` are in the row.
 template <typename T>
 __device__ __forceinline__ void put8(T *p, int there, bool whole, const float v[8])
@@ -78,19 +112,32 @@ __device__ __forceinline__ void put8(T *p, int there, bool whole, const float v[
         store8<T, false>(p, there, v);
 }
 
-__device__ __forceinline__ void floats(const uint32_t (&r)[32], int i, float v[8])
+template <int N>
+__device__ __forceinline__ void floats(const uint32_t (&r)[N], int i, float v[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         v[j] = __uint_as_float(r[i + j]);
 }
 
-// Largest magnitude's bits of 128 columns of this lane's row.
+// ---------------------------------------------------------------- writers
+
+// Writer w has the lanes (rows) 32 (w % 4) .. of tensor memory and one half of the
+// columns (in kForward, of gate's and of up's).  kForward's halves of a row meet in
+// shared memory where a block of 128 codes needs its largest magnitude.
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], summed[2], written[2];
+    uint32_t tmem, stop, last;
+    uint32_t top[2][2][kHalf]; // gate, up; half; row
+};
+
+// Largest magnitude's bits of 64 columns of this lane's row.
 __device__ __forceinline__ uint32_t row_top(uint32_t at)
 {
     uint32_t top = 0;
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
+    for (int c = 0; c < 64; c += 32) {
         uint32_t r[32];
         tmem_load(at + c, r);
         tmem_loaded();
@@ -103,8 +150,8 @@ __device__ __forceinline__ uint32_t row_top(uint32_t at)
 
 // One of gate and up, 8 columns from c on of row r.
 template <typename T>
-__device__ __forceinline__ void keep8(const Kept &to, uint32_t top, long long r, long long c, long long ff,
-                                      bool whole, const float v[8])
+__device__ __forceinline__ void keep8(const Kept &to, uint32_t top, long long r, long long c,
+                                      long long ff, bool whole, const float v[8])
 {
     if (to.exps) {
         const long long nb = blocks_of(ff);
@@ -114,40 +161,47 @@ __device__ __forceinline__ void keep8(const Kept &to, uint32_t top, long long r,
     }
 }
 
-// Rows of a pair's results from tensor memory to where they go: this lane's row r.
-template <typename T>
-__device__ __forceinline__ void write_forward(const Gemm &g, uint32_t at, long long r, long long n0,
-                                              bool whole)
+// Gate and up of this lane's row r, 64 columns from n0 + 64 half on, to where they go.
+template <typename T, int ACT>
+__device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, int half, int quarter,
+                                              uint32_t at, long long r, long long n0, bool whole)
 {
-    uint32_t eg = 0, eu = 0; // bits of the blocks' largest magnitudes
-    if (g.gate.exps)
-        eg = row_top(at);
-    if (g.up.exps)
-        eu = row_top(at + kHalf);
     const bool on = r < g.m;
-    const long long nb = blocks_of(g.n);
-    if (on && g.gate.exps)
-        g.gate.exps[r * nb + n0 / kBlock] = exponent_byte(block_exponent(eg));
-    if (on && g.up.exps)
-        g.up.exps[r * nb + n0 / kBlock] = exponent_byte(block_exponent(eu));
-    for (int c = 0; c < kHalf; c += 32) {
-        uint32_t rg[32], ru[32];
+    uint32_t top[2] = {0, 0}; // bits of the blocks' largest magnitudes
+    if (g.gate.exps || g.up.exps) {
+        const int row = quarter * 32 + threadIdx.x % 32;
+        s.top[0][half][row] = row_top(at + half * 64);
+        s.top[1][half][row] = row_top(at + kHalf + half * 64);
+        named_barrier(2 + quarter, 64);
+        const long long nb = blocks_of(g.n), b = r * nb + n0 / kBlock;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            top[i] = max(s.top[i][0][row], s.top[i][1][row]);
+            int8_t *const exps = i == 0 ? g.gate.exps : g.up.exps;
+            if (on && half == 0 && exps)
+                exps[b] = exponent_byte(block_exponent(top[i]));
+        }
+        named_barrier(2 + quarter, 64); // (read before the next ones are written)
+    }
+#pragma unroll 1
+    for (int c = half * 64; c < half * 64 + 64; c += 16) {
+        uint32_t rg[16], ru[16];
         tmem_load(at + c, rg);
         tmem_load(at + kHalf + c, ru);
         tmem_loaded();
         if (!on)
             continue;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 16; i += 8) {
             float vg[8], vu[8], h[8];
             floats(rg, i, vg);
             floats(ru, i, vu);
             const long long col = n0 + c + i;
-            keep8<T>(g.gate, eg, r, col, g.n, whole, vg);
-            keep8<T>(g.up, eu, r, col, g.n, whole, vu);
+            keep8<T>(g.gate, top[0], r, col, g.n, whole, vg);
+            keep8<T>(g.up, top[1], r, col, g.n, whole, vu);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                h[j] = act_value<false>(g.act, vg[j]) * vu[j];
+                h[j] = act_value<ACT, sizeof(T) == 4>(vg[j]) * vu[j];
             put8(static_cast<T *>(g.out[0]) + r * g.n + col, (int)max(0LL, min(8LL, g.n - col)),
                  whole, h);
         }
@@ -155,11 +209,12 @@ __device__ __forceinline__ void write_forward(const Gemm &g, uint32_t at, long l
 }
 
 template <typename O>
-__device__ __forceinline__ void write_plain(const Gemm &g, O *out, uint32_t at, long long r,
-                                            long long n0, bool whole)
+__device__ __forceinline__ void write_plain(const Gemm &g, O *out, int half, uint32_t at,
+                                            long long r, long long n0, bool whole)
 {
     const bool on = r < g.m;
-    for (int c = 0; c < kSide; c += 32) {
+#pragma unroll 1
+    for (int c = half * kHalf; c < half * kHalf + kHalf; c += 32) {
         uint32_t v[32];
         tmem_load(at + c, v);
         tmem_loaded();
@@ -187,24 +242,101 @@ __device__ __forceinline__ void write_plain(const Gemm &g, O *out, uint32_t at, 
     }
 }
 
-struct Shared {
-    uint64_t full[kStages], empty[kStages], summed[2], written[2];
-    uint32_t tmem, stop;
-};
+// to (+)= the sums at `from`, a warp's 128 columns from `first` on.
+__device__ __forceinline__ void take_sums(uint32_t from, uint32_t to, int first, bool add)
+{
+#pragma unroll 1
+    for (int c = first; c < first + kHalf; c += 32) {
+        uint32_t v[32];
+        tmem_load(from + c, v);
+        if (add) {
+            uint32_t w[32];
+            tmem_load(to + c, w);
+            tmem_loaded();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+        } else {
+            tmem_loaded();
+        }
+        tmem_store(to + c, v);
+    }
+    tmem_stored();
+}
 
+// This item's sums to memory.  In the block that is the last of its tile's splits to
+// get here: all of them added, in the order of the splits, back in tensor memory, and
+// true.  Lane by lane of row `row` and 128 columns from `first` on.
+__device__ __forceinline__ bool join_splits(const Gemm &g, Shared &s, const Item &t, uint32_t rank,
+                                            uint32_t at, int row, int first)
+{
+    constexpr long long kPart = (long long)kHalf * kSide; // floats of a block
+    float *const tile = g.parts + ((long long)t.tile * g.splits * 2 + rank) * kPart;
+    float4 *const mine = reinterpret_cast<float4 *>(tile + t.split * 2 * kPart);
+#pragma unroll 1
+    for (int c = first; c < first + kHalf; c += 32) {
+        uint32_t v[32];
+        tmem_load(at + c, v);
+        tmem_loaded();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+            mine[(c + j) / 4 * kHalf + row] =
+                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                            __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+    }
+    __threadfence();
+    named_barrier(1, 32 * kWriters);
+    unsigned *const count = g.arrivals + t.tile * 2 + rank;
+    if (threadIdx.x == 64) {
+        s.last = atomicAdd(count, 1u) == (unsigned)g.splits - 1;
+        if (s.last)
+            *count = 0;
+    }
+    named_barrier(1, 32 * kWriters);
+    const bool last = s.last;
+    named_barrier(1, 32 * kWriters); // (read before the next item's)
+    if (!last)
+        return false;
+    __threadfence();
+#pragma unroll 1
+    for (int c = first; c < first + kHalf; c += 32) {
+        uint32_t v[32];
+        float sum[32] = {};
+#pragma unroll 1
+        for (int k = 0; k < g.splits; ++k) {
+            const float4 *const p = reinterpret_cast<const float4 *>(tile + k * 2 * kPart);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 q = __ldcg(p + (c + j) / 4 * kHalf + row);
+                sum[j] += q.x, sum[j + 1] += q.y, sum[j + 2] += q.z, sum[j + 3] += q.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(sum[j]);
+        tmem_store(at + c, v);
+    }
+    tmem_stored();
+    return true;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// T: the type of the call's elements; O: of the outputs.
 template <typename T, typename O, int MODE>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
 {
+    constexpr bool F32 = sizeof(T) == 4;
     constexpr bool A_ROWS = MODE == kDw, B_ROWS = MODE != kForward;
     constexpr uint32_t kKind =
-        mma_kind(std::is_same<T, __nv_bfloat16>::value, A_ROWS, B_ROWS, kSide, kSide);
+        mma_kind(!std::is_same<T, __half>::value, A_ROWS, B_ROWS, kSide, kSide);
     extern __shared__ unsigned char raw[];
     // swizzled boxes begin on 1024-byte boundaries
     unsigned char *const stages = raw + (1024 - smem_u32(raw) % 1024) % 1024;
     Shared &s = *reinterpret_cast<Shared *>(stages + kStages * kStageBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
-    const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int pairs = gridDim.x / 2, pair = blockIdx.x / 2, items = g.tiles * g.splits;
 
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -213,7 +345,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.summed[i], 1);
-            mbar_init(&s.written[i], 8); // warps that write, of both blocks
+            mbar_init(&s.written[i], 2 * kWriters); // of both blocks
         }
         s.stop = 0;
         mbar_fence_init();
@@ -228,7 +360,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile uint32_t *const stop = &s.stop;
-    const int slices = MODE == kDx ? 2 * g.slices : g.slices;
     dependents_wait();
     dependents_launch();
 
@@ -236,34 +367,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if (lane == 0) {
             uint32_t step = 0;
             bool ok = true;
-            for (int t = pair; ok && t < g.tiles; t += pairs) {
-                const TilePlace p = tile_place<MODE>(g, t);
+            // one slice of one product of planes
+            const auto load = [&](const TilePlace &p, int k, int pa, int pb) {
                 const int m = (int)p.m0 + (int)rank * kHalf, n = (int)p.n0 + (int)rank * kHalf;
-                for (int k = 0; k < slices; ++k, ++step) {
-                    const int i = step % kStages;
-                    // the first round finds the stages empty
-                    if (!(ok = wait_limited(&s.empty[i], (step / kStages & 1) ^ 1, stop, g.stalled)))
-                        break;
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(&s.full[i], 2 * kStageBytes);
-                    const uint32_t bar = cluster_address(&s.full[i], 0);
-                    unsigned char *const a = stages + i * kStageBytes, *const b = a + kOperandBytes;
-                    if (MODE == kForward) {
-                        load_box(a, &g.a[0], k * kSlice, m, bar);
-                        load_box(b, &g.b[rank], k * kSlice, (int)p.n0, bar);
+                const int i = step % kStages;
+                // the first round finds the stages empty
+                if (!wait_limited(&s.empty[i], (step / kStages & 1) ^ 1, stop, g.stalled))
+                    return false;
+                if (rank == 0)
+                    mbar_arrive_expect_tx(&s.full[i], 2 * kStageBytes);
+                const uint32_t bar = cluster_address(&s.full[i], 0);
+                unsigned char *const a = stages + i * kStageBytes, *const b = a + kOperandBytes;
+                if (MODE == kForward) {
+                    load_box(a, &g.a[0], k * kSlice, m, pa, bar);
+                    load_box(b, &g.b[rank], k * kSlice, (int)p.n0, pb, bar);
+                } else {
+                    const int from = MODE == kDx && k >= g.slices ? 1 : 0;
+                    const int at = (k - from * g.slices) * kSlice;
+                    if (MODE == kDx) {
+                        load_box(a, &g.a[from], at, m, pa, bar);
                     } else {
-                        const int from = MODE == kDx && k >= g.slices ? 1 : 0;
-                        const int at = (k - from * g.slices) * kSlice;
-                        if (MODE == kDx) {
-                            load_box(a, &g.a[from], at, m, bar);
-                        } else {
-                            load_box(a, &g.a[p.which], m, at, bar);
-                            load_box(a + kBoxBytes, &g.a[p.which], m + kSlice, at, bar);
-                        }
-                        load_box(b, &g.b[from], n, at, bar);
-                        load_box(b + kBoxBytes, &g.b[from], n + kSlice, at, bar);
+                        load_box(a, &g.a[p.which], m, at, pa, bar);
+                        load_box(a + kBoxBytes, &g.a[p.which], m + kSlice, at, pa, bar);
                     }
+                    load_box(b, &g.b[from], n, at, pb, bar);
+                    load_box(b + kBoxBytes, &g.b[from], n + kSlice, at, pb, bar);
                 }
+                ++step;
+                return true;
+            };
+            for (int t = pair; ok && t < items; t += pairs) {
+                const Item it = item_of<MODE>(g, t);
+                const TilePlace p = tile_place<MODE>(g, it.tile);
+                const int run = run_of<F32>(it);
+                for (int lo = it.lo; ok && lo < it.hi; lo += run)
+                    for (int q = 0; ok && q < kProducts<F32>; ++q)
+                        for (int k = lo; ok && k < min(lo + run, it.hi); ++k)
+                            ok = load(p, k, F32 ? plane_a(q) : 0, F32 ? plane_b(q) : 0);
             }
             // the other block's arrivals on this one's barriers come before it ends
             for (int i = 0; ok && i < kStages; ++i, ++step)
@@ -279,55 +419,101 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if (lane == 0 && rank == 0) {
             uint32_t step = 0, made = 0;
             bool ok = true;
-            for (int t = pair; ok && t < g.tiles; t += pairs, ++made) {
-                const uint32_t into = made % 2, at = tmem + into * kSide;
-                if (!(ok = wait_limited(&s.written[into], (made / 2 & 1) ^ 1, stop, g.stalled)))
-                    break;
-                tc_fence_after();
-                for (int k = 0; k < slices; ++k, ++step) {
-                    const int i = step % kStages;
-                    if (!(ok = wait_limited(&s.full[i], step / kStages & 1, stop, g.stalled)))
+            for (int t = pair; ok && t < items; t += pairs) {
+                const Item it = item_of<MODE>(g, t);
+                const int run = run_of<F32>(it);
+                for (int lo = it.lo; ok && lo < it.hi; lo += run, ++made) {
+                    // fp32: the second half of tensor memory holds the sums of runs
+                    const uint32_t into = F32 ? 0 : made % 2, round = F32 ? made : made / 2;
+                    const uint32_t at = tmem + into * kSide;
+                    if (!(ok = wait_limited(&s.written[into], (round & 1) ^ 1, stop, g.stalled)))
                         break;
                     tc_fence_after();
-                    const unsigned char *const pa = stages + i * kStageBytes,
-                                        *const pb = pa + kOperandBytes;
-                    const uint64_t a = A_ROWS ? operand_along_rows(pa, kBoxBytes) : operand_along_k(pa);
-                    const uint64_t b = B_ROWS ? operand_along_rows(pb, kBoxBytes) : operand_along_k(pb);
+                    const int count = kProducts<F32> * (min(lo + run, it.hi) - lo);
+                    for (int k = 0; k < count; ++k, ++step) {
+                        const int i = step % kStages;
+                        if (!(ok = wait_limited(&s.full[i], step / kStages & 1, stop, g.stalled)))
+                            break;
+                        tc_fence_after();
+                        const unsigned char *const pa = stages + i * kStageBytes,
+                                            *const pb = pa + kOperandBytes;
+                        const uint64_t a =
+                            A_ROWS ? operand_along_rows(pa, kBoxBytes) : operand_along_k(pa);
+                        const uint64_t b =
+                            B_ROWS ? operand_along_rows(pb, kBoxBytes) : operand_along_k(pb);
 #pragma unroll
-                    for (int j = 0; j < kSlice / 16; ++j)
-                        mma_pair(at, a + j * (A_ROWS ? kStepAlongRows : kStepAlongK),
-                                 b + j * (B_ROWS ? kStepAlongRows : kStepAlongK), kKind,
-                                 k > 0 || j > 0);
-                    mma_commit_pair(&s.empty[i]);
+                        for (int j = 0; j < kSlice / 16; ++j)
+                            mma_pair(at, a + j * (A_ROWS ? kStepAlongRows : kStepAlongK),
+                                     b + j * (B_ROWS ? kStepAlongRows : kStepAlongK), kKind,
+                                     k > 0 || j > 0);
+                        mma_commit_pair(&s.empty[i]);
+                    }
+                    if (ok)
+                        mma_commit_pair(&s.summed[into]);
                 }
-                if (ok)
-                    mma_commit_pair(&s.summed[into]);
             }
         }
     } else {
-        const int quarter = warp % 4; // of the lanes of tensor memory, that a warp can read
+        const int quarter = warp % 4, half = (warp - 2) / 4;
+        const uint32_t lanes = (uint32_t)quarter * 32 << 16;
         uint32_t made = 0;
-        for (int t = pair; t < g.tiles; t += pairs, ++made) {
-            const uint32_t into = made % 2;
-            const bool ok = wait_limited(&s.summed[into], made / 2 & 1, stop, g.stalled);
-            if (!__all_sync(kFull, ok))
-                break;
+        bool ok = true;
+        const auto wait_sums = [&](uint32_t into, uint32_t round) {
+            // (all writers go on or none: they meet at barriers)
+            const bool yes = named_all(1, 32 * kWriters,
+                                       wait_limited(&s.summed[into], round & 1, stop, g.stalled));
+            __syncwarp();
             tc_fence_after();
-            const TilePlace p = tile_place<MODE>(g, t);
-            const long long r = p.m0 + rank * kHalf + quarter * 32 + lane;
-            const uint32_t at = tmem + into * kSide + ((uint32_t)quarter * 32 << 16);
-            O *const out = static_cast<O *>(g.out[p.which]);
-            const bool whole = g.n % 8 == 0 && aligned_to(out, 16);
-            if (MODE == kForward)
-                write_forward<T>(g, at, r, p.n0,
-                                 whole && (g.gate.exps || aligned_to(g.gate.data, 16)) &&
-                                     (g.up.exps || aligned_to(g.up.data, 16)));
-            else
-                write_plain<O>(g, out, at, r, p.n0, whole);
+            return yes;
+        };
+        const auto release = [&](uint32_t into) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 arrive_at(cluster_address(&s.written[into], 0));
+        };
+        for (int t = pair; ok && t < items; t += pairs) {
+            const Item it = item_of<MODE>(g, t);
+            const int run = run_of<F32>(it);
+            uint32_t into = 0;
+            for (int lo = it.lo; ok && lo < it.hi; lo += run, ++made) {
+                into = F32 ? 0 : made % 2;
+                ok = wait_sums(into, F32 ? made : made / 2);
+                if (F32 && ok) {
+                    take_sums(tmem + lanes, tmem + lanes + kSide, half * kHalf, lo > it.lo);
+                    release(0);
+                }
+            }
+            if (!ok)
+                break;
+            const uint32_t at = tmem + lanes + (F32 ? kSide : into * kSide);
+            const TilePlace p = tile_place<MODE>(g, it.tile);
+            const int row = quarter * 32 + lane;
+            const long long r = p.m0 + rank * kHalf + row;
+            bool mine = true;
+            if (g.splits > 1)
+                mine = join_splits(g, s, it, rank, at, row, half * kHalf);
+            if (mine) {
+                O *const out = static_cast<O *>(g.out[p.which]);
+                const bool whole = g.n % 8 == 0 && aligned_to(out, 16);
+                if (MODE == kForward) {
+                    if (F32 || g.splits > 1) { // a half has columns that the other has stored
+                        tc_fence_before();
+                        named_barrier(2 + quarter, 64);
+                        tc_fence_after();
+                    }
+                    by_act(g.act, [&](auto act) {
+                        write_forward<T, decltype(act)::value>(
+                            g, s, half, quarter, at, r, p.n0,
+                            whole && (g.gate.exps || aligned_to(g.gate.data, 16)) &&
+                                (g.up.exps || aligned_to(g.up.data, 16)));
+                    });
+                } else {
+                    write_plain<O>(g, out, half, at, r, p.n0, whole);
+                }
+            }
+            if (!F32)
+                release(into);
         }
     }
     __syncwarp();
@@ -361,34 +547,37 @@ EncodeFn encoder()
     return fn;
 }
 
-// Boxes of 64 x box_rows elements of a matrix of 16-bit numbers; what is outside of it
-// is read as zero.
+// Boxes of 64 x box_rows elements of the planes of a matrix of 16-bit numbers; what is
+// outside of a plane is read as zero.
 bool make_map(CUtensorMap *m, bool bf16, const Matrix16 &x, int box_rows)
 {
     const EncodeFn fn = encoder();
     if (!fn)
         return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows},
-                     strides[1] = {(cuuint64_t)x.ld * 2};
-    const cuuint32_t box[2] = {kSlice, (cuuint32_t)box_rows}, steps[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+    const long long plane = x.planes > 1 ? x.rows * x.ld : x.ld;
+    const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)x.planes},
+                     strides[2] = {(cuuint64_t)x.ld * 2, (cuuint64_t)plane * 2};
+    const cuuint32_t box[3] = {kSlice, (cuuint32_t)box_rows, 1}, steps[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
               const_cast<void *>(x.p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs of blocks that the device runs at a time.
-int resident_pairs(const void *fn)
+// Pairs of blocks that the device runs at a time (the kernels' launches are alike).
+int resident_pairs()
 {
     static std::mutex mu;
     static int cached[64] = {};
+    const void *const fn = reinterpret_cast<const void *>(gemm_kernel<__half, __half, kForward>);
+    const int most = std::max(1, num_sms() / 2);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64)
-        return std::max(1, num_sms() / 2);
+        return most;
     std::lock_guard<std::mutex> lk(mu);
     if (!cached[dev]) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(num_sms() / 2 * 2);
+        cfg.gridDim = dim3(2 * most);
         cfg.blockDim = dim3(kGemmThreads);
         cfg.dynamicSmemBytes = kGemmSmem;
         cudaLaunchAttribute at[1] = {};
@@ -398,11 +587,12 @@ int resident_pairs(const void *fn)
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+        if (op_allow(fn, kGemmSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
-            n = std::max(1, num_sms() / 2);
+            n = most;
         }
-        cached[dev] = std::min(n, std::max(1, num_sms() / 2));
+        cached[dev] = std::min(n, most);
     }
     return cached[dev];
 }
@@ -416,7 +606,7 @@ template <typename T, typename O, int MODE> cudaError_t launch_gemm(Gemm &g, cud
     if ((e = stalled_word(&g.stalled)) != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * std::min(resident_pairs(reinterpret_cast<const void *>(fn)), g.tiles));
+    cfg.gridDim = dim3(2 * std::min(resident_pairs(), g.tiles * g.splits));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = kGemmSmem;
     cfg.stream = st;
@@ -431,19 +621,79 @@ template <typename T, typename O, int MODE> cudaError_t launch_gemm(Gemm &g, cud
     return cudaLaunchKernelEx(&cfg, fn, g);
 }
 
-// Tiles of all outputs; false: more than an int counts.
-bool set_tiles(Gemm &g, int outputs, long long step_n)
+// Tiles, slices and splits of a product: m x n results (of each output), `total` slices
+// for each of them, step_n columns of an output a tile.
+struct Plan {
+    bool ok; // (an int counts the tiles)
+    int tiles_m, tiles_n, tiles, splits, per_split;
+    size_t bytes; // of parts
+};
+
+// Few tiles with many slices are split along k.  The time of a launch in steps, by
+// measurement: a slice takes 0.28 us a pair, an item 3 us to write out, the last of a
+// tile's splits 3 us and 0.6 more a split to join them.
+Plan plan_of(long long m, long long n, int outputs, long long step_n, long long total, bool f32)
 {
-    const long long tm = (g.m + kSide - 1) / kSide, tn = (g.n + step_n - 1) / step_n;
-    if (tm * tn * outputs > 0x3fffffff)
-        return false;
-    g.tiles_m = (int)tm;
-    g.tiles_n = (int)tn;
-    g.tiles = (int)(tm * tn) * outputs;
-    return true;
+    Plan p = {};
+    const long long tm = (m + kSide - 1) / kSide, tn = (n + step_n - 1) / step_n;
+    if (tm * tn * outputs > 0x3fffffff || total > 0x3fffffff)
+        return p;
+    p.ok = true;
+    p.tiles_m = (int)tm;
+    p.tiles_n = (int)tn;
+    p.tiles = (int)(tm * tn) * outputs;
+    const int pairs = resident_pairs();
+    const double slice = 0.28 * (f32 ? kProducts<true> : 1);
+    double best = 0;
+    for (int s = 1; s <= 32 && (s == 1 || (2 * p.tiles <= (int)(kScratchHead / sizeof(unsigned)) &&
+                                           p.tiles * s <= pairs));
+         ++s) {
+        const int per = (int)((total + s - 1) / s);
+        if (s > 1 && (per < 4 || (long long)per * (s - 1) >= total))
+            continue;
+        const double t = (double)((p.tiles * s + pairs - 1) / pairs) * (per * slice + 3) +
+                         (s > 1 ? 3 + 0.6 * s : 0);
+        if (s == 1 || t < best) {
+            best = t;
+            p.splits = s;
+            p.per_split = per;
+        }
+    }
+    if (p.splits > 1)
+        p.bytes = (size_t)p.tiles * p.splits * 2 * kHalf * kSide * sizeof(float);
+    return p;
 }
 
-int slices_of(long long k) { return (int)((k + kSlice - 1) / kSlice); }
+long long slices_of(long long k) { return (k + kSlice - 1) / kSlice; }
+
+Plan plan_forward(const FfArgs &a, bool f32)
+{
+    return plan_of(a.rows, a.ff, 1, kHalf, slices_of(a.dim), f32);
+}
+Plan plan_dx(const FfGradArgs &a, bool f32)
+{
+    return plan_of(a.rows, a.dim, 1, kSide, 2 * slices_of(a.ff), f32);
+}
+Plan plan_dw(const FfGradArgs &a, bool f32)
+{
+    return plan_of(a.ff, a.dim, a.dwg && a.dwu ? 2 : 1, kSide, slices_of(a.rows), f32);
+}
+
+// g's tiles by the plan; scratch: the stream's, parts behind its head.
+bool use_plan(Gemm &g, const Plan &p, long long slices, unsigned char *scratch, size_t parts_at)
+{
+    g.tiles_m = p.tiles_m;
+    g.tiles_n = p.tiles_n;
+    g.tiles = p.tiles;
+    g.slices = (int)slices;
+    g.splits = p.splits;
+    g.per_split = p.per_split;
+    if (p.splits > 1) {
+        g.arrivals = reinterpret_cast<unsigned *>(scratch);
+        g.parts = reinterpret_cast<float *>(scratch + parts_at);
+    }
+    return p.ok;
+}
 
 } // namespace
 
@@ -474,10 +724,19 @@ bool gemm_takes(const Matrix16 &x)
     return aligned_to(x.p, 16) && x.ld % 8 == 0 && x.ld <= (1LL << 38);
 }
 
-template <typename T> cudaError_t gemm_forward(const FfArgs &a, const Matrix16 &x, const Matrix16 &wg,
-                                               const Matrix16 &wu, cudaStream_t st)
+size_t gemm_parts(const FfArgs &a, bool f32) { return plan_forward(a, f32).bytes; }
+
+size_t gemm_parts(const FfGradArgs &a, bool f32)
 {
-    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    return std::max(a.dx ? plan_dx(a, f32).bytes : 0,
+                    a.dwg || a.dwu ? plan_dw(a, f32).bytes : 0);
+}
+
+template <typename T>
+cudaError_t gemm_forward(const FfArgs &a, const Matrix16 (&in)[3], unsigned char *scratch,
+                         size_t parts_at, cudaStream_t st)
+{
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.rows;
     g.n = a.ff;
@@ -485,35 +744,34 @@ template <typename T> cudaError_t gemm_forward(const FfArgs &a, const Matrix16 &
     g.out[0] = a.h;
     g.gate = a.gate;
     g.up = a.up;
-    g.slices = slices_of(a.dim);
-    if (!set_tiles(g, 1, kHalf) || !make_map(&g.a[0], bf16, x, kHalf) ||
-        !make_map(&g.b[0], bf16, wg, kHalf) || !make_map(&g.b[1], bf16, wu, kHalf))
+    if (!use_plan(g, plan_forward(a, sizeof(T) == 4), slices_of(a.dim), scratch, parts_at) ||
+        !make_map(&g.a[0], bf16, in[0], kHalf) || !make_map(&g.b[0], bf16, in[1], kHalf) ||
+        !make_map(&g.b[1], bf16, in[2], kHalf))
         return cudaErrorInvalidValue;
     return launch_gemm<T, T, kForward>(g, st);
 }
 
 template <typename T>
-cudaError_t gemm_dx(const FfGradArgs &a, const Matrix16 &dgate, const Matrix16 &dup,
-                    const Matrix16 &wg, const Matrix16 &wu, cudaStream_t st)
+cudaError_t gemm_dx(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
+                    size_t parts_at, cudaStream_t st)
 {
-    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.rows;
     g.n = a.dim;
     g.out[0] = a.dx;
-    g.slices = slices_of(a.ff);
-    if (!set_tiles(g, 1, kSide) || !make_map(&g.a[0], bf16, dgate, kHalf) ||
-        !make_map(&g.a[1], bf16, dup, kHalf) || !make_map(&g.b[0], bf16, wg, kSlice) ||
-        !make_map(&g.b[1], bf16, wu, kSlice))
+    if (!use_plan(g, plan_dx(a, sizeof(T) == 4), slices_of(a.ff), scratch, parts_at) ||
+        !make_map(&g.a[0], bf16, in[0], kHalf) || !make_map(&g.a[1], bf16, in[1], kHalf) ||
+        !make_map(&g.b[0], bf16, in[2], kSlice) || !make_map(&g.b[1], bf16, in[3], kSlice))
         return cudaErrorInvalidValue;
     return launch_gemm<T, T, kDx>(g, st);
 }
 
 template <typename T, typename O>
-cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 &dgate, const Matrix16 &dup,
-                    const Matrix16 &x, cudaStream_t st)
+cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
+                    size_t parts_at, cudaStream_t st)
 {
-    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.ff;
     g.n = a.dim;
@@ -521,24 +779,28 @@ cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 &dgate, const Matrix16 &
     g.out[1] = a.dwu;
     g.accumulate = a.accumulate;
     g.first_out = a.dwg ? 0 : 1;
-    g.slices = slices_of(a.rows);
-    if (!set_tiles(g, a.dwg && a.dwu ? 2 : 1, kSide) || !make_map(&g.a[0], bf16, dgate, kSlice) ||
-        !make_map(&g.a[1], bf16, dup, kSlice) || !make_map(&g.b[0], bf16, x, kSlice))
+    if (!use_plan(g, plan_dw(a, sizeof(T) == 4), slices_of(a.rows), scratch, parts_at) ||
+        !make_map(&g.a[0], bf16, in[0], kSlice) || !make_map(&g.a[1], bf16, in[1], kSlice) ||
+        !make_map(&g.b[0], bf16, in[4], kSlice))
         return cudaErrorInvalidValue;
     return launch_gemm<T, O, kDw>(g, st);
 }
 
 #define RRA_GEMM(T)                                                                              \
-    template cudaError_t gemm_forward<T>(const FfArgs &, const Matrix16 &, const Matrix16 &,     \
-                                         const Matrix16 &, cudaStream_t);                        \
-    template cudaError_t gemm_dx<T>(const FfGradArgs &, const Matrix16 &, const Matrix16 &,      \
-                                    const Matrix16 &, const Matrix16 &, cudaStream_t);           \
-    template cudaError_t gemm_dw<T, T>(const FfGradArgs &, const Matrix16 &, const Matrix16 &,   \
-                                       const Matrix16 &, cudaStream_t);                          \
-    template cudaError_t gemm_dw<T, float>(const FfGradArgs &, const Matrix16 &,                 \
-                                           const Matrix16 &, const Matrix16 &, cudaStream_t);
+    template cudaError_t gemm_forward<T>(const FfArgs &, const Matrix16 (&)[3], unsigned char *, \
+                                         size_t, cudaStream_t);                                  \
+    template cudaError_t gemm_dx<T>(const FfGradArgs &, const Matrix16 (&)[5], unsigned char *,  \
+                                    size_t, cudaStream_t);                                       \
+    template cudaError_t gemm_dw<T, float>(const FfGradArgs &, const Matrix16 (&)[5],            \
+                                           unsigned char *, size_t, cudaStream_t);
+RRA_GEMM(float)
 RRA_GEMM(__half)
 RRA_GEMM(__nv_bfloat16)
 #undef RRA_GEMM
+template cudaError_t gemm_dw<__half, __half>(const FfGradArgs &, const Matrix16 (&)[5],
+                                             unsigned char *, size_t, cudaStream_t);
+template cudaError_t gemm_dw<__nv_bfloat16, __nv_bfloat16>(const FfGradArgs &,
+                                                           const Matrix16 (&)[5], unsigned char *,
+                                                           size_t, cudaStream_t);
 
 } // namespace rra

@@ -50,6 +50,25 @@ __device__ __forceinline__ bool wait_limited(uint64_t *bar, uint32_t parity, vol
     }
 }
 
+// Barrier `id` of `threads` threads of the block.
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same; true where all of them say so.
+__device__ __forceinline__ bool named_all(int id, int threads, bool yes)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(threads), "r"((uint32_t)yes)
+                 : "memory");
+    return r != 0;
+}
+
 // The address of this block's shared memory `p` in block `rank` of its cluster.
 __device__ __forceinline__ uint32_t cluster_address(const void *p, uint32_t rank)
 {
@@ -86,13 +105,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-// A box of the tensor from (x, y) on to shared memory; its bytes count on `bar`, a
-// cluster address (of either block of the pair).
-__device__ __forceinline__ void load_box(void *to, const CUtensorMap *m, int x, int y, uint32_t bar)
+// A box of plane z of the tensor from (x, y) on to shared memory; its bytes count on
+// `bar`, a cluster address (of either block of the pair).
+__device__ __forceinline__ void load_box(void *to, const CUtensorMap *m, int x, int y, int z,
+                                         uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile."
-                 "mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(to)),
-                 "l"(m), "r"(x), "r"(y), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile."
+                 "mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)),
+                 "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
 
@@ -128,6 +148,36 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32])
           "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
+}
+
+// 16 columns.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at));
+}
+
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_stored()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_loaded()
