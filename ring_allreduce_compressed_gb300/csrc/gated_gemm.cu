@@ -9,6 +9,7 @@
 
 #include "gated_act.cuh"
 #include "op_common.cuh"
+#include "ragged.cuh"
 #include "saved.cuh"
 #include "stream_slot.h"
 #include "tc.cuh"
@@ -102,21 +103,55 @@ template <int MODE> __device__ __forceinline__ Item item_of(const Gemm &g, int i
 // Slices whose sums stay in tensor memory.
 template <bool F32> __device__ __forceinline__ int run_of(const Item &t) { return F32 ? kRun : t.hi - t.lo; }
 
-// Eight values next to each other, of which `there` are in the row.
+// 16 values next to each other, of which `there` are in the row.  whole: on a 32-byte
+// boundary where all are there.  (A lane has a row to itself: stores of 32 bytes fill
+// sectors, of which ones of 16 would write halves.)
 template <typename T>
-__device__ __forceinline__ void put8(T *p, int there, bool whole, const float v[8])
+__device__ __forceinline__ void put16(T *p, int there, bool whole, const float (&v)[16])
 {
-    if (whole && there == 8)
-        store8<T, true>(p, 8, v);
-    else
-        store8<T, false>(p, there, v);
+    if (whole && there == 16) {
+        uint32_t w[kPackWords<T> * 2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t half[kPackWords<T>];
+            to_words<T>(v + 8 * i, half);
+#pragma unroll
+            for (int j = 0; j < kPackWords<T>; ++j)
+                w[i * kPackWords<T> + j] = half[j];
+        }
+#pragma unroll
+        for (int i = 0; i < kPackWords<T> * 2; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             reinterpret_cast<uint32_t *>(p) + i),
+                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                         "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                         : "memory");
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (j < there)
+            p[j] = from_f32<T>(v[j]);
+}
+
+template <typename T>
+__device__ __forceinline__ void get16(const T *p, int there, bool whole, float (&v)[16])
+{
+    if (whole && there == 16) {
+        load8<T, true>(p, 8, *reinterpret_cast<float(*)[8]>(&v[0]));
+        load8<T, true>(p + 8, 8, *reinterpret_cast<float(*)[8]>(&v[8]));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        v[j] = j < there ? to_f32(p[j]) : 0.0f;
 }
 
 template <int N>
-__device__ __forceinline__ void floats(const uint32_t (&r)[N], int i, float v[8])
+__device__ __forceinline__ void floats(const uint32_t (&r)[N], int i, float (&v)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 16; ++j)
         v[j] = __uint_as_float(r[i + j]);
 }
 
@@ -148,16 +183,18 @@ __device__ __forceinline__ uint32_t row_top(uint32_t at)
     return top;
 }
 
-// One of gate and up, 8 columns from c on of row r.
+// One of gate and up, 16 columns from c on of row r.
 template <typename T>
-__device__ __forceinline__ void keep8(const Kept &to, uint32_t top, long long r, long long c,
-                                      long long ff, bool whole, const float v[8])
+__device__ __forceinline__ void keep16(const Kept &to, uint32_t top, long long r, long long c,
+                                       long long ff, bool whole, const float (&v)[16])
 {
     if (to.exps) {
         const long long nb = blocks_of(ff);
-        store_codes(static_cast<int8_t *>(to.data) + r * nb * kBlock + c, encode8(v, top));
+        const Codes8 a = encode8(v, top), b = encode8(v + 8, top);
+        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(to.data) + r * nb * kBlock + c) =
+            make_uint4(a.w[0], a.w[1], b.w[0], b.w[1]);
     } else if (to.data) {
-        put8(static_cast<T *>(to.data) + r * ff + c, (int)max(0LL, min(8LL, ff - c)), whole, v);
+        put16(static_cast<T *>(to.data) + r * ff + c, (int)max(0LL, min(16LL, ff - c)), whole, v);
     }
 }
 
@@ -191,20 +228,17 @@ __device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, int half
         tmem_loaded();
         if (!on)
             continue;
+        float vg[16], vu[16];
+        floats(rg, 0, vg);
+        floats(ru, 0, vu);
+        const long long col = n0 + c;
+        keep16<T>(g.gate, top[0], r, col, g.n, whole, vg);
+        keep16<T>(g.up, top[1], r, col, g.n, whole, vu);
 #pragma unroll
-        for (int i = 0; i < 16; i += 8) {
-            float vg[8], vu[8], h[8];
-            floats(rg, i, vg);
-            floats(ru, i, vu);
-            const long long col = n0 + c + i;
-            keep8<T>(g.gate, top[0], r, col, g.n, whole, vg);
-            keep8<T>(g.up, top[1], r, col, g.n, whole, vu);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                h[j] = act_value<ACT, sizeof(T) == 4>(vg[j]) * vu[j];
-            put8(static_cast<T *>(g.out[0]) + r * g.n + col, (int)max(0LL, min(8LL, g.n - col)),
-                 whole, h);
-        }
+        for (int j = 0; j < 16; ++j)
+            vg[j] = act_value<ACT, sizeof(T) == 4>(vg[j]) * vu[j];
+        put16(static_cast<T *>(g.out[0]) + r * g.n + col, (int)max(0LL, min(16LL, g.n - col)), whole,
+              vg);
     }
 }
 
@@ -221,23 +255,20 @@ __device__ __forceinline__ void write_plain(const Gemm &g, O *out, int half, uin
         if (!on)
             continue;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 32; i += 16) {
             const long long col = n0 + c + i;
-            const int there = (int)max(0LL, min(8LL, g.n - col));
-            float f[8];
+            const int there = (int)max(0LL, min(16LL, g.n - col));
+            float f[16];
             floats(v, i, f);
             O *const p = out + r * g.n + col;
             if (g.accumulate) {
-                float old[8];
-                if (whole && there == 8)
-                    load8<O, true>(p, 8, old);
-                else
-                    load8<O, false>(p, there, old);
+                float old[16];
+                get16(p, there, whole, old);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 16; ++j)
                     f[j] += old[j];
             }
-            put8(p, there, whole, f);
+            put16(p, there, whole, f);
         }
     }
 }
@@ -495,7 +526,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                 mine = join_splits(g, s, it, rank, at, row, half * kHalf);
             if (mine) {
                 O *const out = static_cast<O *>(g.out[p.which]);
-                const bool whole = g.n % 8 == 0 && aligned_to(out, 16);
+                const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 32);
                 if (MODE == kForward) {
                     if (F32 || g.splits > 1) { // a half has columns that the other has stored
                         tc_fence_before();
@@ -505,8 +536,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                     by_act(g.act, [&](auto act) {
                         write_forward<T, decltype(act)::value>(
                             g, s, half, quarter, at, r, p.n0,
-                            whole && (g.gate.exps || aligned_to(g.gate.data, 16)) &&
-                                (g.up.exps || aligned_to(g.up.data, 16)));
+                            whole && (g.gate.exps || aligned_to(g.gate.data, 32)) &&
+                                (g.up.exps || aligned_to(g.up.data, 32)));
                     });
                 } else {
                     write_plain<O>(g, out, half, at, r, p.n0, whole);

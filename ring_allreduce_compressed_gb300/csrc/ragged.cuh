@@ -46,7 +46,7 @@ template <typename T> __device__ __forceinline__ float element(const uint32_t (&
 }
 
 template <typename T>
-__device__ __forceinline__ void to_words(const float v[8], uint32_t (&w)[kPackWords<T>])
+__device__ __forceinline__ void to_words(const float *v, uint32_t (&w)[kPackWords<T>])
 {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
