@@ -21,46 +21,79 @@ namespace {
 constexpr int kActThreads = 256;
 
 // Packs of 8 elements of a row; SAVED: gate and up in 8 bits.  Every element is read
-// before it is written, so outputs may take inputs' places.
-template <typename T, bool SAVED, bool VEC, int ACT>
+// before it is written, so outputs may take inputs' places; WHOLE: every pack is on a
+// 16-byte boundary.
+template <typename T, bool SAVED, bool WHOLE, int ACT>
 __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs a, int lanes)
 {
     constexpr bool exact = sizeof(T) == 4;
-    const T *const dh = static_cast<const T *>(a.dh);
+    constexpr int N = kPackWords<T>;
+    const long long count = a.rows * a.ff;
+    const T *const dh = static_cast<const T *>(a.dh), *const gate = static_cast<const T *>(a.gate.data),
+                   *const up = static_cast<const T *>(a.up.data);
     const long long nb = blocks_of(a.ff), packs = (a.ff + kPack - 1) / kPack;
-    const int li = threadIdx.x % lanes, groups = kActThreads / lanes;
+    const int li = threadIdx.x % lanes, groups = kActThreads / lanes, stretch = min(lanes, 32);
     dependents_wait();
     dependents_launch();
-    for (long long r = (long long)blockIdx.x * groups + threadIdx.x / lanes; r < a.rows;
-         r += (long long)gridDim.x * groups)
-        for (long long u = li; u < packs; u += lanes) {
-            const int there = (int)min((long long)kPack, a.ff - u * kPack);
-            const long long at = r * a.ff + u * kPack;
-            float g[8], v[8], d[8];
+    // (all lanes go on together: those of a warp store together)
+    for (long long base = (long long)blockIdx.x * groups; base < a.rows;
+         base += (long long)gridDim.x * groups) {
+        const long long r = base + threadIdx.x / lanes;
+        for (long long u0 = 0; u0 < packs; u0 += lanes) {
+            const long long u = u0 + li, at = r * a.ff + u * kPack;
+            const bool on = r < a.rows;
+            const auto in = [&](long long p) {
+                return (int)max(0LL, min((long long)kPack, a.ff - p * kPack));
+            };
+            const int there = on ? in(u) : 0;
+            float g[8], v[8];
+            uint32_t d[N];
+            load_words<T, WHOLE>(dh + at, there, dh, dh + count, d);
             if (SAVED) {
                 const long long b = r * nb + u / kBlockPacks, c = (r * nb * kBlockPacks + u) * kPack;
-                decode8(load_codes(static_cast<const int8_t *>(a.gate.data) + c), a.gate.exps[b],
-                        g);
-                decode8(load_codes(static_cast<const int8_t *>(a.up.data) + c), a.up.exps[b], v);
+                Codes8 cg = {{0u, 0u}}, cu = cg;
+                int8_t eg = 0, eu = 0;
+                if (there > 0) {
+                    cg = load_codes(static_cast<const int8_t *>(a.gate.data) + c);
+                    cu = load_codes(static_cast<const int8_t *>(a.up.data) + c);
+                    eg = a.gate.exps[b];
+                    eu = a.up.exps[b];
+                }
+                decode8(cg, eg, g);
+                decode8(cu, eu, v);
             } else {
-                load8<T, VEC>(static_cast<const T *>(a.gate.data) + at, there, g);
-                load8<T, VEC>(static_cast<const T *>(a.up.data) + at, there, v);
+                uint32_t wg[N], wu[N];
+                load_words<T, WHOLE>(gate + at, there, gate, gate + count, wg);
+                load_words<T, WHOLE>(up + at, there, up, up + count, wu);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    g[j] = element<T>(wg, j);
+                    v[j] = element<T>(wu, j);
+                }
             }
-            load8<T, VEC>(dh + at, there, d);
-            float dg[8], h[8];
+            float dg[8], du[8], h[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float slope;
-                const float value = act_both<ACT, exact>(g[j], &slope);
-                dg[j] = d[j] * v[j] * slope;
+                const float value = act_both<ACT, exact>(g[j], &slope), x = element<T>(d, j);
+                dg[j] = x * v[j] * slope;
+                du[j] = x * value;
                 h[j] = value * v[j];
-                d[j] *= value;
             }
-            store8<T, VEC>(static_cast<T *>(a.dgate) + at, there, dg);
-            store8<T, VEC>(static_cast<T *>(a.dup) + at, there, d);
-            if (a.h)
-                store8<T, VEC>(static_cast<T *>(a.h) + at, there, h);
+            // (a misaligned store takes neighbours' elements along: all of the warp has read)
+            if (!WHOLE)
+                __syncwarp();
+            uint32_t o[N];
+            to_words<T>(dg, o);
+            store_words<T, WHOLE>(static_cast<T *>(a.dgate) + at, there, in(u + 1), on, stretch, o);
+            to_words<T>(du, o);
+            store_words<T, WHOLE>(static_cast<T *>(a.dup) + at, there, in(u + 1), on, stretch, o);
+            if (a.h) {
+                to_words<T>(h, o);
+                store_words<T, WHOLE>(static_cast<T *>(a.h) + at, there, in(u + 1), on, stretch, o);
+            }
         }
+    }
 }
 
 template <typename T> cudaError_t act_grad(const FfGradArgs &a, cudaStream_t st)
@@ -92,11 +125,21 @@ template <typename T> cudaError_t act_grad(const FfGradArgs &a, cudaStream_t st)
 // of fp32 numbers cut into three planes of bf16, 8 bits of each number in the first,
 // the next 8 in the second and the rest in the third.  (Cut, not rounded: the three
 // add up to the number exactly, and none is larger.)
-template <typename T>
-__global__ void __launch_bounds__(kActThreads) operand_kernel(const T *from, uint32_t *to,
-                                                              long long rows, long long cols,
-                                                              long long ld)
+struct Copies {
+    struct {
+        const void *from;
+        uint32_t *to;
+        long long rows, cols, ld;
+    } c[5];
+};
+
+// blockIdx.y: the matrix.
+template <typename T> __global__ void __launch_bounds__(kActThreads) operand_kernel(const Copies all)
 {
+    const T *const from = static_cast<const T *>(all.c[blockIdx.y].from);
+    uint32_t *const to = all.c[blockIdx.y].to;
+    const long long rows = all.c[blockIdx.y].rows, cols = all.c[blockIdx.y].cols,
+                    ld = all.c[blockIdx.y].ld;
     const long long packs = ld / kPack, total = rows * packs;
     dependents_wait();
     dependents_launch();
@@ -166,20 +209,24 @@ public:
             return RRA_OK;
         return op_scratch(st, parts_at + parts, lk_, &scratch);
     }
-    // Copies operand i, once what it holds is there.
-    cudaError_t fill(int i, cudaStream_t st)
+    // Copies those that need it, once what they hold is there.
+    cudaError_t fill(cudaStream_t st)
     {
-        if (!copy_[i])
+        Copies all = {};
+        int n = 0;
+        long long most = 0;
+        for (int i = 0; i < N; ++i)
+            if (copy_[i]) {
+                uint32_t *const to = reinterpret_cast<uint32_t *>(scratch + at_[i]);
+                all.c[n++] = {m[i].p, to, m[i].rows, m[i].cols, m[i].ld};
+                most = std::max(most, m[i].rows * (m[i].ld / kPack));
+                m[i].p = to;
+            }
+        if (n == 0)
             return cudaSuccess;
-        uint32_t *const to = reinterpret_cast<uint32_t *>(scratch + at_[i]);
-        const long long packs = m[i].rows * (m[i].ld / kPack);
-        const unsigned grid = (unsigned)std::min((packs + kActThreads - 1) / kActThreads,
-                                                 (long long)num_sms() * 32);
-        const cudaError_t e =
-            launch_chained(operand_kernel<T>, dim3(grid), kActThreads, st,
-                           static_cast<const T *>(m[i].p), to, m[i].rows, m[i].cols, m[i].ld);
-        m[i].p = to;
-        return e;
+        const unsigned grid =
+            (unsigned)std::min((most + kActThreads - 1) / kActThreads, (long long)num_sms() * 16);
+        return launch_chained(operand_kernel<T>, dim3(grid, n), kActThreads, st, all);
     }
 
 private:
@@ -216,9 +263,7 @@ template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
                        {a.wu, a.ff, a.dim, a.dim, 1}});
     if ((s = in.take(gemm_parts(a, sizeof(T) == 4), st)) != RRA_OK)
         return s;
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < 3 && e == cudaSuccess; ++i)
-        e = in.fill(i, st);
+    const cudaError_t e = in.fill(st);
     return launched(e == cudaSuccess ? gemm_forward<T>(a, in.m, in.scratch, in.parts_at, st) : e);
 }
 
@@ -244,8 +289,8 @@ template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaSt
     if (products && (s = in.take(gemm_parts(a, sizeof(T) == 4), st)) != RRA_OK)
         return s;
     cudaError_t e = act_grad<T>(a, st);
-    for (int i = 0; i < 5 && e == cudaSuccess; ++i)
-        e = in.fill(i, st);
+    if (e == cudaSuccess && products)
+        e = in.fill(st);
     if (e == cudaSuccess && a.dx)
         e = gemm_dx<T>(a, in.m, in.scratch, in.parts_at, st);
     if (e == cudaSuccess && weights)

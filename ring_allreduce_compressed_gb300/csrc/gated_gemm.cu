@@ -103,24 +103,41 @@ template <int MODE> __device__ __forceinline__ Item item_of(const Gemm &g, int i
 // Slices whose sums stay in tensor memory.
 template <bool F32> __device__ __forceinline__ int run_of(const Item &t) { return F32 ? kRun : t.hi - t.lo; }
 
-// 16 values next to each other, of which `there` are in the row.  whole: on a 32-byte
-// boundary where all are there.  (A lane has a row to itself: stores of 32 bytes fill
-// sectors, of which ones of 16 would write halves.)
-template <typename T>
-__device__ __forceinline__ void put16(T *p, int there, bool whole, const float (&v)[16])
+// 16 columns from `col` on of a warp's 32 rows (from r0 on; a lane has a row) to an
+// output of m x n.  whole: every 16 columns are on a 32-byte boundary.  A lane then
+// writes its own 32 or 64 bytes (whole sectors, of which 16 bytes would write halves);
+// else they go through shared memory, so that a store has two rows' neighbouring
+// elements and not 32 rows' (which takes a cycle a row: 333 x 513 x 1001 fp16, dx: 50 us).
+constexpr int kStageRow = 17; // floats: rows begin in different banks
+template <typename O>
+__device__ __forceinline__ void put_columns(float *stage, O *out, long long m, long long n,
+                                            long long r0, long long col, bool whole,
+                                            bool accumulate, float (&v)[16])
 {
-    if (whole && there == 16) {
-        uint32_t w[kPackWords<T> * 2];
+    const int lane = threadIdx.x % 32;
+    if (whole && col + 16 <= n) {
+        O *const p = out + (r0 + lane) * n + col;
+        if (r0 + lane >= m)
+            return;
+        if (accumulate) {
+            float old[16];
+            load8<O, true>(p, 8, *reinterpret_cast<float(*)[8]>(&old[0]));
+            load8<O, true>(p + 8, 8, *reinterpret_cast<float(*)[8]>(&old[8]));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[j] += old[j];
+        }
+        uint32_t w[kPackWords<O> * 2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            uint32_t half[kPackWords<T>];
-            to_words<T>(v + 8 * i, half);
+            uint32_t half[kPackWords<O>];
+            to_words<O>(v + 8 * i, half);
 #pragma unroll
-            for (int j = 0; j < kPackWords<T>; ++j)
-                w[i * kPackWords<T> + j] = half[j];
+            for (int j = 0; j < kPackWords<O>; ++j)
+                w[i * kPackWords<O> + j] = half[j];
         }
 #pragma unroll
-        for (int i = 0; i < kPackWords<T> * 2; i += 8)
+        for (int i = 0; i < kPackWords<O> * 2; i += 8)
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                              reinterpret_cast<uint32_t *>(p) + i),
                          "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
@@ -130,21 +147,17 @@ __device__ __forceinline__ void put16(T *p, int there, bool whole, const float (
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-        if (j < there)
-            p[j] = from_f32<T>(v[j]);
-}
-
-template <typename T>
-__device__ __forceinline__ void get16(const T *p, int there, bool whole, float (&v)[16])
-{
-    if (whole && there == 16) {
-        load8<T, true>(p, 8, *reinterpret_cast<float(*)[8]>(&v[0]));
-        load8<T, true>(p + 8, 8, *reinterpret_cast<float(*)[8]>(&v[8]));
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        v[j] = j < there ? to_f32(p[j]) : 0.0f;
+        stage[lane * kStageRow + j] = v[j];
+    __syncwarp();
+    const long long c = col + lane % 16;
+    O *p = out + (r0 + lane / 16) * n + c;
+#pragma unroll 8
+    for (int i = lane / 16; i < 32; i += 2, p += 2 * n)
+        if (r0 + i < m && c < n) {
+            const float f = stage[i * kStageRow + lane % 16];
+            *p = from_f32<O>(accumulate ? to_f32(*p) + f : f);
+        }
+    __syncwarp();
 }
 
 template <int N>
@@ -165,6 +178,7 @@ struct Shared {
     uint64_t full[kStages], empty[kStages], summed[2], written[2];
     uint32_t tmem, stop, last;
     uint32_t top[2][2][kHalf]; // gate, up; half; row
+    float stage[kWriters][32 * kStageRow];
 };
 
 // Largest magnitude's bits of 64 columns of this lane's row.
@@ -183,40 +197,44 @@ __device__ __forceinline__ uint32_t row_top(uint32_t at)
     return top;
 }
 
-// One of gate and up, 16 columns from c on of row r.
+// One of gate and up, 16 columns from col on.
 template <typename T>
-__device__ __forceinline__ void keep16(const Kept &to, uint32_t top, long long r, long long c,
-                                       long long ff, bool whole, const float (&v)[16])
+__device__ __forceinline__ void keep_columns(const Kept &to, float *stage, uint32_t top,
+                                             const Gemm &g, long long r0, long long col, bool whole,
+                                             float (&v)[16])
 {
+    const long long r = r0 + threadIdx.x % 32;
     if (to.exps) {
-        const long long nb = blocks_of(ff);
+        if (r >= g.m)
+            return;
         const Codes8 a = encode8(v, top), b = encode8(v + 8, top);
-        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(to.data) + r * nb * kBlock + c) =
-            make_uint4(a.w[0], a.w[1], b.w[0], b.w[1]);
+        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(to.data) + r * blocks_of(g.n) * kBlock +
+                                   col) = make_uint4(a.w[0], a.w[1], b.w[0], b.w[1]);
     } else if (to.data) {
-        put16(static_cast<T *>(to.data) + r * ff + c, (int)max(0LL, min(16LL, ff - c)), whole, v);
+        put_columns(stage, static_cast<T *>(to.data), g.m, g.n, r0, col, whole, false, v);
     }
 }
 
-// Gate and up of this lane's row r, 64 columns from n0 + 64 half on, to where they go.
+// Gate and up of a warp's rows from r0 on, 64 columns from n0 + 64 half on, to where
+// they go.
 template <typename T, int ACT>
-__device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, int half, int quarter,
-                                              uint32_t at, long long r, long long n0, bool whole)
+__device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, float *stage, int half,
+                                              int quarter, uint32_t at, long long r0, long long n0,
+                                              bool whole)
 {
-    const bool on = r < g.m;
     uint32_t top[2] = {0, 0}; // bits of the blocks' largest magnitudes
     if (g.gate.exps || g.up.exps) {
         const int row = quarter * 32 + threadIdx.x % 32;
+        const long long r = r0 + threadIdx.x % 32;
         s.top[0][half][row] = row_top(at + half * 64);
         s.top[1][half][row] = row_top(at + kHalf + half * 64);
         named_barrier(2 + quarter, 64);
-        const long long nb = blocks_of(g.n), b = r * nb + n0 / kBlock;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             top[i] = max(s.top[i][0][row], s.top[i][1][row]);
             int8_t *const exps = i == 0 ? g.gate.exps : g.up.exps;
-            if (on && half == 0 && exps)
-                exps[b] = exponent_byte(block_exponent(top[i]));
+            if (r < g.m && half == 0 && exps)
+                exps[r * blocks_of(g.n) + n0 / kBlock] = exponent_byte(block_exponent(top[i]));
         }
         named_barrier(2 + quarter, 64); // (read before the next ones are written)
     }
@@ -226,49 +244,32 @@ __device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, int half
         tmem_load(at + c, rg);
         tmem_load(at + kHalf + c, ru);
         tmem_loaded();
-        if (!on)
-            continue;
         float vg[16], vu[16];
         floats(rg, 0, vg);
         floats(ru, 0, vu);
-        const long long col = n0 + c;
-        keep16<T>(g.gate, top[0], r, col, g.n, whole, vg);
-        keep16<T>(g.up, top[1], r, col, g.n, whole, vu);
+        keep_columns<T>(g.gate, stage, top[0], g, r0, n0 + c, whole, vg);
+        keep_columns<T>(g.up, stage, top[1], g, r0, n0 + c, whole, vu);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             vg[j] = act_value<ACT, sizeof(T) == 4>(vg[j]) * vu[j];
-        put16(static_cast<T *>(g.out[0]) + r * g.n + col, (int)max(0LL, min(16LL, g.n - col)), whole,
-              vg);
+        put_columns(stage, static_cast<T *>(g.out[0]), g.m, g.n, r0, n0 + c, whole, false, vg);
     }
 }
 
 template <typename O>
-__device__ __forceinline__ void write_plain(const Gemm &g, O *out, int half, uint32_t at,
-                                            long long r, long long n0, bool whole)
+__device__ __forceinline__ void write_plain(const Gemm &g, float *stage, O *out, int half,
+                                            uint32_t at, long long r0, long long n0, bool whole)
 {
-    const bool on = r < g.m;
 #pragma unroll 1
-    for (int c = half * kHalf; c < half * kHalf + kHalf; c += 32) {
+    for (int c = half * kHalf; c < half * kHalf + kHalf && n0 + c < g.n; c += 32) {
         uint32_t v[32];
         tmem_load(at + c, v);
         tmem_loaded();
-        if (!on)
-            continue;
 #pragma unroll
         for (int i = 0; i < 32; i += 16) {
-            const long long col = n0 + c + i;
-            const int there = (int)max(0LL, min(16LL, g.n - col));
             float f[16];
             floats(v, i, f);
-            O *const p = out + r * g.n + col;
-            if (g.accumulate) {
-                float old[16];
-                get16(p, there, whole, old);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    f[j] += old[j];
-            }
-            put16(p, there, whole, f);
+            put_columns(stage, out, g.m, g.n, r0, n0 + c + i, whole, g.accumulate != 0, f);
         }
     }
 }
@@ -297,9 +298,10 @@ __device__ __forceinline__ void take_sums(uint32_t from, uint32_t to, int first,
 
 // This item's sums to memory.  In the block that is the last of its tile's splits to
 // get here: all of them added, in the order of the splits, back in tensor memory, and
-// true.  Lane by lane of row `row` and 128 columns from `first` on.
+// true.  Lane by lane of row `row` (there: one of the output's), 128 columns from
+// `first` on.
 __device__ __forceinline__ bool join_splits(const Gemm &g, Shared &s, const Item &t, uint32_t rank,
-                                            uint32_t at, int row, int first)
+                                            uint32_t at, int row, int first, bool there)
 {
     constexpr long long kPart = (long long)kHalf * kSide; // floats of a block
     float *const tile = g.parts + ((long long)t.tile * g.splits * 2 + rank) * kPart;
@@ -310,7 +312,7 @@ __device__ __forceinline__ bool join_splits(const Gemm &g, Shared &s, const Item
         tmem_load(at + c, v);
         tmem_loaded();
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
+        for (int j = 0; there && j < 32; j += 4)
             mine[(c + j) / 4 * kHalf + row] =
                 make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
                             __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
@@ -330,20 +332,33 @@ __device__ __forceinline__ bool join_splits(const Gemm &g, Shared &s, const Item
         return false;
     __threadfence();
 #pragma unroll 1
-    for (int c = first; c < first + kHalf; c += 32) {
-        uint32_t v[32];
-        float sum[32] = {};
+    for (int c = first; c < first + kHalf; c += 16) {
+        constexpr int kAhead = 4; // splits whose parts are on their way
+        uint32_t v[16];
+        float sum[16] = {};
 #pragma unroll 1
-        for (int k = 0; k < g.splits; ++k) {
-            const float4 *const p = reinterpret_cast<const float4 *>(tile + k * 2 * kPart);
+        for (int k0 = 0; k0 < g.splits; k0 += kAhead) {
+            float4 q[kAhead][4];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 q = __ldcg(p + (c + j) / 4 * kHalf + row);
-                sum[j] += q.x, sum[j + 1] += q.y, sum[j + 2] += q.z, sum[j + 3] += q.w;
+            for (int k = 0; k < kAhead; ++k) {
+                const float4 *const p =
+                    reinterpret_cast<const float4 *>(tile + (k0 + k) * 2 * kPart) +
+                    c / 4 * kHalf + row;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[k][j] = there && k0 + k < g.splits ? __ldcg(p + j * kHalf)
+                                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[4 * j] += q[k][j].x, sum[4 * j + 1] += q[k][j].y;
+                    sum[4 * j + 2] += q[k][j].z, sum[4 * j + 3] += q[k][j].w;
+                }
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             v[j] = __float_as_uint(sum[j]);
         tmem_store(at + c, v);
     }
@@ -520,10 +535,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             const uint32_t at = tmem + lanes + (F32 ? kSide : into * kSide);
             const TilePlace p = tile_place<MODE>(g, it.tile);
             const int row = quarter * 32 + lane;
-            const long long r = p.m0 + rank * kHalf + row;
+            const long long r0 = p.m0 + rank * kHalf + quarter * 32;
+            float *const stage = s.stage[warp - 2];
             bool mine = true;
             if (g.splits > 1)
-                mine = join_splits(g, s, it, rank, at, row, half * kHalf);
+                mine = join_splits(g, s, it, rank, at, row, half * kHalf, r0 + lane < g.m);
             if (mine) {
                 O *const out = static_cast<O *>(g.out[p.which]);
                 const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 32);
@@ -535,12 +551,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                     }
                     by_act(g.act, [&](auto act) {
                         write_forward<T, decltype(act)::value>(
-                            g, s, half, quarter, at, r, p.n0,
+                            g, s, stage, half, quarter, at, r0, p.n0,
                             whole && (g.gate.exps || aligned_to(g.gate.data, 32)) &&
                                 (g.up.exps || aligned_to(g.up.data, 32)));
                     });
                 } else {
-                    write_plain<O>(g, out, half, at, r, p.n0, whole);
+                    write_plain<O>(g, stage, out, half, at, r0, p.n0, whole);
                 }
             }
             if (!F32)
