@@ -40,8 +40,7 @@ __device__ __forceinline__ int in_pack(long long dim, long long u)
 }
 
 // The pairs of a pack.
-template <typename T>
-__device__ __forceinline__ Pair pair_in(const uint32_t (&w)[kPackWords<T>], int j)
+template <typename T> __device__ __forceinline__ Pair pair_in(const uint32_t *w, int j)
 {
     return pair_of(element<T>(w, 2 * j), element<T>(w, 2 * j + 1));
 }
@@ -58,47 +57,138 @@ struct Save {
     Group g;
 };
 
-// Threads of a block, wide rows apart: 80 registers a thread hold a row without
-// spilling, 64 do not.
+// Threads of a block, wide rows apart, which need their registers.
 constexpr int kSaveThreads = 256;
 constexpr int kSaveHeld = 4; // packs of a lane
 
-// A row in the registers of a group of lanes, as in norm_kernel: lane i holds
-// packs i, i + lanes, ..., and 16 lanes of a warp a block of codes.
+// Larger of the two halves of each, as unsigned numbers.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Bits of the largest magnitudes of the blocks of codes that a lane's P packs are in, as
+// fp32.  16-bit numbers are compared as whole numbers, two packs in a word.
+template <typename T, int P>
+__device__ __forceinline__ void block_tops(const uint32_t (&w)[P][kPackWords<T>], uint32_t (&top)[P])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = element<T>(w[k], j);
+            top[k] = half_warp_max(top_bits(v));
+        }
+    } else {
+        uint32_t most[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            uint32_t m = w[k][0] & 0x7fff7fffu;
+#pragma unroll
+            for (int j = 1; j < 4; ++j)
+                m = max_halves(m, w[k][j] & 0x7fff7fffu);
+            most[k] = max_halves(m, m >> 16); // the lower half
+        }
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+            uint32_t m = k + 1 < P ? __byte_perm(most[k], most[k + 1], 0x5410) : most[k] & 0xffffu;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                m = max_halves(m, __shfl_xor_sync(kFull, m, o));
+#pragma unroll
+            for (int i = 0; i < 2 && k + i < P; ++i) {
+                const uint32_t h = i ? m >> 16 : m & 0xffffu;
+                top[k + i] = std::is_same<T, __nv_bfloat16>::value
+                                 ? h << 16
+                                 : __float_as_uint(__half2float(__ushort_as_half((uint16_t)h)));
+            }
+        }
+    }
+}
+
+// Weights of the whole packs of a row, or `none` where there is no array.
+template <typename W> __device__ __forceinline__ void whole_weights(const W *p, float none, Pair (&v)[4])
+{
+    float t[8];
+    if (p) {
+        load8<W, true>(p, 8, t);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t[j] = none;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = pair_of(t[2 * j], t[2 * j + 1]);
+}
+
+// Which pack of a row is a lane's k-th: a warp of several holds 32 K neighbouring ones,
+// 32 apart in a lane, so that its K are at constant distances; lanes of less than a warp
+// hold every `lanes`-th.
+template <int K, bool MULTI> __device__ __forceinline__ int pack_of(int li, int k, int lanes)
+{
+    return MULTI ? li / 32 * (32 * K) + k * 32 + li % 32 : li + k * lanes;
+}
+
+// Rows in the registers of a group of lanes, as in norm_kernel; 16 lanes of a warp hold a
+// block of codes.  The next row is on its way while one is worked on.
 // WHOLE: every pack is whole and on a 16-byte boundary.
 template <typename T, typename W, int K, bool MULTI, bool WHOLE, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 3 : 1)
+__global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
     save_kernel(const Save a)
 {
+    constexpr int N = kPackWords<T>;
     __shared__ __align__(16) float sm[MULTI ? 2 * 32 : 4];
     const T *const x = static_cast<const T *>(a.x), *const x_end = x + a.rows * a.dim;
     T *const y = static_cast<T *>(a.y);
-    const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
-                                                                static_cast<const W *>(a.beta);
     const int lanes = a.g.lanes(), li = threadIdx.x % lanes, groups = blockDim.x / lanes;
+    const int gap = (MULTI ? 32 : lanes) * kPack; // elements between a lane's packs
     const int dim = (int)a.dim, nb = (int)blocks_of(dim), packs = nb * kBlockPacks;
     const float n = (float)dim, inverse = 1.0f / n;
     GroupOf group = group_of(a.g, sm, 1);
     if (MULTI) {
-        if (threadIdx.x < 64)
-            sm[threadIdx.x] = 0.0f;
+        for (int i = threadIdx.x; i < 2 * 32; i += blockDim.x)
+            sm[i] = 0.0f;
         __syncthreads();
     }
-    const int first = threadIdx.x / lanes;
-    const auto there = [&](int u) { return max(0, min(kPack, dim - u * kPack)); };
+    const int first = threadIdx.x / lanes, u0 = pack_of<K, MULTI>(li, 0, lanes);
+    const W *const gamma = static_cast<const W *>(a.gamma),
+                   *const beta = static_cast<const W *>(a.beta);
+    int there[K], next[K]; // elements of the lane's packs, and of the ones behind them
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = u0 * kPack + k * gap;
+        there[k] = max(0, min(kPack, dim - c));
+        next[k] = max(0, min(kPack, dim - c - kPack));
+    }
+    const long long step = (long long)gridDim.x * groups;
     dependents_wait();
     dependents_launch();
-    for (long long base = (long long)blockIdx.x * groups; base < a.rows;
-         base += (long long)gridDim.x * groups) {
+    uint32_t ahead[K][N];
+    const auto read = [&](long long base) {
         // every lane takes part in the sums, some in vain: they read the last row
-        const long long r = MULTI ? base : min(base + first, a.rows - 1);
-        const bool on = MULTI || base + first < a.rows;
-        uint32_t w[K][kPackWords<T>];
-        const T *const p = x + r * dim;
+        const T *const p = x + min(base + (MULTI ? 0 : first), a.rows - 1) * dim + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            load_words<T, WHOLE>(p + (li + k * lanes) * kPack, there(li + k * lanes), x, x_end,
-                                 w[k]);
+            load_words<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
+    };
+    long long base = (long long)blockIdx.x * groups;
+    read(base);
+    for (; base < a.rows; base += step) {
+        const long long r = min(base + (MULTI ? 0 : first), a.rows - 1);
+        const bool on = MULTI || base + first < a.rows;
+        uint32_t w[K][N];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                w[k][j] = ahead[k][j];
+        if (base + step < a.rows)
+            read(base + step);
         Pair sum = pair_of(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -110,53 +200,71 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 3 : 1)
         const Pair minus = pair_of(-mu, -mu);
         sum = pair_of(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = there(li + k * lanes);
-            if (c == kPack) {
+        for (int k = 0; k < K; ++k)
+            if (there[k] == kPack) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const Pair d = add(pair_in<T>(w[k], j), minus);
                     sum = fma(d, d, sum);
                 }
-            } else if (!WHOLE && c > 0) {
+            } else if (!WHOLE && there[k] > 0) {
                 float t = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float d = j < c ? element<T>(w[k], j) - mu : 0.0f;
+                    const float d = j < there[k] ? element<T>(w[k], j) - mu : 0.0f;
                     t = fmaf(d, d, t);
                 }
                 sum = add(sum, pair_of(t, 0.0f));
             }
-        }
         s.v[0] = sum_of(sum);
         const float rs = rsqrtf(quotient(group_sum<MULTI, 1>(s, group).v[0], n, inverse) + a.eps);
         const Pair scale = pair_of(rs, rs);
+        uint32_t top[K];
+        block_tops<T, K>(w, top);
+        bool special = false;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            special = special || special_block(top[k]);
+        // (one question a row: asked for every pack, its ways apart cost more than the codes)
+        const bool plain = !__any_sync(kFull, special);
+        int8_t *const codes = a.codes + (r * packs + u0) * kPack;
+        T *const to = y + r * dim + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int u = li + k * lanes, c = there(u);
-            if (MULTI && k * lanes >= packs) // (of all lanes)
-                break;
-            float v[8], g[8], b[8];
+            const int u = u0 + k * (gap / kPack);
+            float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = element<T>(w[k], j);
-            const uint32_t top = half_warp_max(top_bits(v));
             if (on && u < packs) {
-                store_codes(a.codes + (r * packs + u) * kPack, encode8(v, top));
+                store_codes(codes + k * gap, plain ? plain_codes8(v, top[k]) : encode8(v, top[k]));
                 if (u % kBlockPacks == 0)
-                    a.exps[r * nb + u / kBlockPacks] = exponent_byte(block_exponent(top));
+                    a.exps[r * nb + u / kBlockPacks] = exponent_byte(block_exponent(top[k]));
             }
-            weights8<W, WHOLE>(gamma, u * kPack, c, 1.0f, g);
-            weights8<W, WHOLE>(beta, u * kPack, c, 0.0f, b);
+            Pair g[4], b[4];
+            if (WHOLE) {
+                // (behind the row: its first weights, for nothing)
+                const int c = there[k] ? u * kPack : 0;
+                whole_weights(gamma ? gamma + c : nullptr, 1.0f, g);
+                whole_weights(beta ? beta + c : nullptr, 0.0f, b);
+            } else {
+                float t[8];
+                weights8<W, false>(gamma, u * kPack, there[k], 1.0f, t);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Pair q = fma(mul(add(pair_of(v[2 * j], v[2 * j + 1]), minus), scale),
-                                   pair_of(g[2 * j], g[2 * j + 1]), pair_of(b[2 * j], b[2 * j + 1]));
-                halves(q, v[2 * j], v[2 * j + 1]);
+                for (int j = 0; j < 4; ++j)
+                    g[j] = pair_of(t[2 * j], t[2 * j + 1]);
+                weights8<W, false>(beta, u * kPack, there[k], 0.0f, t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    b[j] = pair_of(t[2 * j], t[2 * j + 1]);
             }
-            uint32_t o[kPackWords<T>];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                halves(fma(mul(add(pair_of(v[2 * j], v[2 * j + 1]), minus), scale), g[j], b[j]),
+                       v[2 * j], v[2 * j + 1]);
+            uint32_t o[N];
             to_words<T>(v, o);
-            store_words<T, WHOLE>(y + r * dim + u * kPack, c, there(u + 1), on, min(lanes, 32), o);
+            store_words<T, WHOLE>(to + k * gap, there[k], next[k], on, min(lanes, 32), o);
         }
         if (on && li == 0) {
             a.mean[r] = mu;
@@ -224,7 +332,15 @@ Group save_group(long long packs, int K)
     return {packs <= kBlockPacks ? 4 : 5, (int)((packs + 32 * K - 1) / (32 * K))};
 }
 
-template <typename T, typename W, bool VEC> cudaError_t save_rows(Save a, cudaStream_t st)
+template <typename T, typename W, int K, bool MULTI, bool WHOLE, int THREADS>
+cudaError_t save_launch(const Save &a, cudaStream_t st)
+{
+    const int threads = MULTI ? 32 * a.g.warps : kSaveThreads, rows = threads / a.g.lanes();
+    return launch_chained(save_kernel<T, W, K, MULTI, WHOLE, THREADS>,
+                          dim3(grid_of((a.rows + rows - 1) / rows, 2048 / threads)), threads, st, a);
+}
+
+template <typename T, typename W, bool WHOLE> cudaError_t save_rows(Save a, cudaStream_t st)
 {
     const long long packs = blocks_of(a.dim) * kBlockPacks;
     if (packs > 1024LL * kSaveHeld)
@@ -232,21 +348,14 @@ template <typename T, typename W, bool VEC> cudaError_t save_rows(Save a, cudaSt
                               a);
     const bool few = packs <= 32;
     a.g = save_group(packs, few ? 1 : kSaveHeld);
-    if (a.g.warps > 1) {
-        const int threads = 32 * a.g.warps;
-        const dim3 grid(grid_of(a.rows, 2048 / threads));
-        return threads <= kSaveThreads
-                   ? launch_chained(save_kernel<T, W, kSaveHeld, true, VEC, kSaveThreads>, grid,
-                                    threads, st, a)
-                   : launch_chained(save_kernel<T, W, kSaveHeld, true, VEC, 1024>, grid, threads,
-                                    st, a);
-    }
-    const int per_block = kSaveThreads / a.g.lanes();
-    const unsigned grid = grid_of((a.rows + per_block - 1) / per_block, 16);
-    return few ? launch_chained(save_kernel<T, W, 1, false, VEC, kSaveThreads>, dim3(grid),
-                                kSaveThreads, st, a)
-               : launch_chained(save_kernel<T, W, kSaveHeld, false, VEC, kSaveThreads>, dim3(grid),
-                                kSaveThreads, st, a);
+    if (a.g.warps > 16)
+        return save_launch<T, W, kSaveHeld, true, WHOLE, 1024>(a, st);
+    if (a.g.warps > kSaveThreads / 32)
+        return save_launch<T, W, kSaveHeld, true, WHOLE, 512>(a, st);
+    if (a.g.warps > 1)
+        return save_launch<T, W, kSaveHeld, true, WHOLE, kSaveThreads>(a, st);
+    return few ? save_launch<T, W, 1, false, WHOLE, kSaveThreads>(a, st)
+               : save_launch<T, W, kSaveHeld, false, WHOLE, kSaveThreads>(a, st);
 }
 
 // Is every pack of 8 elements of these rows, and of the weights, whole and on
@@ -281,82 +390,97 @@ struct Restore {
 };
 
 constexpr int kRestoreThreads = 256;
-constexpr int kRestorePacks = 2, kRestoreRows = 2; // of a thread at a time
-constexpr int kRestoreCols = kRestoreThreads * kRestorePacks * kPack; // of a block, blockIdx.y each
+constexpr int kRestorePack = 16; // elements of a thread in a row: 16 bytes of codes
+constexpr int kRestoreRows = 4;  // of a thread at a time
+constexpr int kRestoreCols = kRestoreThreads * kRestorePack; // of a block, blockIdx.y each
 
 // A thread keeps its columns' weights in registers over all of its rows, and has the
 // codes of several rows on their way at a time.
 template <typename T, typename W, bool WHOLE>
-__global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const Restore a)
+__global__ void __launch_bounds__(kRestoreThreads, 2) restore_kernel(const Restore a)
 {
-    constexpr int K = kRestorePacks, R = kRestoreRows;
+    constexpr int E = kRestorePack, R = kRestoreRows;
     const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
                                                                 static_cast<const W *>(a.beta);
     T *const y = static_cast<T *>(a.y);
     const long long nb = blocks_of(a.dim), width = nb * kBlock;
-    const int li = threadIdx.x % a.lanes, groups = kRestoreThreads / a.lanes;
-    const long long u0 = (long long)blockIdx.y * (kRestoreCols / kPack) + li;
-    const long long step = (long long)gridDim.x * groups, first = (long long)blockIdx.x * groups;
+    const int groups = kRestoreThreads / a.lanes, mine = threadIdx.x / a.lanes;
+    const long long c0 = (long long)blockIdx.y * kRestoreCols + threadIdx.x % a.lanes * E;
+    const long long step = (long long)gridDim.x * groups;
+    const auto in = [&](long long c) { return (int)max(0LL, min((long long)E, a.dim - c)); };
+    const int there = in(c0), next = in(c0 + E);
     dependents_wait();
     dependents_launch();
-    int there[K], next[K];
-    Pair g[K][4], b[K][4];
+    Pair g[E / 2], b[E / 2];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const long long u = u0 + k * a.lanes;
-        there[k] = in_pack(a.dim, u);
-        next[k] = in_pack(a.dim, u + 1);
+    for (int h = 0; h < E; h += 8) {
+        const int n = max(0, min(8, there - h));
         float t[8];
-        weights8<W, WHOLE>(gamma, u * kPack, there[k], 1.0f, t);
+        weights8<W, WHOLE>(gamma, c0 + h, n, 1.0f, t);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            g[k][j] = pair_of(t[2 * j], t[2 * j + 1]);
-        weights8<W, WHOLE>(beta, u * kPack, there[k], 0.0f, t);
+            g[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
+        weights8<W, WHOLE>(beta, c0 + h, n, 0.0f, t);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            b[k][j] = pair_of(t[2 * j], t[2 * j + 1]);
+            b[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
     }
     // the rows of a block's groups go on together: whole warps store
-    for (long long base = first; base < a.rows; base += R * step) {
-        Codes8 c[R][K];
-        int8_t e[R][K];
+    for (long long base = (long long)blockIdx.x * groups; base < a.rows; base += R * step) {
+        uint4 c[R];
+        int8_t e[R];
         float mu[R], rs[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const long long r = base + i * step + threadIdx.x / a.lanes;
-            const bool on = r < a.rows;
-            mu[i] = on && a.mean ? a.mean[r] : 0.0f;
-            rs[i] = on && a.rstd ? a.rstd[r] : 1.0f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const long long u = u0 + k * a.lanes;
-                c[i][k] = {{0u, 0u}};
-                e[i][k] = 0;
-                if (on && there[k] > 0) {
-                    c[i][k] = load_codes(a.codes + r * width + u * kPack);
-                    e[i][k] = a.exps[r * nb + u / kBlockPacks];
-                }
+            const long long r = base + i * step + mine;
+            const bool on = r < a.rows && there > 0;
+            c[i] = make_uint4(0u, 0u, 0u, 0u);
+            e[i] = 0;
+            mu[i] = 0.0f;
+            rs[i] = 1.0f;
+            if (on) {
+                c[i] = *reinterpret_cast<const uint4 *>(a.codes + r * width + c0);
+                e[i] = a.exps[r * nb + c0 / kBlock];
+                if (a.mean)
+                    mu[i] = a.mean[r];
+                if (a.rstd)
+                    rs[i] = a.rstd[r];
             }
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const long long r = base + i * step + threadIdx.x / a.lanes;
+            const long long r = base + i * step + mine;
             const Pair minus = pair_of(-mu[i], -mu[i]), scale = pair_of(rs[i], rs[i]);
+            const float s = block_scale(e[i]);
+            const Pair unit = pair_of(s, s);
+            uint32_t o[kPackWords<T, E>];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
+            for (int h = 0; h < 2; ++h) {
                 float2 f[4];
-                fractions8(c[i][k], f);
-                const float s = block_scale(e[i][k]);
+                fractions8(h ? Codes8{{c[i].z, c[i].w}} : Codes8{{c[i].x, c[i].y}}, f);
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    halves(fma(mul(fma(pair_of(f[j].x, f[j].y), pair_of(s, s), minus), scale),
-                               g[k][j], b[k][j]),
+                    halves(fma(mul(fma(pair_of(f[j].x, f[j].y), unit, minus), scale), g[4 * h + j],
+                               b[4 * h + j]),
                            v[2 * j], v[2 * j + 1]);
-                uint32_t o[kPackWords<T>];
-                to_words<T>(v, o);
-                store_words<T, WHOLE>(y + r * a.dim + (u0 + k * a.lanes) * kPack, there[k], next[k],
-                                      r < a.rows, min(a.lanes, 32), o);
+                uint32_t w[kPackWords<T>];
+                to_words<T>(v, w);
+#pragma unroll
+                for (int j = 0; j < kPackWords<T>; ++j)
+                    o[h * kPackWords<T> + j] = w[j];
+            }
+            if constexpr (WHOLE) { // (8 elements, or 16)
+                if (r < a.rows)
+#pragma unroll
+                    for (int j = 0; j < kPackWords<T, E>; j += 4)
+                        if (j * 4 < there * (int)sizeof(T))
+                            *reinterpret_cast<uint4 *>(
+                                reinterpret_cast<uint32_t *>(y + r * a.dim + c0) + j) =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            } else {
+                store_words<T, false, E>(y + r * a.dim + c0, there, next, r < a.rows,
+                                         min(a.lanes, 32), o);
             }
         }
     }
@@ -365,14 +489,14 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const Restore 
 template <typename T, typename W> rra_status restore(Restore a, cudaStream_t st)
 {
     a.lanes = 1;
-    while (a.lanes < kRestoreThreads && a.lanes * kRestorePacks * kPack < a.dim)
+    while (a.lanes < kRestoreThreads && a.lanes * kRestorePack < a.dim)
         a.lanes *= 2;
-    const int groups = kRestoreThreads / a.lanes;
+    const int rows = kRestoreThreads / a.lanes * kRestoreRows; // of a block at a time
     const long long cols = (a.dim + kRestoreCols - 1) / kRestoreCols;
-    const long long blocks = std::max(1LL, num_sms() * 8LL / cols);
     if (cols > 65535) // (rows of 2^28 elements and more)
         return RRA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)std::min((a.rows + groups - 1) / groups, blocks), (unsigned)cols);
+    const long long blocks = std::max(1LL, num_sms() * 8LL / cols);
+    const dim3 grid((unsigned)std::min((a.rows + rows - 1) / rows, blocks), (unsigned)cols);
     return launched(whole_packs<T>(a.dim, {a.y, a.gamma, a.beta})
                         ? launch_chained(restore_kernel<T, W, true>, grid, kRestoreThreads, st, a)
                         : launch_chained(restore_kernel<T, W, false>, grid, kRestoreThreads, st,
@@ -441,20 +565,31 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
     constexpr int kRow = THREADS * 16, kCodes = K * C * kRow, kStage = kCodes + K * THREADS * 8;
     unsigned char *const slots = stages + threadIdx.x * 16;
     unsigned char *const codes = stages + kCodes + threadIdx.x * 8;
-    const auto there = [&](int u) { return max(0, min(kPack, dim - u * kPack)); };
+    const int gap = (MULTI ? 32 : lanes) * kPack; // elements between a lane's packs
+    const int u0 = pack_of<K, MULTI>(li, 0, lanes);
+    int there[K], next[K]; // elements of the lane's packs, and of the ones behind them
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = u0 * kPack + k * gap;
+        there[k] = max(0, min(kPack, dim - c));
+        next[k] = max(0, min(kPack, dim - c - kPack));
+    }
     dependents_wait();
 
     const auto stage_row = [&](int stage, long long r) {
         unsigned char *const to = slots + stage * kStage;
+        const bool on = r < a.rows;
+        const T *const row = dy + r * dim + u0 * kPack;
+        const int8_t *const row_codes = a.codes + r * nb * kBlock + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int u = li + k * lanes, in = r < a.rows ? there(u) : 0;
-            if (in == 0)
+            const int in = there[k];
+            if (!on || in == 0)
                 continue;
-            const T *const p = dy + r * dim + u * kPack;
+            const T *const p = row + k * gap;
             asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
                              smem_u32(codes + stage * kStage + k * THREADS * 8)),
-                         "l"(a.codes + (r * nb * kBlockPacks + u) * kPack)
+                         "l"(row_codes + k * gap)
                          : "memory");
             if (WHOLE) {
 #pragma unroll
@@ -499,8 +634,8 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         next_rs = a.rstd[q];
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (li + k * lanes < packs)
-                next_e[k] = a.exps[q * nb + (li + k * lanes) / kBlockPacks];
+            if (there[k] > 0)
+                next_e[k] = a.exps[q * nb + (u0 * kPack + k * gap) / kBlock];
     };
     next_row(r);
     for (int i = threadIdx.x; i < width; i += blockDim.x)
@@ -528,7 +663,6 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         // dy and xh of the k-th pack, out of its slot
         const auto take = [&](int k, Pair (&d)[4], Pair (&xh)[4]) {
             const unsigned char *const at = slots + now * kStage;
-            const int u = li + k * lanes;
             uint32_t w[N];
             if (WHOLE) {
 #pragma unroll
@@ -543,8 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
                     const uint4 q = *reinterpret_cast<const uint4 *>(at + (k * C + c) * kRow);
                     in[4 * c] = q.x, in[4 * c + 1] = q.y, in[4 * c + 2] = q.z, in[4 * c + 3] = q.w;
                 }
-                shift_bytes(in, (int)(reinterpret_cast<uintptr_t>(dy + r * dim + u * kPack) & 15),
-                            w);
+                shift_bytes(in, (int)(reinterpret_cast<uintptr_t>(dy + r * dim) & 15), w);
             }
             const Codes8 q = load_codes(
                 reinterpret_cast<const int8_t *>(codes + now * kStage + k * THREADS * 8));
@@ -559,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         };
         const auto weight = [&](int k, Pair (&g)[4]) {
             const float4 *const p =
-                reinterpret_cast<const float4 *>(weights + (li + k * lanes) * kPack);
+                reinterpret_cast<const float4 *>(weights + u0 * kPack + k * gap);
             const float4 lo = p[0], hi = p[1];
             g[0] = pair_of(lo.x, lo.y), g[1] = pair_of(lo.z, lo.w);
             g[2] = pair_of(hi.x, hi.y), g[3] = pair_of(hi.z, hi.w);
@@ -568,7 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         if (on) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (li + k * lanes >= packs)
+                if (there[k] == 0)
                     continue;
                 Pair d[4], xh[4], g[4];
                 take(k, d, xh);
@@ -592,9 +725,8 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         const Pair m0 = pair_of(t0, t0), m1 = pair_of(t1, t1);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int u = li + k * lanes;
             uint32_t o[N] = {};
-            if (on && u < packs) {
+            if (on && there[k] > 0) {
                 Pair d[4], xh[4], g[4];
                 float v[8];
                 take(k, d, xh);
@@ -604,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
                     halves(fma(xh[j], m1, fma(mul(d[j], g[j]), scale, m0)), v[2 * j], v[2 * j + 1]);
                 to_words<T>(v, o);
             }
-            store_words<T, WHOLE>(dx + r * dim + u * kPack, there(u), there(u + 1), on,
+            store_words<T, WHOLE>(dx + r * dim + u0 * kPack + k * gap, there[k], next[k], on,
                                   min(lanes, 32), o);
         }
     }
@@ -639,9 +771,9 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
     if (holds)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (li + k * lanes < packs) {
-                store_values<float, 8>(own + (li + k * lanes) * kPack, fg[k]);
-                store_values<float, 8>(own + width + (li + k * lanes) * kPack, fb[k]);
+            if (there[k] > 0) {
+                store_values<float, 8>(own + u0 * kPack + k * gap, fg[k]);
+                store_values<float, 8>(own + width + u0 * kPack + k * gap, fb[k]);
             }
     __syncthreads();
     for (int c = threadIdx.x; c < dim; c += blockDim.x) {

@@ -32,10 +32,10 @@ __device__ __forceinline__ void shift_bytes(const uint32_t (&in)[N_IN], int q, u
         out[i] = q & 16 ? t[i + 4] : t[i];
 }
 
-// Words of a pack of 8 elements.
-template <typename T> constexpr int kPackWords = 8 * sizeof(T) / 4;
+// Words of a pack of 8 elements, or of 16.
+template <typename T, int E = 8> constexpr int kPackWords = E * sizeof(T) / 4;
 
-template <typename T> __device__ __forceinline__ float element(const uint32_t (&w)[kPackWords<T>], int j)
+template <typename T> __device__ __forceinline__ float element(const uint32_t *w, int j)
 {
     if constexpr (sizeof(T) == 4)
         return __uint_as_float(w[j]);
@@ -111,16 +111,16 @@ __device__ __forceinline__ void load_words(const T *p, int n, const T *begin, co
     }
 }
 
-// Writes the n (0..8) elements at p; `next`: how many the next lane's pack has.  A
+// Writes the n (0..E) elements at p; `next`: how many the next lane's pack has.  A
 // stretch of `lanes` (a power of two, at most a warp) lanes holds neighbouring packs
 // of one row; all lanes of the warp are here.  on: is the lane's row written at all?
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, int E = 8>
 __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int lanes,
-                                            const uint32_t (&w)[kPackWords<T>])
+                                            const uint32_t (&w)[kPackWords<T, E>])
 {
-    constexpr int N = kPackWords<T>;
+    constexpr int N = kPackWords<T, E>;
     if constexpr (WHOLE) {
-        if (on && n == 8)
+        if (on && n == E)
 #pragma unroll
             for (int i = 0; i < N; i += 4)
                 *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(p) + i) =
@@ -141,17 +141,19 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
         // chunk i holds elements [16 i / sizeof(T) - s, ...) of the pack
         constexpr int C = 16 / sizeof(T); // elements of a chunk
         unsigned char *const c = reinterpret_cast<unsigned char *>(p) - m;
-        int done = 0;                     // elements from the first on that are written
-        if (m > 0 && place == 0) {        // the chunk's first elements are not this lane's
+        const auto one = [&](int j) {
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t *>(p)[j] = w[j];
+            else
+                reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+        };
+        int done = 0;              // elements from the first on that are written
+        if (m > 0 && place == 0) { // the chunk's first elements are not this lane's
             done = min(n, C - s);
 #pragma unroll
             for (int j = 0; j < C; ++j)
-                if (j < done) {
-                    if constexpr (sizeof(T) == 4)
-                        reinterpret_cast<uint32_t *>(p)[j] = w[j];
-                    else
-                        reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
-                }
+                if (j < done)
+                    one(j);
         }
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
@@ -163,17 +165,13 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
             }
         }
         // the rest is the next lane's, which begins with it
-        if (m > 0 && n == 8 && done == 8 - s && place != lanes - 1 && next >= C - s)
+        if (m > 0 && n == E && done == E - s && place != lanes - 1 && next >= C - s)
             return;
         // (a chunk that the row ends in has elements of the lane before: it wrote them)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j >= done && j < n) {
-                if constexpr (sizeof(T) == 4)
-                    reinterpret_cast<uint32_t *>(p)[j] = w[j];
-                else
-                    reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
-            }
+        for (int j = 0; j < E; ++j)
+            if (j >= done && j < n)
+                one(j);
     }
 }
 

@@ -79,6 +79,35 @@ __device__ __forceinline__ Codes8 encode8(const float v[8], uint32_t top)
     return c;
 }
 
+// Is a block with this largest magnitude one that plain_codes8 cannot take: not finite,
+// subnormal or nearly so, or with a value that rounds past 127?
+__device__ __forceinline__ bool special_block(uint32_t top)
+{
+    return (top & 0x7fffffu) >= 0x7f0000u || top - (6u << 23) >= (249u << 23);
+}
+
+// encode8 of any other block.
+__device__ __forceinline__ Codes8 plain_codes8(const float v[8], uint32_t top)
+{
+    constexpr float kEnc = kMagic + 128.0f;
+    const float s = __uint_as_float((260u << 23) - (top & 0x7f800000u));
+    float2 t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        t[j] = __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), make_float2(s, s),
+                          make_float2(kEnc, kEnc));
+    Codes8 c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 a = t[2 * h], b = t[2 * h + 1];
+        c.w[h] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                             __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040),
+                             0x5410) ^
+                 0x80808080u;
+    }
+    return c;
+}
+
 // 2^e of a block's exponent byte (an infinity for a block that is not finite).
 __device__ __forceinline__ float block_scale(int8_t e)
 {
