@@ -461,6 +461,7 @@ class _Ops:
         self.lib = lib()
         self.dtypes = {torch.float32: RRA_F32, torch.float16: RRA_F16, torch.bfloat16: RRA_BF16}
         self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
+        self.i8 = torch.int8
         torch.cuda.init()
         # the plain C functions below torch.cuda's: a fifth of their time
         self.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -479,15 +480,16 @@ def _op(t, name, device, dtype=None, shape=None):
     """Address of a contiguous tensor on `device`, or None for None."""
     if t is None:
         return None
+    if t.get_device() == device and t.is_contiguous() and \
+            (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor")
     if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on the current device")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _op_dtype(ops, t) -> int:
@@ -671,9 +673,8 @@ class Saved:
     __slots__ = ("exps", "codes", "dim")
 
     def __init__(self, exps, codes, dim: int):
-        nb = -(-dim // BFP_BLOCK)
-        if exps.dim() != 2 or exps.shape[1] != nb or \
-                codes.shape != (exps.shape[0], nb * BFP_BLOCK):
+        nb, shape = -(-dim // BFP_BLOCK), exps.shape
+        if len(shape) != 2 or shape[1] != nb or codes.shape != (shape[0], nb * BFP_BLOCK):
             raise ValueError(f"Saved: expected exps (rows, {nb}) and codes (rows, "
                              f"{nb * BFP_BLOCK}) for rows of {dim} elements, got "
                              f"{tuple(exps.shape)} and {tuple(codes.shape)}")
@@ -687,13 +688,12 @@ class Saved:
         return cls(torch.empty(rows, nb, dtype=torch.int8, device=device),
                    torch.empty(rows, nb * BFP_BLOCK, dtype=torch.int8, device=device), dim)
 
-    def _at(self, name, device, rows, dim):
+    def _at(self, name, ops, device, rows, dim):
         """Addresses of exps and codes, for rows of dim elements."""
-        import torch
         if self.dim != dim or self.exps.shape[0] != rows:
             raise ValueError(f"{name}: expected {rows} saved rows of {dim} elements, got "
                              f"{self.exps.shape[0]} of {self.dim}")
-        return (_op(self.exps, name, device, torch.int8), _op(self.codes, name, device, torch.int8))
+        return _op(self.exps, name, device, ops.i8), _op(self.codes, name, device, ops.i8)
 
 
 def layer_norm_save(x, gamma, beta, y, saved: Saved, mean, rstd, eps: float = 1e-5, stream=None):
@@ -706,7 +706,7 @@ def layer_norm_save(x, gamma, beta, y, saved: Saved, mean, rstd, eps: float = 1e
     dev = ops.device()
     w = gamma if gamma is not None else beta if beta is not None else x
     wt = w.dtype
-    exps, codes = saved._at("saved", dev, rows, dim)
+    exps, codes = saved._at("saved", ops, dev, rows, dim)
     _check(ops.lib.rra_layer_norm_save(_op(x, "x", dev), _op(gamma, "gamma", dev, wt, (dim,)),
                                        _op(beta, "beta", dev, wt, (dim,)), rows, dim,
                                        _op_dtype(ops, x), _op_dtype(ops, w), eps,
@@ -727,7 +727,7 @@ def layer_norm_restore(saved: Saved, y, gamma=None, beta=None, mean=None, rstd=N
     dev = ops.device()
     w = gamma if gamma is not None else beta if beta is not None else y
     wt = w.dtype
-    exps, codes = saved._at("saved", dev, rows, dim)
+    exps, codes = saved._at("saved", ops, dev, rows, dim)
     _check(ops.lib.rra_layer_norm_restore(exps, codes, _op(mean, "mean", dev, ops.f32, (rows,)),
                                           _op(rstd, "rstd", dev, ops.f32, (rows,)),
                                           _op(gamma, "gamma", dev, wt, (dim,)),
@@ -749,7 +749,7 @@ def layer_norm_saved_grad(dy, saved: Saved, gamma, mean, rstd, dx, dgamma, dbeta
     w = gamma if gamma is not None else dgamma if dgamma is not None else \
         dbeta if dbeta is not None else dy
     wt = w.dtype
-    exps, codes = saved._at("saved", dev, rows, dim)
+    exps, codes = saved._at("saved", ops, dev, rows, dim)
     _check(ops.lib.rra_layer_norm_saved_grad(_op(dy, "dy", dev), exps, codes,
                                              _op(gamma, "gamma", dev, wt, (dim,)),
                                              _op(mean, "mean", dev, ops.f32, (rows,)),
@@ -773,10 +773,10 @@ def _act_code(act) -> int:
     return _ACTS[act]
 
 
-def _kept(t, name, device, dtype, shape, rows, ff):
+def _kept(t, name, ops, device, dtype, shape, rows, ff):
     """Addresses (exps, data) of gate or up: Saved, a tensor, or None."""
     if isinstance(t, Saved):
-        return t._at(name, device, rows, ff)
+        return t._at(name, ops, device, rows, ff)
     return None, _op(t, name, device, dtype, shape)
 
 
@@ -794,8 +794,8 @@ def gated_ff(x, w_gate, w_up, h, gate=None, up=None, act: str = "silu", stream=N
     dev = ops.device()
     ff = w_gate.shape[0]
     shape = x.shape[:-1] + (ff,)
-    gate_exps, gate_data = _kept(gate, "gate", dev, x.dtype, shape, rows, ff)
-    up_exps, up_data = _kept(up, "up", dev, x.dtype, shape, rows, ff)
+    gate_exps, gate_data = _kept(gate, "gate", ops, dev, x.dtype, shape, rows, ff)
+    up_exps, up_data = _kept(up, "up", ops, dev, x.dtype, shape, rows, ff)
     _check(ops.lib.rra_gated_ff(_op(x, "x", dev), _op(w_gate, "w_gate", dev, x.dtype, (ff, dim)),
                                 _op(w_up, "w_up", dev, x.dtype, (ff, dim)), rows, dim, ff,
                                 _op_dtype(ops, x), kind, _op(h, "h", dev, x.dtype, shape),
@@ -822,8 +822,8 @@ def gated_ff_grad(dh, x, w_gate, w_up, gate, up, dgate, dup, dx=None, dw_gate=No
     dim, t = w_gate.shape[1], dh.dtype
     if isinstance(gate, Saved) != isinstance(up, Saved):
         raise TypeError("gate, up: expected both Saved or both tensors")
-    gate_exps, gate_data = _kept(gate, "gate", dev, t, dh.shape, rows, ff)
-    up_exps, up_data = _kept(up, "up", dev, t, dh.shape, rows, ff)
+    gate_exps, gate_data = _kept(gate, "gate", ops, dev, t, dh.shape, rows, ff)
+    up_exps, up_data = _kept(up, "up", ops, dev, t, dh.shape, rows, ff)
     dw = dw_gate if dw_gate is not None else dw_up if dw_up is not None else dh
     dt, wide = dw.dtype, dh.shape[:-1] + (dim,)
     _check(ops.lib.rra_gated_ff_grad(_op(dh, "dh", dev), _op(x, "x", dev, t, wide),

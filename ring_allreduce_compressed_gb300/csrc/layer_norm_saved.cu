@@ -168,13 +168,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
     const long long step = (long long)gridDim.x * groups;
     dependents_wait();
     dependents_launch();
-    uint32_t ahead[K][N];
+    uint32_t ahead[K][N] = {}; // (what is not there stays zero)
     const auto read = [&](long long base) {
         // every lane takes part in the sums, some in vain: they read the last row
         const T *const p = x + min(base + (MULTI ? 0 : first), a.rows - 1) * dim + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            load_words<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
+            if (there[k] > 0)
+                load_words<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
     };
     long long base = (long long)blockIdx.x * groups;
     read(base);
@@ -228,6 +229,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
         // (one question a row: asked for every pack, its ways apart cost more than the codes)
         const bool plain = !__any_sync(kFull, special);
         int8_t *const codes = a.codes + (r * packs + u0) * kPack;
+        int8_t *const exps = a.exps + r * nb + u0 / kBlockPacks;
+        const auto save_codes = [&](auto encode) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = element<T>(w[k], j);
+                if (on && u0 + k * (gap / kPack) < packs) {
+                    store_codes(codes + k * gap, encode(v, top[k]));
+                    if (li % kBlockPacks == 0)
+                        exps[k * gap / kBlock] = exponent_byte(block_exponent(top[k]));
+                }
+            }
+        };
+        if (plain)
+            save_codes([](const float *v, uint32_t t) { return plain_codes8(v, t); });
+        else
+            save_codes([](const float *v, uint32_t t) { return encode8(v, t); });
         T *const to = y + r * dim + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -236,11 +256,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = element<T>(w[k], j);
-            if (on && u < packs) {
-                store_codes(codes + k * gap, plain ? plain_codes8(v, top[k]) : encode8(v, top[k]));
-                if (u % kBlockPacks == 0)
-                    a.exps[r * nb + u / kBlockPacks] = exponent_byte(block_exponent(top[k]));
-            }
             Pair g[4], b[4];
             if (WHOLE) {
                 // (behind the row: its first weights, for nothing)
