@@ -23,17 +23,23 @@ import ring_allreduce_compressed_gb300 as rra  # noqa: E402
 class Model:
     """Weights, and one rank's buffers for activations and gradients."""
 
-    def __init__(self, vocab, dim, tokens, ranks, seed=0):
+    def __init__(self, vocab, dim, tokens, ranks, seed=0, ff=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
-        self.vocab, self.dim, self.tokens, self.ranks = vocab, dim, tokens, ranks
+        self.vocab, self.dim, self.tokens, self.ranks, self.ff = vocab, dim, tokens, ranks, ff
         self.scale = math.sqrt(dim)
         self.table = torch.randn(vocab, dim, generator=g, device="cuda") * 0.02
-        # gamma, beta and the head's weight in one flat bucket
-        n = 2 * dim + vocab * dim
+        # gamma, beta and the head's weight in one flat bucket; the block's behind them
+        n = 2 * dim + vocab * dim + 3 * ff * dim
         self.bucket = torch.zeros(n, device="cuda")
         self.gamma, self.beta, self.head = self.views(self.bucket)
         self.gamma.fill_(1.0)
         self.head.copy_(torch.randn(vocab, dim, generator=g, device="cuda") * 0.02)
+        if ff:
+            for w, fan in zip(self.block(self.bucket), (dim, dim, ff)):
+                w.copy_(torch.randn(w.shape, generator=g, device="cuda") / math.sqrt(fan))
+            self.saved = rra.Saved.empty(tokens, dim)
+            self.gate, self.up = (rra.Saved.empty(tokens, ff) for _ in range(2))
+            self.h, self.dh, self.dup = (torch.empty(tokens, ff, device="cuda") for _ in range(3))
         self.x = torch.empty(tokens, dim, device="cuda")
         self.y = torch.empty_like(self.x)
         self.mean, self.rstd = (torch.empty(tokens, device="cuda") for _ in range(2))
@@ -44,23 +50,57 @@ class Model:
 
     def views(self, bucket):
         d = self.dim
-        return bucket[:d], bucket[d:2 * d], bucket[2 * d:].view(self.vocab, d)
+        return bucket[:d], bucket[d:2 * d], bucket[2 * d:(2 + self.vocab) * d].view(self.vocab, d)
+
+    def block(self, bucket):
+        """The feed-forward block's gate, up (ff, dim) and down (dim, ff) weights."""
+        d, n = self.dim, self.ff * self.dim
+        gate, up, down = bucket[(2 + self.vocab) * d:].split(n)
+        return gate.view(self.ff, d), up.view(self.ff, d), down.view(d, self.ff)
+
+    def forward(self, inputs):
+        """What the head scores."""
+        rra.embedding(self.table, inputs, self.x, scale=self.scale)
+        if not self.ff:
+            rra.layer_norm(self.x, self.gamma, self.beta, self.y, self.mean, self.rstd)
+            return self.y
+        rra.layer_norm_save(self.x, self.gamma, self.beta, self.y, self.saved, self.mean, self.rstd)
+        gate, up, down = self.block(self.bucket)
+        rra.gated_ff(self.y, gate, up, self.h, self.gate, self.up)
+        return torch.addmm(self.y, self.h, down.t())
+
+    def backward(self, rank, dy):
+        """From the gradient of forward's result: into x's, in dy's place, and the weights'."""
+        dgamma, dbeta, _ = self.views(self.dbucket[rank])
+        if not self.ff:
+            rra.layer_norm_grad(dy, self.x, self.gamma, self.mean, self.rstd, dy, dgamma, dbeta)
+            return
+        gate, up, down = self.block(self.bucket)
+        dgate, dup, ddown = self.block(self.dbucket[rank])
+        torch.mm(dy, down, out=self.dh)
+        # y and h again, out of 8 bits
+        rra.layer_norm_restore(self.saved, self.y, self.gamma, self.beta, self.mean, self.rstd)
+        dnorm = torch.empty_like(dy)
+        rra.gated_ff_grad(self.dh, self.y, gate, up, self.gate, self.up, self.dh, self.dup,
+                          dx=dnorm, dw_gate=dgate, dw_up=dup, h=self.h)
+        torch.mm(dy.t(), self.h, out=ddown)
+        dy += dnorm
+        rra.layer_norm_saved_grad(dy, self.saved, self.gamma, self.mean, self.rstd, dy, dgamma,
+                                  dbeta)
 
     def rank_gradients(self, rank, inputs, targets):
         """Forward and backward pass of one rank; returns its loss."""
-        rra.embedding(self.table, inputs, self.x, scale=self.scale)
-        rra.layer_norm(self.x, self.gamma, self.beta, self.y, self.mean, self.rstd)
-        logits = self.y @ self.head.t()
+        y = self.forward(inputs)
+        logits = y @ self.head.t()
         logp = torch.log_softmax(logits, 1)
         at = torch.arange(self.tokens, device="cuda")
         loss = -logp[at, targets].mean()
         dlogits = logp.exp()
         dlogits[at, targets] -= 1
         dlogits /= self.tokens
-        dgamma, dbeta, dhead = self.views(self.dbucket[rank])
-        torch.mm(dlogits.t(), self.y, out=dhead)
+        torch.mm(dlogits.t(), y, out=self.views(self.dbucket[rank])[2])
         dy = dlogits @ self.head
-        rra.layer_norm_grad(dy, self.x, self.gamma, self.mean, self.rstd, dy, dgamma, dbeta)
+        self.backward(rank, dy)
         rra.embedding_grad(dy, inputs, self.dtable[rank], scale=self.scale)
         return loss
 
@@ -88,8 +128,9 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--ranks", type=int, default=4)
+    ap.add_argument("--ff", type=int, default=0, help="width of the feed-forward block (0: none)")
     a = ap.parse_args()
-    m = Model(vocab=512, dim=256, tokens=1024, ranks=a.ranks)
+    m = Model(vocab=512, dim=256, tokens=1024, ranks=a.ranks, ff=a.ff)
     for s in range(a.steps):
         loss = m.step([batch(m, s, r) for r in range(a.ranks)], lr=2.0, max_norm=1.0)
         if s % 5 == 0 or s == a.steps - 1:

@@ -420,82 +420,85 @@ __global__ void __launch_bounds__(kRestoreThreads, 2) restore_kernel(const Resto
     T *const y = static_cast<T *>(a.y);
     const long long nb = blocks_of(a.dim), width = nb * kBlock;
     const int groups = kRestoreThreads / a.lanes, mine = threadIdx.x / a.lanes;
-    const long long c0 = (long long)blockIdx.y * kRestoreCols + threadIdx.x % a.lanes * E;
     const long long step = (long long)gridDim.x * groups;
     const auto in = [&](long long c) { return (int)max(0LL, min((long long)E, a.dim - c)); };
-    const int there = in(c0), next = in(c0 + E);
     dependents_wait();
     dependents_launch();
-    Pair g[E / 2], b[E / 2];
+    for (long long first = (long long)blockIdx.y * kRestoreCols; first < a.dim;
+         first += (long long)gridDim.y * kRestoreCols) {
+        const long long c0 = first + threadIdx.x % a.lanes * E;
+        const int there = in(c0), next = in(c0 + E);
+        Pair g[E / 2], b[E / 2];
 #pragma unroll
-    for (int h = 0; h < E; h += 8) {
-        const int n = max(0, min(8, there - h));
-        float t[8];
-        weights8<W, WHOLE>(gamma, c0 + h, n, 1.0f, t);
+        for (int h = 0; h < E; h += 8) {
+            const int n = max(0, min(8, there - h));
+            float t[8];
+            weights8<W, WHOLE>(gamma, c0 + h, n, 1.0f, t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            g[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
-        weights8<W, WHOLE>(beta, c0 + h, n, 0.0f, t);
+            for (int j = 0; j < 4; ++j)
+                g[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
+            weights8<W, WHOLE>(beta, c0 + h, n, 0.0f, t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            b[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
-    }
-    // the rows of a block's groups go on together: whole warps store
-    for (long long base = (long long)blockIdx.x * groups; base < a.rows; base += R * step) {
-        uint4 c[R];
-        int8_t e[R];
-        float mu[R], rs[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const long long r = base + i * step + mine;
-            const bool on = r < a.rows && there > 0;
-            c[i] = make_uint4(0u, 0u, 0u, 0u);
-            e[i] = 0;
-            mu[i] = 0.0f;
-            rs[i] = 1.0f;
-            if (on) {
-                c[i] = *reinterpret_cast<const uint4 *>(a.codes + r * width + c0);
-                e[i] = a.exps[r * nb + c0 / kBlock];
-                if (a.mean)
-                    mu[i] = a.mean[r];
-                if (a.rstd)
-                    rs[i] = a.rstd[r];
-            }
+            for (int j = 0; j < 4; ++j)
+                b[h / 2 + j] = pair_of(t[2 * j], t[2 * j + 1]);
         }
+        // the rows of a block's groups go on together: whole warps store
+        long long r = (long long)blockIdx.x * groups + mine; // to read, and to write
+        const int8_t *codes = a.codes + r * width + c0, *exps = a.exps + r * nb + c0 / kBlock;
+        T *to = y + r * a.dim + c0;
+        const long long codes_step = step * width, exps_step = step * nb, to_step = step * a.dim;
+        for (long long base = (long long)blockIdx.x * groups; base < a.rows; base += R * step) {
+            uint4 c[R];
+            int8_t e[R];
+            float mu[R], rs[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const long long r = base + i * step + mine;
-            const Pair minus = pair_of(-mu[i], -mu[i]), scale = pair_of(rs[i], rs[i]);
-            const float s = block_scale(e[i]);
-            const Pair unit = pair_of(s, s);
-            uint32_t o[kPackWords<T, E>];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 f[4];
-                fractions8(h ? Codes8{{c[i].z, c[i].w}} : Codes8{{c[i].x, c[i].y}}, f);
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    halves(fma(mul(fma(pair_of(f[j].x, f[j].y), unit, minus), scale), g[4 * h + j],
-                               b[4 * h + j]),
-                           v[2 * j], v[2 * j + 1]);
-                uint32_t w[kPackWords<T>];
-                to_words<T>(v, w);
-#pragma unroll
-                for (int j = 0; j < kPackWords<T>; ++j)
-                    o[h * kPackWords<T> + j] = w[j];
+            for (int i = 0; i < R; ++i, codes += codes_step, exps += exps_step) {
+                const long long at = r + i * step;
+                c[i] = make_uint4(0u, 0u, 0u, 0u);
+                e[i] = 0;
+                mu[i] = 0.0f;
+                rs[i] = 1.0f;
+                if (at < a.rows && there > 0) {
+                    c[i] = *reinterpret_cast<const uint4 *>(codes);
+                    e[i] = *exps;
+                    if (a.mean)
+                        mu[i] = a.mean[at];
+                    if (a.rstd)
+                        rs[i] = a.rstd[at];
+                }
             }
-            if constexpr (WHOLE) { // (8 elements, or 16)
-                if (r < a.rows)
 #pragma unroll
-                    for (int j = 0; j < kPackWords<T, E>; j += 4)
-                        if (j * 4 < there * (int)sizeof(T))
-                            *reinterpret_cast<uint4 *>(
-                                reinterpret_cast<uint32_t *>(y + r * a.dim + c0) + j) =
-                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-            } else {
-                store_words<T, false, E>(y + r * a.dim + c0, there, next, r < a.rows,
-                                         min(a.lanes, 32), o);
+            for (int i = 0; i < R; ++i, r += step, to += to_step) {
+                const Pair minus = pair_of(-mu[i], -mu[i]), scale = pair_of(rs[i], rs[i]);
+                const float s = block_scale(e[i]);
+                const Pair unit = pair_of(s, s);
+                uint32_t o[kPackWords<T, E>];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 f[4];
+                    fractions8(h ? Codes8{{c[i].z, c[i].w}} : Codes8{{c[i].x, c[i].y}}, f);
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        halves(fma(mul(fma(pair_of(f[j].x, f[j].y), unit, minus), scale), g[4 * h + j],
+                                   b[4 * h + j]),
+                               v[2 * j], v[2 * j + 1]);
+                    uint32_t w[kPackWords<T>];
+                    to_words<T>(v, w);
+#pragma unroll
+                    for (int j = 0; j < kPackWords<T>; ++j)
+                        o[h * kPackWords<T> + j] = w[j];
+                }
+                if constexpr (WHOLE) { // (8 elements, or 16)
+                    if (r < a.rows)
+#pragma unroll
+                        for (int j = 0; j < kPackWords<T, E>; j += 4)
+                            if (j * 4 < there * (int)sizeof(T))
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(to) + j) =
+                                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                } else {
+                    store_words<T, false, E>(to, there, next, r < a.rows, min(a.lanes, 32), o);
+                }
             }
         }
     }
@@ -507,9 +510,7 @@ template <typename T, typename W> rra_status restore(Restore a, cudaStream_t st)
     while (a.lanes < kRestoreThreads && a.lanes * kRestorePack < a.dim)
         a.lanes *= 2;
     const int rows = kRestoreThreads / a.lanes * kRestoreRows; // of a block at a time
-    const long long cols = (a.dim + kRestoreCols - 1) / kRestoreCols;
-    if (cols > 65535) // (rows of 2^28 elements and more)
-        return RRA_ERR_UNSUPPORTED;
+    const long long cols = std::min((a.dim + kRestoreCols - 1) / kRestoreCols, 65535LL);
     const long long blocks = std::max(1LL, num_sms() * 8LL / cols);
     const dim3 grid((unsigned)std::min((a.rows + rows - 1) / rows, blocks), (unsigned)cols);
     return launched(whole_packs<T>(a.dim, {a.y, a.gamma, a.beta})

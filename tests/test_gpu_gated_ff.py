@@ -375,3 +375,138 @@ def test_ff_on_a_stream_and_in_a_graph(t, rows, dim, ff):
         torch.cuda.synchronize()
         for o, f in zip(outs, first):
             assert torch.equal(o, f)
+
+
+# ---------------------------------------------------------------- few tiles, many slices
+
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,dim,ff", [(300, 2056, 130), (20, 4096, 264), (65, 1000, 129),
+                                         (257, 8192, 64), (70, 385, 257)])
+def test_ff_split_along_k(rows, dim, ff, t):
+    """Few results of long sums."""
+    x, w = randn((rows, dim), 1, 1.0, t), weights(dim, ff, t)
+    h, _ = check_ff(x, *w, keep="bits8", name="gelu_tanh")
+    again, _ = check_ff(x, *w, keep="full", name="gelu_tanh")
+    assert torch.equal(h, again)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,ff", [(40, 72, 5000), (300, 500, 2064), (5000, 72, 40),
+                                         (2100, 264, 130), (129, 130, 131)])
+def test_ff_grad_split_along_k(rows, dim, ff, t):
+    dh, x, w, kept = grad_inputs(rows, dim, ff, t, "bits8")
+    first = check_ff_grad(dh, x, w, kept)
+    for _ in range(3):
+        again = check_ff_grad(dh, x, w, kept)
+        assert torch.equal(first[3], again[3])
+        for a, b in zip(first[4], again[4]):
+            assert torch.equal(a, b)
+
+
+def test_ff_of_sizes_around_the_tiles():
+    """Every remainder that an end of a tile, of a slice, of a block of codes can have."""
+    for rows in (31, 65, 127, 129, 255, 257, 385):
+        for dim, ff in ((63, 127), (64, 128), (65, 129), (72, 136), (128, 264), (200, 392)):
+            x, w = randn((rows, dim), rows, 1.0, "bf16"), weights(dim, ff, "bf16")
+            check_ff(x, *w, keep="bits8" if (rows + ff) % 2 else "full")
+
+
+@pytest.mark.parametrize("keep", ["full", "bits8"])
+def test_ff_beyond_32_bits(keep):
+    """More than 2^31 elements of h, whose last rows alone are not zero."""
+    rows, dim, ff = 131_100, 64, 16_384
+    x = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = randn((3, dim), 1, 1.0, "bf16")
+    w = weights(dim, ff, "bf16")
+    h = torch.full((rows, ff), 9.0, dtype=torch.bfloat16, device="cuda")
+    kept = [rra.Saved.empty(rows, ff) if keep == "bits8" else torch.full_like(h, 9.0)
+            for _ in range(2)]
+    rra.gated_ff(x, *w, h, *kept)
+    tail = torch.empty(300, ff, dtype=torch.bfloat16, device="cuda")
+    rra.gated_ff(x[-300:], *w, tail)
+    assert torch.equal(h[-300:], tail) and int(torch.count_nonzero(h[:-3])) == 0
+    dh = torch.zeros_like(h)
+    dh[-3:] = randn((3, ff), 4, 0.1, "bf16")
+    dx, dw = torch.full_like(x, 9.0), [torch.full_like(v, 9.0) for v in w]
+    rra.gated_ff_grad(dh, x, *w, *kept, dh, h, dx=dx, dw_gate=dw[0], dw_up=dw[1])
+    g, u = (values(k)[-3:] if keep == "bits8" else k[-3:].double() for k in
+            ([rra.Saved(k.exps[-3:], k.codes[-3:], ff) if keep == "bits8" else k for k in kept]))
+    d = randn((3, ff), 4, 0.1, "bf16").double()
+    a, slope, _ = act("silu", g)
+    close(h[-3:], d * a, rounded(d * a, h.dtype, d.abs() * act_errors("silu", g)[0]
+                                 + 3 * U * (d * a).abs()), "dup")
+    for k, part in enumerate((dh, h)):
+        want = part[-3:].double().t() @ x[-3:].double()
+        close(dw[k], want, rounded(want, dw[k].dtype, products(
+            11, part[-3:].double().abs().t() @ x[-3:].double().abs())), "dw")
+    assert int(torch.count_nonzero(dx[:-3])) == 0 and torch.isfinite(dx[-3:]).all()
+
+
+# ---------------------------------------------------------------- streams, scratch
+
+def test_ff_scratch_does_not_grow_during_a_capture():
+    st = torch.cuda.Stream()
+    x, w = randn((100, 999), 1), weights(999, 2001, "f32")  # operands laid out anew
+    h, mark = torch.empty(100, 2001, device="cuda"), torch.zeros(1, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        with pytest.raises(rra.RRAError) as e:
+            rra.gated_ff(x, *w, h)
+        assert e.value.code == rra.RRA_ERR_INVALID
+        mark.add_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(mark) == 1.0
+
+
+def test_ff_on_two_streams_at_once():
+    """Calls that use scratch (copies of operands, splits) side by side."""
+    cases = []
+    for k, (rows, dim, ff, t) in enumerate([(300, 2056, 130, "bf16"), (200, 999, 257, "f32"),
+                                            (40, 72, 5000, "bf16"), (333, 513, 301, "f16")]):
+        dh, x, w, kept = grad_inputs(rows, dim, ff, t, "bits8")
+        outs = [torch.empty_like(dh) for _ in range(3)] + [torch.empty_like(x)] + \
+            [torch.empty_like(v) for v in w]
+        cases.append((dh, x, w, kept, outs))
+
+    def call(case, st=None):
+        dh, x, w, kept, outs = case
+        rra.gated_ff(x, *w, outs[0], stream=st)
+        rra.gated_ff_grad(dh, x, *w, *kept, outs[1], outs[2], dx=outs[3], dw_gate=outs[4],
+                          dw_up=outs[5], stream=st)
+    want = []
+    for c in cases:
+        call(c)
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in c[4]])
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(10):
+        for c in cases:
+            for o in c[4]:
+                o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for c, st in zip(cases, streams):
+                call(c, st)
+        torch.cuda.synchronize()
+        for c, ws in zip(cases, want):
+            for o, v in zip(c[4], ws):
+                assert torch.equal(o, v)
+
+
+def test_ff_calls_behind_one_another_and_behind_their_inputs_writers():
+    """Inputs written right before the call on its stream, outputs read right behind it."""
+    for rows, dim, ff, t in ((1, 2048, 4096, "bf16"), (300, 520, 1032, "bf16"), (33, 65, 129, "f32")):
+        x, w = randn((rows, dim), 1, 1.0, t), weights(dim, ff, t)
+        want = [torch.empty(rows, ff, dtype=DT[t], device="cuda") for _ in range(2)]
+        other = randn((rows, dim), 9, 1.0, t)
+        for v, o in zip((x, other), want):
+            rra.gated_ff(v, *w, o)
+            torch.cuda.synchronize()
+        inp, h, seen = torch.empty_like(x), torch.empty_like(want[0]), []
+        for k in range(20):
+            inp.copy_(x if k % 2 == 0 else other)
+            rra.gated_ff(inp, *w, h)
+            seen.append(h.clone())
+        for k, s in enumerate(seen):
+            assert torch.equal(s, want[k % 2])
