@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs 
     for (long long base = (long long)blockIdx.x * groups; base < a.rows;
          base += (long long)gridDim.x * groups) {
         const long long r = base + threadIdx.x / lanes;
+#pragma unroll 2
         for (long long u0 = 0; u0 < packs; u0 += lanes) {
             const long long u = u0 + li, at = r * a.ff + u * kPack;
             const bool on = r < a.rows;
@@ -247,7 +248,6 @@ rra_status stalled_status()
     if (!*w)
         return RRA_OK;
     *w = 0;
-    op_scratch_spoilt();
     return RRA_ERR_TIMEOUT;
 }
 

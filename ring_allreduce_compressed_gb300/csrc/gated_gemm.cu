@@ -61,8 +61,7 @@ struct Gemm {
     Kept gate, up;
     int accumulate;
     int first_out;      // kDw: the output of the first tiles
-    float *parts;       // more than one split: [tile][split][block of the pair][64][128][4]
-    unsigned *arrivals; // [tile][block of the pair], zero before and after
+    float *parts; // more than one split: sums, [tile][split][256 rows][256 columns]
     unsigned *stalled;
 };
 
@@ -179,7 +178,7 @@ __device__ __forceinline__ void floats(const uint32_t (&r)[N], int i, float (&v)
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], summed[2], written[2];
-    uint32_t tmem, stop, last;
+    uint32_t tmem, stop;
     uint32_t top[2][2][kHalf]; // gate, up; half; row
     float stage[kWriters][32 * kStageRow];
 };
@@ -299,74 +298,24 @@ __device__ __forceinline__ void take_sums(uint32_t from, uint32_t to, int first,
     tmem_stored();
 }
 
-// This item's sums to memory.  In the block that is the last of its tile's splits to
-// get here: all of them added, in the order of the splits, back in tensor memory, and
-// true.  Lane by lane of row `row` (there: one of the output's), 128 columns from
-// `first` on.
-__device__ __forceinline__ bool join_splits(const Gemm &g, Shared &s, const Item &t, uint32_t rank,
-                                            uint32_t at, int row, int first, bool there)
+// A warp's sums of an item (128 columns from `first` on; `there`: the lane's row is one of
+// the output's) to memory, for finish_kernel.
+__device__ __forceinline__ void write_part(const Gemm &g, const Item &t, uint32_t at, int row,
+                                           int first, bool there)
 {
-    constexpr long long kPart = (long long)kHalf * kSide; // floats of a block
-    float *const tile = g.parts + ((long long)t.tile * g.splits * 2 + rank) * kPart;
-    float4 *const mine = reinterpret_cast<float4 *>(tile + t.split * 2 * kPart);
+    float *const to = g.parts + (((long long)t.tile * g.splits + t.split) * kSide + row) * kSide;
 #pragma unroll 1
     for (int c = first; c < first + kHalf; c += 32) {
         uint32_t v[32];
         tmem_load(at + c, v);
         tmem_loaded();
 #pragma unroll
-        for (int j = 0; there && j < 32; j += 4)
-            mine[(c + j) / 4 * kHalf + row] =
-                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                            __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+        for (int j = 0; there && j < 32; j += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + j),
+                         "r"(v[j]), "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3]), "r"(v[j + 4]),
+                         "r"(v[j + 5]), "r"(v[j + 6]), "r"(v[j + 7])
+                         : "memory");
     }
-    __threadfence();
-    named_barrier(1, 32 * kWriters);
-    unsigned *const count = g.arrivals + t.tile * 2 + rank;
-    if (threadIdx.x == 64) {
-        s.last = atomicAdd(count, 1u) == (unsigned)g.splits - 1;
-        if (s.last)
-            *count = 0;
-    }
-    named_barrier(1, 32 * kWriters);
-    const bool last = s.last;
-    named_barrier(1, 32 * kWriters); // (read before the next item's)
-    if (!last)
-        return false;
-    __threadfence();
-#pragma unroll 1
-    for (int c = first; c < first + kHalf; c += 16) {
-        constexpr int kAhead = 4; // splits whose parts are on their way
-        uint32_t v[16];
-        float sum[16] = {};
-#pragma unroll 1
-        for (int k0 = 0; k0 < g.splits; k0 += kAhead) {
-            float4 q[kAhead][4];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const float4 *const p =
-                    reinterpret_cast<const float4 *>(tile + (k0 + k) * 2 * kPart) +
-                    c / 4 * kHalf + row;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    q[k][j] = there && k0 + k < g.splits ? __ldcg(p + j * kHalf)
-                                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum[4 * j] += q[k][j].x, sum[4 * j + 1] += q[k][j].y;
-                    sum[4 * j + 2] += q[k][j].z, sum[4 * j + 3] += q[k][j].w;
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            v[j] = __float_as_uint(sum[j]);
-        tmem_store(at + c, v);
-    }
-    tmem_stored();
-    return true;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -540,14 +489,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             const int row = quarter * 32 + lane;
             const long long r0 = p.m0 + rank * kHalf + quarter * 32;
             float *const stage = s.stage[warp - 2];
-            bool mine = true;
-            if (g.splits > 1)
-                mine = join_splits(g, s, it, rank, at, row, half * kHalf, r0 + lane < g.m);
-            if (mine) {
+            if (g.splits > 1) {
+                write_part(g, it, at, rank * kHalf + row, half * kHalf, r0 + lane < g.m);
+            } else {
                 O *const out = static_cast<O *>(g.out[p.which]);
                 const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 32);
                 if (MODE == kForward) {
-                    if (F32 || g.splits > 1) { // a half has columns that the other has stored
+                    if (F32) { // a half has columns whose sums the other has stored
                         tc_fence_before();
                         named_barrier(2 + quarter, 64);
                         tc_fence_after();
@@ -575,6 +523,117 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 }
 
 constexpr int kGemmSmem = kStages * kStageBytes + 1024 + (int)sizeof(Shared);
+
+// ---------------------------------------------------------------- splits
+
+// The sums of a tile's splits added, in their order, and on to where they go: a warp has
+// a row of a tile, a lane 4 of its first 128 columns and the same 4 of its last.  (A
+// launch of its own, with all of the GPU: the last of a tile's splits to end took 10 us
+// for it.)
+constexpr int kFinishThreads = 256;
+
+template <typename O>
+__device__ __forceinline__ void put4(O *p, long long there, bool whole, const float v[4])
+{
+    if (whole && there >= 4) {
+        Pack<O, 4> q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            q.e[j] = from_f32<O>(v[j]);
+        store_pack<O, 4>(p, q);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < there)
+            p[j] = from_f32<O>(v[j]);
+}
+
+template <typename T>
+__device__ __forceinline__ void keep4(const Kept &to, long long r, long long n0, long long n,
+                                      bool whole, const float v[4])
+{
+    const int c = threadIdx.x % 32 * 4;
+    if (to.exps) { // (all of the warp is here)
+        float w[8] = {};
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = v[j];
+            top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+        }
+        top = __reduce_max_sync(kFull, top);
+        const long long b = r * blocks_of(n) + n0 / kBlock;
+        *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(to.data) + b * kBlock + c) =
+            encode8(w, top).w[0];
+        if (c == 0)
+            to.exps[b] = exponent_byte(block_exponent(top));
+    } else if (to.data) {
+        put4(static_cast<T *>(to.data) + r * n + n0 + c, n - n0 - c, whole, v);
+    }
+}
+
+template <typename T, typename O, int MODE>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Gemm g)
+{
+    constexpr int kWarps = kFinishThreads / 32, kAhead = 4; // splits on their way
+    const int c = threadIdx.x % 32 * 4;
+    dependents_wait();
+    dependents_launch();
+    for (long long i = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
+         i < (long long)g.tiles * kSide; i += (long long)gridDim.x * kWarps) {
+        const int tile = (int)(i / kSide), row = (int)(i % kSide);
+        const TilePlace p = tile_place<MODE>(g, tile);
+        const long long r = p.m0 + row;
+        if (r >= g.m)
+            continue;
+        const float *const from = g.parts + ((long long)tile * g.splits * kSide + row) * kSide + c;
+        float v[2][4] = {};
+        for (int k0 = 0; k0 < g.splits; k0 += kAhead) {
+            float4 q[kAhead][2];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    q[k][h] = k0 + k < g.splits
+                                  ? __ldcs(reinterpret_cast<const float4 *>(
+                                        from + (long long)(k0 + k) * kSide * kSide + h * kHalf))
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[h][0] += q[k][h].x, v[h][1] += q[k][h].y;
+                    v[h][2] += q[k][h].z, v[h][3] += q[k][h].w;
+                }
+        }
+        O *const out = static_cast<O *>(g.out[p.which]);
+        const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 4 * sizeof(O));
+        if constexpr (MODE == kForward) {
+            const bool kept = whole && (g.gate.exps || aligned_to(g.gate.data, 4 * sizeof(T))) &&
+                              (g.up.exps || aligned_to(g.up.data, 4 * sizeof(T)));
+            keep4<T>(g.gate, r, p.n0, g.n, kept, v[0]);
+            keep4<T>(g.up, r, p.n0, g.n, kept, v[1]);
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = act_of<sizeof(T) == 4>(g.act, v[0][j]) * v[1][j];
+            put4(out + r * g.n + p.n0 + c, g.n - p.n0 - c, whole, h);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const long long col = p.n0 + h * kHalf + c;
+                O *const to = out + r * g.n + col;
+                if (g.accumulate)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + j < g.n)
+                            v[h][j] += to_f32(to[j]);
+                put4(to, g.n - col, whole, v[h]);
+            }
+        }
+    }
+}
 
 // ---------------------------------------------------------------- host
 
@@ -668,7 +727,12 @@ template <typename T, typename O, int MODE> cudaError_t launch_gemm(Gemm &g, cud
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fn, g);
+    if ((e = cudaLaunchKernelEx(&cfg, fn, g)) != cudaSuccess || g.splits == 1)
+        return e;
+    const long long rows = (long long)g.tiles * kSide, warps = kFinishThreads / 32;
+    return launch_chained(finish_kernel<T, O, MODE>,
+                          dim3((unsigned)std::min((rows + warps - 1) / warps, num_sms() * 8LL)),
+                          kFinishThreads, st, g);
 }
 
 // Tiles, slices and splits of a product: m x n results (of each output), `total` slices
@@ -679,9 +743,9 @@ struct Plan {
     size_t bytes; // of parts
 };
 
-// Few tiles with many slices are split along k.  The time of a launch in steps, by
-// measurement: a slice takes 0.28 us a pair, an item 3 us to write out, the last of a
-// tile's splits 3 us and 0.6 more a split to join them.
+// Few tiles with many slices are split along k.  The time of a launch in steps, as
+// measured: a slice takes 0.28 us a pair, an item 3 us to write out, adding up the splits
+// 4 us and 0.2 more for each.
 Plan plan_of(long long m, long long n, int outputs, long long step_n, long long total, bool f32)
 {
     Plan p = {};
@@ -695,15 +759,13 @@ Plan plan_of(long long m, long long n, int outputs, long long step_n, long long 
     const int pairs = resident_pairs();
     const double slice = 0.28 * (f32 ? kProducts<true> : 1);
     double best = 0;
-    for (int s = 1; s <= 32 && (s == 1 || (2 * p.tiles <= (int)(kScratchHead / sizeof(unsigned)) &&
-                                           p.tiles * s <= pairs));
-         ++s) {
+    for (int s = 1; s <= 64 && (s == 1 || p.tiles * s <= 2 * pairs); ++s) {
         const int per = (int)((total + s - 1) / s);
         // (a split has some slices, and none is empty)
         if (s > 1 && (per * (f32 ? kProducts<true> : 1) < 4 || (long long)per * (s - 1) >= total))
             continue;
         const double t = (double)((p.tiles * s + pairs - 1) / pairs) * (per * slice + 3) +
-                         (s > 1 ? 3 + 0.6 * s : 0);
+                         (s > 1 ? 4 + 0.2 * s : 0);
         if (s == 1 || t < best) {
             best = t;
             p.splits = s;
@@ -711,7 +773,7 @@ Plan plan_of(long long m, long long n, int outputs, long long step_n, long long 
         }
     }
     if (p.splits > 1)
-        p.bytes = (size_t)p.tiles * p.splits * 2 * kHalf * kSide * sizeof(float);
+        p.bytes = (size_t)p.tiles * p.splits * kSide * kSide * sizeof(float);
     return p;
 }
 
@@ -730,7 +792,7 @@ Plan plan_dw(const FfGradArgs &a, bool f32)
     return plan_of(a.ff, a.dim, a.dwg && a.dwu ? 2 : 1, kSide, slices_of(a.rows), f32);
 }
 
-// g's tiles by the plan; scratch: the stream's, parts behind its head.
+// g's tiles by the plan; parts: where they are in the stream's scratch.
 bool use_plan(Gemm &g, const Plan &p, long long slices, unsigned char *scratch, size_t parts_at)
 {
     g.tiles_m = p.tiles_m;
@@ -739,10 +801,8 @@ bool use_plan(Gemm &g, const Plan &p, long long slices, unsigned char *scratch, 
     g.slices = (int)slices;
     g.splits = p.splits;
     g.per_split = p.per_split;
-    if (p.splits > 1) {
-        g.arrivals = reinterpret_cast<unsigned *>(scratch);
+    if (p.splits > 1)
         g.parts = reinterpret_cast<float *>(scratch + parts_at);
-    }
     return p.ok;
 }
 

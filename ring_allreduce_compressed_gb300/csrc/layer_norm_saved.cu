@@ -351,8 +351,11 @@ template <typename T, typename W, int K, bool MULTI, bool WHOLE, int THREADS>
 cudaError_t save_launch(const Save &a, cudaStream_t st)
 {
     const int threads = MULTI ? 32 * a.g.warps : kSaveThreads, rows = threads / a.g.lanes();
+    // one wave of blocks, for the rows that they have ahead (16384 x 4096 bf16: 60 us, 62
+    // with three waves)
+    const int per_sm = std::max(1, (K == 1 ? 1024 : 640) / threads);
     return launch_chained(save_kernel<T, W, K, MULTI, WHOLE, THREADS>,
-                          dim3(grid_of((a.rows + rows - 1) / rows, 2048 / threads)), threads, st, a);
+                          dim3(grid_of((a.rows + rows - 1) / rows, per_sm)), threads, st, a);
 }
 
 template <typename T, typename W, bool WHOLE> cudaError_t save_rows(Save a, cudaStream_t st)
@@ -406,15 +409,20 @@ struct Restore {
 
 constexpr int kRestoreThreads = 256;
 constexpr int kRestorePack = 16; // elements of a thread in a row: 16 bytes of codes
-constexpr int kRestoreRows = 4;  // of a thread at a time
+// Rows of a thread at a time, and blocks an SM: 16384 x 4096 bf16 take 37 us with 2 and 3,
+// 44 with 2 and 2, 46 with 3 and 2; 3001 x 1001 fp32, whose packs are shifted, 9.5 us with
+// 3 and 2, 12 with 2 and 3.
+template <bool WHOLE> constexpr int kRestoreRows = WHOLE ? 2 : 3;
+template <bool WHOLE> constexpr int kRestoreBlocks = WHOLE ? 3 : 2;
 constexpr int kRestoreCols = kRestoreThreads * kRestorePack; // of a block, blockIdx.y each
 
 // A thread keeps its columns' weights in registers over all of its rows, and has the
 // codes of several rows on their way at a time.
 template <typename T, typename W, bool WHOLE>
-__global__ void __launch_bounds__(kRestoreThreads, 2) restore_kernel(const Restore a)
+__global__ void __launch_bounds__(kRestoreThreads, kRestoreBlocks<WHOLE>)
+    restore_kernel(const Restore a)
 {
-    constexpr int E = kRestorePack, R = kRestoreRows;
+    constexpr int E = kRestorePack, R = kRestoreRows<WHOLE>;
     const W *const gamma = static_cast<const W *>(a.gamma), *const beta =
                                                                 static_cast<const W *>(a.beta);
     T *const y = static_cast<T *>(a.y);
@@ -504,19 +512,23 @@ __global__ void __launch_bounds__(kRestoreThreads, 2) restore_kernel(const Resto
     }
 }
 
+template <typename T, typename W, bool WHOLE> cudaError_t restore_launch(const Restore &a, cudaStream_t st)
+{
+    const int rows = kRestoreThreads / a.lanes * kRestoreRows<WHOLE>; // of a block at a time
+    const long long cols = std::min((a.dim + kRestoreCols - 1) / kRestoreCols, 65535LL);
+    // (one wave: a block's weights are read once)
+    const long long blocks = std::max(1LL, num_sms() * (long long)kRestoreBlocks<WHOLE> / cols);
+    const dim3 grid((unsigned)std::min((a.rows + rows - 1) / rows, blocks), (unsigned)cols);
+    return launch_chained(restore_kernel<T, W, WHOLE>, grid, kRestoreThreads, st, a);
+}
+
 template <typename T, typename W> rra_status restore(Restore a, cudaStream_t st)
 {
     a.lanes = 1;
     while (a.lanes < kRestoreThreads && a.lanes * kRestorePack < a.dim)
         a.lanes *= 2;
-    const int rows = kRestoreThreads / a.lanes * kRestoreRows; // of a block at a time
-    const long long cols = std::min((a.dim + kRestoreCols - 1) / kRestoreCols, 65535LL);
-    const long long blocks = std::max(1LL, num_sms() * 8LL / cols);
-    const dim3 grid((unsigned)std::min((a.rows + rows - 1) / rows, blocks), (unsigned)cols);
-    return launched(whole_packs<T>(a.dim, {a.y, a.gamma, a.beta})
-                        ? launch_chained(restore_kernel<T, W, true>, grid, kRestoreThreads, st, a)
-                        : launch_chained(restore_kernel<T, W, false>, grid, kRestoreThreads, st,
-                                         a));
+    return launched(whole_packs<T>(a.dim, {a.y, a.gamma, a.beta}) ? restore_launch<T, W, true>(a, st)
+                                                                  : restore_launch<T, W, false>(a, st));
 }
 
 // ---------------------------------------------------------------- gradient

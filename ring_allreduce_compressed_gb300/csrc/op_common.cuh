@@ -304,12 +304,9 @@ __host__ __device__ inline bool pack_fits(const void *base, size_t row_bytes, si
 // but kept if a captured graph may hold its address; sizes at least double.
 // RRA_ERR_INVALID: the buffer would have to grow while the stream is being
 // captured; RRA_ERR_NOMEM, RRA_ERR_CUDA.
-constexpr size_t kScratchHead = 1024;
+constexpr size_t kScratchHead = 256;
 rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex> &lk,
                       unsigned char **out);
-
-// A kernel has ended before its time: heads are cleared before they are used again.
-void op_scratch_spoilt();
 
 // Allows a kernel `smem` bytes of dynamic shared memory, and clusters of more
 // than 8 blocks: once per kernel and device, not on every launch.

@@ -53,7 +53,6 @@ struct Buffer {
     size_t bytes = 0;
     unsigned long long id = 0; // of the stream that it belongs to
     bool captured = false;     // a graph may hold its address
-    bool spoilt = false;       // its head may not be zero
 };
 
 std::mutex g_mu;
@@ -125,23 +124,11 @@ rra_status op_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex
             cudaFree(p);
             return RRA_ERR_CUDA;
         }
-        *ws = Buffer{p, want, slot.id, false, false};
-    }
-    if (ws->spoilt) {
-        if (cudaMemsetAsync(ws->p, 0, kScratchHead, st) != cudaSuccess)
-            return RRA_ERR_CUDA;
-        ws->spoilt = false;
+        *ws = Buffer{p, want, slot.id, false};
     }
     ws->captured |= slot.capturing;
     *out = ws->p;
     return RRA_OK;
-}
-
-void op_scratch_spoilt()
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    for (auto &ws : g_ws)
-        ws.second.spoilt = true;
 }
 
 cudaError_t op_allow(const void *fn, int smem, bool large_clusters)
