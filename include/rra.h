@@ -793,8 +793,14 @@ typedef enum {
  *                 (gate_exps and gate as codes, of rows of ff elements), or
  *                 rounded to dtype (rows * ff elements; gate_exps NULL), or
  *                 nothing (both NULL); up the same, apart from gate.
- * Arrays of 16-byte alignment with dim a multiple of 16 bytes run fastest;
- * others of 16-bit types are laid out anew in scratch memory first.
+ * Arrays of 16-byte alignment with dim a multiple of 16 bytes run fastest; others
+ * of 16-bit types, and fp32 ones of more than 16 rows, are laid out anew in
+ * scratch memory first (2 or 6 bytes an element of x, w_gate and w_up).
+ * Products run on tensor cores, whose fp32 sums are cut off and not rounded at
+ * every 16 elements of k: by less than 2^-24 k / 16 of the sum of magnitudes.
+ * fp32 operands are multiplied as three parts of 8 bits each, and sums of more
+ * than 256 elements of k put together by rounded additions: an infinity among
+ * them may give NaN.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, dim or ff 0, rows, dim or ff above
  * 2^30, an array of more than 64 TB, an output that overlaps an input or another
  * output), RRA_ERR_NOMEM, RRA_ERR_CUDA; RRA_ERR_TIMEOUT (this call did nothing): a
@@ -811,8 +817,8 @@ rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, siz
  *   dup = dh * a(g),  dgate = dh * u * a'(g),  h = a(g) * u
  *   dx = dgate * w_gate + dup * w_up
  *   dw_gate = dgate^T * x,  dw_up = dup^T * x
- *  dgate, dup     rows * ff elements of dtype, required: the products below are
- *                 taken of these rounded values.
+ *  dgate, dup     rows * ff elements of dtype, required: the products are taken of
+ *                 these rounded values.
  *  h              the inner activation again (for the gradient of what follows
  *                 it); NULL: not computed.
  *                 Each of the three may take the place of dh, gate or up (not of
@@ -822,6 +828,7 @@ rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, siz
  *                 RRA_ERR_UNSUPPORTED); either may be NULL.  accumulate nonzero:
  *                 added to what they hold, in fp32.
  * x is not read when both weights' gradients are NULL, the weights not when dx is.
+ * Arrays are laid out anew as in rra_gated_ff, dgate and dup among them.
  * Errors: as rra_gated_ff.
  */
 rra_status rra_gated_ff_grad(const void *dh, const void *x, const void *w_gate, const void *w_up,

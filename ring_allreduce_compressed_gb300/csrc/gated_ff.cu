@@ -6,6 +6,11 @@
 //   dx = dgate Wg + dup Wu,  dWg = dgate^T x,  dWu = dup^T x
 //
 // with M rows of x, D = dim and F = ff: 4 M F D operations forward, 8 backward.
+//
+// Here: the calls, the elementwise part of the gradient, and operands laid out for the
+// products, which stand in gated_gemm.cu and, for few rows, gated_rows.cu.  dgate and dup
+// are rounded to the call's type before they are multiplied, as the tensor cores take
+// them: an error of half a step of a 16-bit number in each, as large as the results' own.
 #include "gated_ff.h"
 
 #include "gated_act.cuh"
@@ -21,8 +26,9 @@ namespace {
 constexpr int kActThreads = 256;
 
 // Packs of 8 elements of a row; SAVED: gate and up in 8 bits.  Every element is read
-// before it is written, so outputs may take inputs' places; WHOLE: every pack is on a
-// 16-byte boundary.
+// before it is written, so outputs may take inputs' places.  Bound by memory: 8192 x 16384
+// bf16 from 8 bits take 180 us (1.08 GB, 6.0 TB/s).  WHOLE: every pack is on a 16-byte
+// boundary.
 template <typename T, bool SAVED, bool WHOLE, int ACT>
 __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs a, int lanes)
 {

