@@ -22,12 +22,16 @@
 namespace rra {
 namespace {
 
-// 8 weights as fp32 from column c on, of which n are there.
+// 8 weights as fp32 from column c (a multiple of 8) on, of which n are there; VEC: all or
+// none, on a 16-byte boundary.
 template <typename W, bool VEC>
 __device__ __forceinline__ void weights8(const W *p, long long c, int n, float none, float v[8])
 {
     if (p) {
-        load8<W, VEC>(p + c, n, v);
+        if (VEC || (n == 8 && aligned_to(p, 16)))
+            load8<W, true>(p + c, n, v);
+        else
+            load8<W, false>(p + c, n, v);
         return;
     }
 #pragma unroll
@@ -172,14 +176,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
     const long long step = (long long)gridDim.x * groups;
     dependents_wait();
     dependents_launch();
-    uint32_t ahead[K][N] = {}; // (what is not there stays zero)
+    uint32_t ahead[K][kChunkWords<T, WHOLE>] = {}; // (what is not there stays zero)
     const auto read = [&](long long base) {
         // every lane takes part in the sums, some in vain: they read the last row
         const T *const p = x + min(base + (MULTI ? 0 : first), a.rows - 1) * dim + u0 * kPack;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (there[k] > 0)
-                load_words<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
+                load_chunks<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
     };
     long long base = (long long)blockIdx.x * groups;
     read(base);
@@ -189,9 +193,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
         uint32_t w[K][N];
 #pragma unroll
         for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                w[k][j] = ahead[k][j];
+            settle<T, WHOLE>(ahead[k], x + r * dim, there[k], w[k]);
         if (base + step < a.rows)
             read(base + step);
         Pair sum = pair_of(0.0f, 0.0f);
@@ -632,12 +634,12 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
             const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15);
             const uint4 *const from =
                 reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
-            if (in == kPack && reinterpret_cast<const T *>(from) >= dy &&
+            if (reinterpret_cast<const T *>(from) >= dy &&
                 reinterpret_cast<const T *>(from + C) <= dy_end) {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
                     stage16(to + (k * C + c) * kRow, from + c);
-            } else { // an end of the row or the array: what is there, zeros behind it
+            } else { // an end of the array: what is there, zeros behind it
                 for (int j = 0; j < kPack; ++j) {
                     const int at = m + j * (int)sizeof(T);
                     *reinterpret_cast<T *>(to + (k * C + at / 16) * kRow + at % 16) =
@@ -693,12 +695,12 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         next_row(r + step);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // dy and xh of the k-th pack, out of its slot
-        const auto take = [&](int k, Pair (&d)[4], Pair (&xh)[4]) {
-            const unsigned char *const at = slots + now * kStage;
+        const auto take = [&](int k, bool shifted, Pair (&d)[4], Pair (&xh)[4]) {
+            unsigned char *const at = slots + now * kStage;
             uint32_t w[N];
-            if (WHOLE) {
+            if (WHOLE || shifted) {
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
+                for (int c = 0; c < N / 4; ++c) {
                     const uint4 q = *reinterpret_cast<const uint4 *>(at + (k * C + c) * kRow);
                     w[4 * c] = q.x, w[4 * c + 1] = q.y, w[4 * c + 2] = q.z, w[4 * c + 3] = q.w;
                 }
@@ -710,6 +712,13 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
                     in[4 * c] = q.x, in[4 * c + 1] = q.y, in[4 * c + 2] = q.z, in[4 * c + 3] = q.w;
                 }
                 shift_bytes(in, (int)(reinterpret_cast<uintptr_t>(dy + r * dim) & 15), w);
+                if (there[k] < kPack)
+                    keep_first<T>(w, there[k]);
+                if (dx) // (for the second time)
+#pragma unroll
+                    for (int c = 0; c < N / 4; ++c)
+                        *reinterpret_cast<uint4 *>(at + (k * C + c) * kRow) =
+                            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
             const Codes8 q = load_codes(
                 reinterpret_cast<const int8_t *>(codes + now * kStage + k * THREADS * 8));
@@ -736,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
                 if (there[k] == 0)
                     continue;
                 Pair d[4], xh[4], g[4];
-                take(k, d, xh);
+                take(k, false, d, xh);
                 weight(k, g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -761,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
             if (on && there[k] > 0) {
                 Pair d[4], xh[4], g[4];
                 float v[8];
-                take(k, d, xh);
+                take(k, true, d, xh);
                 weight(k, g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

@@ -12,24 +12,35 @@
 
 namespace rra {
 
-// Words from byte q (0..16, a multiple of 2) of `in` on.
+// Words from byte q (0..16, a multiple of 2) of `in` on.  (A warp with one row has one q,
+// and goes one of the five ways: an instruction a word, where selects took three.)
 template <int N_IN, int N_OUT>
 __device__ __forceinline__ void shift_bytes(const uint32_t (&in)[N_IN], int q, uint32_t (&out)[N_OUT])
 {
     static_assert(N_IN == N_OUT + 4, "16 bytes more");
-    uint32_t t[N_IN];
+    const uint32_t bits = 8 * (q & 3);
+    const auto words = [&](auto from) {
+        constexpr int S = decltype(from)::value;
 #pragma unroll
-    for (int i = 0; i < N_IN; ++i)
-        t[i] = q & 2 ? __byte_perm(in[i], i + 1 < N_IN ? in[i + 1] : 0u, 0x5432) : in[i];
-#pragma unroll
-    for (int i = 0; i + 1 < N_IN; ++i)
-        t[i] = q & 4 ? t[i + 1] : t[i];
-#pragma unroll
-    for (int i = 0; i + 2 < N_IN; ++i)
-        t[i] = q & 8 ? t[i + 2] : t[i];
-#pragma unroll
-    for (int i = 0; i < N_OUT; ++i)
-        out[i] = q & 16 ? t[i + 4] : t[i];
+        for (int i = 0; i < N_OUT; ++i)
+            out[i] = S == 4 ? in[i + 4] : __funnelshift_r(in[i + S], in[i + S + 1], bits);
+    };
+    switch (q >> 2) {
+    case 0:
+        words(std::integral_constant<int, 0>());
+        break;
+    case 1:
+        words(std::integral_constant<int, 1>());
+        break;
+    case 2:
+        words(std::integral_constant<int, 2>());
+        break;
+    case 3:
+        words(std::integral_constant<int, 3>());
+        break;
+    default:
+        words(std::integral_constant<int, 4>());
+    }
 }
 
 // Words of a pack of 8 elements, or of 16.
@@ -67,53 +78,115 @@ __device__ __forceinline__ void to_words(const float *v, uint32_t (&w)[kPackWord
     }
 }
 
-// The n (0..8) elements at p, zeros behind them; WHOLE: n is 0 or 8 and p on a
-// 16-byte boundary.  [begin, end): the array; nothing outside of it is read.
+// Words of a pack with zeros behind its first n elements.
+template <typename T> __device__ __forceinline__ void keep_first(uint32_t (&w)[kPackWords<T>], int n)
+{
+#pragma unroll
+    for (int i = 0; i < kPackWords<T>; ++i) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = i < n ? w[i] : 0u;
+        else
+            w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+    }
+}
+
+// Words of the chunks that a pack touches (WHOLE: of the pack).
+template <typename T, bool WHOLE> constexpr int kChunkWords = kPackWords<T> + (WHOLE ? 0 : 4);
+
+// The chunks of the n (1..8) elements at p, still where they are in memory, so that
+// nothing waits for them; settle() has the elements.  WHOLE: n is 8 and p on a 16-byte
+// boundary.  [begin, end): the array; nothing outside of it is read.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void load_chunks(const T *p, int n, const T *begin, const T *end,
+                                            uint32_t (&raw)[kChunkWords<T, WHOLE>])
+{
+    constexpr int N = kPackWords<T>;
+    const int m = WHOLE ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4 *const c = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
+    if (WHOLE || (reinterpret_cast<const T *>(c) >= begin &&
+                  reinterpret_cast<const T *>(c + N / 4 + 1) <= end)) {
+#pragma unroll
+        for (int i = 0; i < kChunkWords<T, WHOLE>; i += 4) {
+            const uint4 q = c[i / 4];
+            raw[i] = q.x, raw[i + 1] = q.y, raw[i + 2] = q.z, raw[i + 3] = q.w;
+        }
+        return;
+    }
+    if constexpr (!WHOLE) { // an end of the array: as many elements, at the same place
+        uint32_t w[N + 8] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) {
+                if constexpr (sizeof(T) == 4)
+                    w[4 + j] = reinterpret_cast<const uint32_t *>(p)[j];
+                else
+                    w[4 + j / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[j]
+                                    << (16 * (j % 2));
+            }
+        shift_bytes(w, 16 - m, raw);
+    }
+}
+
+// The elements of load_chunks(p, n, ...), zeros behind them.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void settle(const uint32_t (&raw)[kChunkWords<T, WHOLE>], const T *p, int n,
+                                       uint32_t (&w)[kPackWords<T>])
+{
+    if constexpr (WHOLE) {
+#pragma unroll
+        for (int i = 0; i < kPackWords<T>; ++i)
+            w[i] = raw[i];
+    } else {
+        shift_bytes(raw, (int)(reinterpret_cast<uintptr_t>(p) & 15), w);
+        if (n < 8)
+            keep_first<T>(w, n);
+    }
+}
+
+// Both, of n (0..8) elements (WHOLE: 0 or 8).
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void load_words(const T *p, int n, const T *begin, const T *end,
                                            uint32_t (&w)[kPackWords<T>])
 {
-    constexpr int N = kPackWords<T>;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < kPackWords<T>; ++i)
         w[i] = 0;
     if (n == 0)
         return;
-    if constexpr (WHOLE) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + i);
-            w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
-        }
-    } else {
-        const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-        const uint4 *const c = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
-        if (n == 8 && reinterpret_cast<const T *>(c) >= begin &&
-            reinterpret_cast<const T *>(c + N / 4 + 1) <= end) {
-            uint32_t in[N + 4];
-#pragma unroll
-            for (int i = 0; i < N + 4; i += 4) {
-                const uint4 q = c[i / 4];
-                in[i] = q.x, in[i + 1] = q.y, in[i + 2] = q.z, in[i + 3] = q.w;
-            }
-            shift_bytes(in, m, w);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) {
-                    if constexpr (sizeof(T) == 4)
-                        w[j] = reinterpret_cast<const uint32_t *>(p)[j];
-                    else
-                        w[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[j]
-                                    << (16 * (j % 2));
-                }
-        }
-    }
+    uint32_t raw[kChunkWords<T, WHOLE>];
+    load_chunks<T, WHOLE>(p, n, begin, end, raw);
+    settle<T, WHOLE>(raw, p, n, w);
+}
+
+// The first r bytes (even, below 16) of a chunk, or those from byte m (even, above 0) on.
+__device__ __forceinline__ void put_begin(unsigned char *c, int r, uint32_t a, uint32_t b, uint32_t x,
+                                          uint32_t y)
+{
+    if (r & 8)
+        *reinterpret_cast<uint2 *>(c) = make_uint2(a, b);
+    if (r & 4)
+        *reinterpret_cast<uint32_t *>(c + (r & 8)) = r & 8 ? x : a;
+    if (r & 2)
+        *reinterpret_cast<uint16_t *>(c + (r & 12)) =
+            (uint16_t)(r & 8 ? (r & 4 ? y : x) : (r & 4 ? b : a));
+}
+__device__ __forceinline__ void put_end(unsigned char *c, int m, uint32_t a, uint32_t b, uint32_t x,
+                                        uint32_t y)
+{
+    if (m & 2)
+        *reinterpret_cast<uint16_t *>(c + m) =
+            (uint16_t)((m & 8 ? (m & 4 ? y : x) : (m & 4 ? b : a)) >> 16);
+    const int q = (m + 2) & ~3; // whole words from here on
+    if (q & 4)
+        *reinterpret_cast<uint32_t *>(c + q) = q & 8 ? y : b;
+    if (q <= 8)
+        *reinterpret_cast<uint2 *>(c + 8) = make_uint2(x, y);
 }
 
 // Writes the n (0..E) elements at p; `next`: how many the next lane's pack has.  A
 // stretch of `lanes` (a power of two, at most a warp) lanes holds neighbouring packs
 // of one row; all lanes of the warp are here.  on: is the lane's row written at all?
+// A chunk with the ends of two lanes' packs is the second one's to write.
 template <typename T, bool WHOLE, int E = 8>
 __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int lanes,
                                             const uint32_t (&w)[kPackWords<T, E>])
@@ -126,8 +199,7 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
                 *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(p) + i) =
                     make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     } else {
-        const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15), s = m / (int)sizeof(T);
-        const int place = threadIdx.x % lanes;
+        const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15), place = threadIdx.x % lanes;
         uint32_t in[N + 4], out[N];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -138,40 +210,43 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
         shift_bytes(in, 16 - m, out);
         if (!on || n == 0)
             return;
-        // chunk i holds elements [16 i / sizeof(T) - s, ...) of the pack
-        constexpr int C = 16 / sizeof(T); // elements of a chunk
         unsigned char *const c = reinterpret_cast<unsigned char *>(p) - m;
-        const auto one = [&](int j) {
-            if constexpr (sizeof(T) == 4)
-                reinterpret_cast<uint32_t *>(p)[j] = w[j];
-            else
-                reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
-        };
-        int done = 0;              // elements from the first on that are written
-        if (m > 0 && place == 0) { // the chunk's first elements are not this lane's
-            done = min(n, C - s);
+        const int bytes = m + n * (int)sizeof(T);  // from the first chunk's begin on
+        const bool first = place == 0 && m > 0;    // its first bytes are not this lane's
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                if (j < done)
-                    one(j);
-        }
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const int last = (i + 1) * C - s; // elements up to the chunk's end
-            if (done < last && n >= last) {
+        for (int i = 0; i < N / 4; ++i)
+            if (16 * (i + 1) <= bytes && !(i == 0 && first))
                 *reinterpret_cast<uint4 *>(c + 16 * i) =
                     make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-                done = last;
-            }
-        }
-        // the rest is the next lane's, which begins with it
-        if (m > 0 && n == E && done == E - s && place != lanes - 1 && next >= C - s)
-            return;
-        // (a chunk that the row ends in has elements of the lane before: it wrote them)
+        if (first) {
+            if (bytes < 16) { // a row, or its rest, inside of a chunk
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (j >= done && j < n)
-                one(j);
+                for (int j = 0; j < 16 / (int)sizeof(T); ++j)
+                    if (j < n) {
+                        if constexpr (sizeof(T) == 4)
+                            reinterpret_cast<uint32_t *>(p)[j] = w[j];
+                        else
+                            reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+                    }
+                return;
+            }
+            put_end(c, m, out[0], out[1], out[2], out[3]);
+        }
+        const int rest = bytes & 15;
+        if (rest > 0 && (next == 0 || place == lanes - 1)) {
+            // the chunk that the row or the stretch ends in: one of `out`, or the pack's own
+            // last bytes alone
+            const uint32_t last[8] = {w[N - 4], w[N - 3], w[N - 2], w[N - 1], 0u, 0u, 0u, 0u};
+            uint32_t t[4];
+            shift_bytes(last, 16 - m, t);
+            const int at = bytes / 16;
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    t[j] = at == i ? out[4 * i + j] : t[j];
+            put_begin(c + 16 * at, rest, t[0], t[1], t[2], t[3]);
+        }
     }
 }
 
