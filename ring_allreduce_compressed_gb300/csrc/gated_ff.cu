@@ -91,13 +91,15 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs 
             if (!WHOLE)
                 __syncwarp();
             uint32_t o[N];
+            const int next = in(u + 1);
+            Carry<T> none;
             to_words<T>(dg, o);
-            store_words<T, WHOLE>(static_cast<T *>(a.dgate) + at, there, in(u + 1), on, stretch, o);
+            store_words<T, WHOLE>(static_cast<T *>(a.dgate) + at, there, next, on, stretch, o, none);
             to_words<T>(du, o);
-            store_words<T, WHOLE>(static_cast<T *>(a.dup) + at, there, in(u + 1), on, stretch, o);
+            store_words<T, WHOLE>(static_cast<T *>(a.dup) + at, there, next, on, stretch, o, none);
             if (a.h) {
                 to_words<T>(h, o);
-                store_words<T, WHOLE>(static_cast<T *>(a.h) + at, there, in(u + 1), on, stretch, o);
+                store_words<T, WHOLE>(static_cast<T *>(a.h) + at, there, next, on, stretch, o, none);
             }
         }
     }

@@ -13,7 +13,7 @@
 // Bound by memory: one pass over what is read and written, 8 bits of the saved
 // row among it.  Measured at 16384 x 4096 bf16: save 60 us (338 MB, 5.6 TB/s), restore 37 us
 // (202 MB, 5.5 TB/s), gradient 75 us (338 MB, 4.5 TB/s: issue slots 56 % and 12 warps an SM,
-// 5 of the 75 for adding the partial rows); 3001 x 1001 fp32: restore 9.4 us, gradient 17.
+// 5 of the 75 for adding the partial rows); 3001 x 1001 fp32: restore 7.4 us, gradient 15.6.
 #include "op_common.cuh"
 #include "ragged.cuh"
 #include "row_group.cuh"
@@ -179,11 +179,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
     uint32_t ahead[K][kChunkWords<T, WHOLE>] = {}; // (what is not there stays zero)
     const auto read = [&](long long base) {
         // every lane takes part in the sums, some in vain: they read the last row
-        const T *const p = x + min(base + (MULTI ? 0 : first), a.rows - 1) * dim + u0 * kPack;
+        const T *const row = x + min(base + (MULTI ? 0 : first), a.rows - 1) * dim;
+        const bool inside = WHOLE || row_inside(row, dim, x, x_end);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (there[k] > 0)
-                load_chunks<T, WHOLE>(p + k * gap, there[k], x, x_end, ahead[k]);
+                load_chunks<T, WHOLE>(row + u0 * kPack + k * gap, there[k], x, x_end, ahead[k],
+                                      inside);
     };
     long long base = (long long)blockIdx.x * groups;
     read(base);
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
         else
             save_codes([](const float *v, uint32_t t) { return encode8(v, t); });
         T *const to = y + r * dim + u0 * kPack;
+        Carry<T> carry;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int u = u0 + k * (gap / kPack);
@@ -285,7 +288,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
                        v[2 * j], v[2 * j + 1]);
             uint32_t o[N];
             to_words<T>(v, o);
-            store_words<T, WHOLE>(to + k * gap, there[k], next[k], on, min(lanes, 32), o);
+            store_words<T, WHOLE>(to + k * gap, there[k], next[k], on, min(lanes, 32), o, carry,
+                                  k > 0, k == K - 1);
         }
         if (on && li == 0) {
             a.mean[r] = mu;
@@ -416,8 +420,8 @@ struct Restore {
 constexpr int kRestoreThreads = 256;
 constexpr int kRestorePack = 16; // elements of a thread in a row: 16 bytes of codes
 // Rows of a thread at a time, and blocks an SM: 16384 x 4096 bf16 take 37 us with 2 and 3,
-// 44 with 2 and 2, 46 with 3 and 2; 3001 x 1001 fp32, whose packs are shifted, 9.5 us with
-// 3 and 2, 12 with 2 and 3.
+// 44 with 2 and 2, 46 with 3 and 2; 3001 x 1001 fp32, whose packs are shifted, took 9.5 us
+// with 3 and 2, 12 with 2 and 3.
 template <bool WHOLE> constexpr int kRestoreRows = WHOLE ? 2 : 3;
 template <bool WHOLE> constexpr int kRestoreBlocks = WHOLE ? 3 : 2;
 constexpr int kRestoreCols = kRestoreThreads * kRestorePack; // of a block, blockIdx.y each
@@ -511,7 +515,8 @@ __global__ void __launch_bounds__(kRestoreThreads, kRestoreBlocks<WHOLE>)
                                 *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(to) + j) =
                                     make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 } else {
-                    store_words<T, false, E>(to, there, next, r < a.rows, min(a.lanes, 32), o);
+                    Carry<T, E> carry;
+                    store_words<T, false, E>(to, there, next, r < a.rows, min(a.lanes, 32), o, carry);
                 }
             }
         }
@@ -613,6 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
     const auto stage_row = [&](int stage, long long r) {
         unsigned char *const to = slots + stage * kStage;
         const bool on = r < a.rows;
+        const bool inside = WHOLE || row_inside(dy + r * dim, dim, dy, dy_end);
         const T *const row = dy + r * dim + u0 * kPack;
         const int8_t *const row_codes = a.codes + r * nb * kBlock + u0 * kPack;
 #pragma unroll
@@ -634,8 +640,8 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
             const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15);
             const uint4 *const from =
                 reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
-            if (reinterpret_cast<const T *>(from) >= dy &&
-                reinterpret_cast<const T *>(from + C) <= dy_end) {
+            if (inside || (reinterpret_cast<const T *>(from) >= dy &&
+                           reinterpret_cast<const T *>(from + C) <= dy_end)) {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
                     stage16(to + (k * C + c) * kRow, from + c);
@@ -764,6 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
         // dx = rs w - rs mean(w) - xh rs mean(w xh)
         const float t0 = -rs * quotient(s.v[0], n, inverse), t1 = -rs * quotient(s.v[1], n, inverse);
         const Pair m0 = pair_of(t0, t0), m1 = pair_of(t1, t1);
+        Carry<T> carry;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             uint32_t o[N] = {};
@@ -778,7 +785,7 @@ __global__ void __launch_bounds__(THREADS, 1) saved_grad_kernel(const SavedGrad 
                 to_words<T>(v, o);
             }
             store_words<T, WHOLE>(dx + r * dim + u0 * kPack + k * gap, there[k], next[k], on,
-                                  min(lanes, 32), o);
+                                  min(lanes, 32), o, carry, k > 0, k == K - 1);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -90,21 +90,30 @@ template <typename T> __device__ __forceinline__ void keep_first(uint32_t (&w)[k
     }
 }
 
+// Are all chunks that packs of a row of dim elements touch in [begin, end)?
+template <typename T>
+__device__ __forceinline__ bool row_inside(const T *row, long long dim, const T *begin, const T *end)
+{
+    return row - 16 / (int)sizeof(T) >= begin && row + dim + 8 + 16 / (int)sizeof(T) <= end;
+}
+
 // Words of the chunks that a pack touches (WHOLE: of the pack).
 template <typename T, bool WHOLE> constexpr int kChunkWords = kPackWords<T> + (WHOLE ? 0 : 4);
 
 // The chunks of the n (1..8) elements at p, still where they are in memory, so that
 // nothing waits for them; settle() has the elements.  WHOLE: n is 8 and p on a 16-byte
-// boundary.  [begin, end): the array; nothing outside of it is read.
+// boundary.  [begin, end): the array; nothing outside of it is read.  inside: is it known
+// that the chunks are?
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void load_chunks(const T *p, int n, const T *begin, const T *end,
-                                            uint32_t (&raw)[kChunkWords<T, WHOLE>])
+                                            uint32_t (&raw)[kChunkWords<T, WHOLE>],
+                                            bool inside = false)
 {
     constexpr int N = kPackWords<T>;
     const int m = WHOLE ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15);
     const uint4 *const c = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - m);
-    if (WHOLE || (reinterpret_cast<const T *>(c) >= begin &&
-                  reinterpret_cast<const T *>(c + N / 4 + 1) <= end)) {
+    if (WHOLE || inside || (reinterpret_cast<const T *>(c) >= begin &&
+                            reinterpret_cast<const T *>(c + N / 4 + 1) <= end)) {
 #pragma unroll
         for (int i = 0; i < kChunkWords<T, WHOLE>; i += 4) {
             const uint4 q = c[i / 4];
@@ -183,13 +192,21 @@ __device__ __forceinline__ void put_end(unsigned char *c, int m, uint32_t a, uin
         *reinterpret_cast<uint2 *>(c + 8) = make_uint2(x, y);
 }
 
-// Writes the n (0..E) elements at p; `next`: how many the next lane's pack has.  A
-// stretch of `lanes` (a power of two, at most a warp) lanes holds neighbouring packs
-// of one row; all lanes of the warp are here.  on: is the lane's row written at all?
-// A chunk with the ends of two lanes' packs is the second one's to write.
+// What a lane's last bytes of its pack before are, for the next store_words.
+template <typename T, int E = 8> struct Carry {
+    uint32_t w[4] = {};
+};
+
+// Writes the n (0..E) elements at p.  A stretch of `lanes` (a power of two, at most a
+// warp) lanes holds neighbouring packs of one row, and the stretch of the lanes' next
+// packs may follow it: `next`: how many elements the pack behind this one has; joined:
+// does this stretch follow the one that `carry` is of?  last: does none follow it?  All
+// lanes of the warp are here.  on: is the lane's row written at all?
+// A chunk with the ends of two packs is the second one's to write.
 template <typename T, bool WHOLE, int E = 8>
 __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int lanes,
-                                            const uint32_t (&w)[kPackWords<T, E>])
+                                            const uint32_t (&w)[kPackWords<T, E>], Carry<T, E> &carry,
+                                            bool joined = false, bool last = true)
 {
     constexpr int N = kPackWords<T, E>;
     if constexpr (WHOLE) {
@@ -200,10 +217,15 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
                     make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     } else {
         const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15), place = threadIdx.x % lanes;
+        // the lane before; before the first one the last of the stretch before
+        const int before = threadIdx.x % 32 - place + (place + lanes - 1) % lanes;
         uint32_t in[N + 4], out[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            in[i] = __shfl_up_sync(kFull, w[N - 4 + i], 1);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t mine = w[N - 4 + i];
+            in[i] = __shfl_sync(kFull, place == lanes - 1 ? carry.w[i] : mine, before);
+            carry.w[i] = mine;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i)
             in[4 + i] = w[i];
@@ -211,8 +233,8 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
         if (!on || n == 0)
             return;
         unsigned char *const c = reinterpret_cast<unsigned char *>(p) - m;
-        const int bytes = m + n * (int)sizeof(T);  // from the first chunk's begin on
-        const bool first = place == 0 && m > 0;    // its first bytes are not this lane's
+        const int bytes = m + n * (int)sizeof(T); // from the first chunk's begin on
+        const bool first = !joined && place == 0 && m > 0; // its first bytes are not this lane's
 #pragma unroll
         for (int i = 0; i < N / 4; ++i)
             if (16 * (i + 1) <= bytes && !(i == 0 && first))
@@ -233,12 +255,12 @@ __device__ __forceinline__ void store_words(T *p, int n, int next, bool on, int 
             put_end(c, m, out[0], out[1], out[2], out[3]);
         }
         const int rest = bytes & 15;
-        if (rest > 0 && (next == 0 || place == lanes - 1)) {
+        if (rest > 0 && (next == 0 || (last && place == lanes - 1))) {
             // the chunk that the row or the stretch ends in: one of `out`, or the pack's own
             // last bytes alone
-            const uint32_t last[8] = {w[N - 4], w[N - 3], w[N - 2], w[N - 1], 0u, 0u, 0u, 0u};
+            const uint32_t own[8] = {w[N - 4], w[N - 3], w[N - 2], w[N - 1], 0u, 0u, 0u, 0u};
             uint32_t t[4];
-            shift_bytes(last, 16 - m, t);
+            shift_bytes(own, 16 - m, t);
             const int at = bytes / 16;
 #pragma unroll
             for (int i = 0; i < N / 4; ++i)
