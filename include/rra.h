@@ -799,13 +799,11 @@ typedef enum {
  * Products run on tensor cores, whose fp32 sums are cut off and not rounded at
  * every 16 elements of k: by less than 2^-24 k / 16 of the sum of magnitudes.
  * fp32 operands are multiplied as three parts of 8 bits each, and sums of more
- * than 256 elements of k put together by rounded additions: an infinity among
+ * than 64 elements of k put together by rounded additions: an infinity among
  * them may give NaN.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, dim or ff 0, rows, dim or ff above
  * 2^30, an array of more than 64 TB, an output that overlaps an input or another
- * output), RRA_ERR_NOMEM, RRA_ERR_CUDA; RRA_ERR_TIMEOUT (this call did nothing): a
- * wait inside a kernel of an earlier call of these two ran out of time (4 s), and
- * that call's outputs are not complete.
+ * output), RRA_ERR_NOMEM, RRA_ERR_CUDA.
  */
 rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, size_t rows,
                         size_t dim, size_t ff, rra_dtype dtype, rra_act act, void *h,

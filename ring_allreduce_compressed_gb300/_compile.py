@@ -24,7 +24,7 @@ SOURCES = ["rra_host.cu", "ring_none.cu", "ring_bfp8.cu", "ring_bfp4.cu", "ring_
            "layer_norm_saved.cu", "gated_ff.cu", "gated_gemm.cu",
            "gated_rows.cu"]
 HEADERS = ["rra_device.cuh", "rra_kernels.h", "bfp_group.cuh", "ring_kernel.cuh", "wire_sparse.cuh",
-           "op_common.cuh", "row_group.cuh", "saved.cuh", "ragged.cuh", "gated_act.cuh", "gated_ff.h", "tc.cuh",
+           "op_common.cuh", "row_group.cuh", "saved.cuh", "ragged.cuh", "gated_act.cuh", "gated_ff.h",
            "token_sort.cuh", "stream_slot.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -246,26 +246,11 @@ private:
 
 // ---------------------------------------------------------------- calls
 
-// Has a kernel given up waiting since the last call?
-rra_status stalled_status()
-{
-    unsigned *word = nullptr;
-    if (stalled_word(&word) != cudaSuccess)
-        return RRA_ERR_CUDA;
-    volatile unsigned *const w = word;
-    if (!*w)
-        return RRA_OK;
-    *w = 0;
-    return RRA_ERR_TIMEOUT;
-}
-
 template <typename T> rra_status ff(const FfArgs &a, cudaStream_t st)
 {
     if (few_rows<T>(a))
         return rows_forward<T>(a, st);
-    rra_status s = stalled_status();
-    if (s != RRA_OK)
-        return s;
+    rra_status s;
     Operands<T, 3> in({{a.x, a.rows, a.dim, a.dim, 1},
                        {a.wg, a.ff, a.dim, a.dim, 1},
                        {a.wu, a.ff, a.dim, a.dim, 1}});
@@ -285,9 +270,7 @@ template <typename T, typename O> rra_status ff_grad(const FfGradArgs &a, cudaSt
                 e = cudaMemsetAsync(out, 0, (size_t)a.ff * a.dim * sizeof(O), st);
         return launched(e);
     }
-    rra_status s = stalled_status();
-    if (s != RRA_OK)
-        return s;
+    rra_status s = RRA_OK;
     const bool products = a.dx || weights;
     Operands<T, 5> in({{products ? a.dgate : nullptr, a.rows, a.ff, a.ff, 1},
                        {products ? a.dup : nullptr, a.rows, a.ff, a.ff, 1},

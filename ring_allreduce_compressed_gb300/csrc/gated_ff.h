@@ -40,7 +40,7 @@ struct Matrix16 {
     int planes;
 };
 
-// Can tensor maps read it?  (16-byte aligned rows)
+// Can the products read it as it is?  (16-byte aligned rows)
 bool gemm_takes(const Matrix16 &x);
 
 // The products on the tensor cores (gated_gemm.cu); operands as gemm_takes has them.
@@ -61,8 +61,5 @@ cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char 
 // Few rows (gated_rows.cu): is the call one of those, and its kernel.
 template <typename T> bool few_rows(const FfArgs &a);
 template <typename T> rra_status rows_forward(const FfArgs &a, cudaStream_t st);
-
-// Host word that a kernel sets when a wait of its has run out of time.
-cudaError_t stalled_word(unsigned **word);
 
 } // namespace rra

@@ -1,16 +1,9 @@
 // gated_gemm.cu -- the products of the gated feed-forward block on the tensor cores.
 //
-// A pair of blocks makes 256 x 256 results at a time: each block has 128 of the rows
-// and half of the other operand's 256 columns in its shared memory, and one
-// instruction of the pair multiplies all of it.  Slices of 64 along k come by tensor
-// maps, six in flight (5 take the same time); the sums of two results lie in tensor
-// memory, so that one is written out while the next is summed.
-//
-// Bound by the tensor cores, and those by the GPU's power: at 8192 x 4096 x 16384 bf16 the
-// SM clock falls from 2.0 to 1.55 GHz and the products run at 1.69-1.76 PFLOP/s (forward,
-// nothing kept: 1250-1270 us; gate and up kept whole 1285-1330, in 8 bits 1300-1310), 1.66
-// and 1.6 for dx and the weights' gradients (1317 and 1367 us each); the library's plain
-// products of these sizes run at 1.79-1.84.
+// A block makes 128 x 256 results (fp32: 64 x 256) of a stretch of k, in registers: eight
+// warps, each 64 (32) rows and 64 columns.  Slices of 64 along k are copied to shared memory
+// ahead of their use, four of them in a ring.  All waits are for the block's own
+// copies and barriers: none depends on another block or launch.
 #include "gated_ff.h"
 
 #include "gated_act.cuh"
@@ -18,31 +11,24 @@
 #include "ragged.cuh"
 #include "saved.cuh"
 #include "stream_slot.h"
-#include "tc.cuh"
 
 namespace rra {
 namespace {
 
-constexpr int kSide = 256;      // rows and columns of a pair's results
-constexpr int kHalf = 128;      // rows of a block, columns it has in shared memory
-constexpr int kSlice = 64;      // elements of k: 128 bytes
-constexpr int kStages = 6;
-constexpr int kOperandBytes = kHalf * kSlice * 2, kStageBytes = 2 * kOperandBytes;
-constexpr int kBoxBytes = kSlice * kSlice * 2; // 64 rows for 64 elements of k
-constexpr int kWriters = 8;                    // warps that write results
-constexpr int kGemmThreads = 64 + 32 * kWriters; // copies, instructions, and those
-// Tiles along m that share their columns' slices in L2 (8192 x 4096 x 16384 bf16: forward
-// 1257 us with 16, 1271 with 8; dx 1317 with 8, 1368 with 16, 1381 with 4).
-template <int MODE> constexpr int kGroup = MODE == 0 ? 16 : 8;
+constexpr int kWide = 256, kHalf = 128; // columns of a block's results; half of them
+constexpr int kSlice = 64;              // elements of k
+constexpr int kStages = 4;
+constexpr int kGemmThreads = 256, kGemmWarps = kGemmThreads / 32;
+template <bool F32> constexpr int kTall = F32 ? 64 : 128; // rows of a block's results
+template <bool F32> constexpr int kStageBytes = (kTall<F32> + kWide) * kSlice * 2;
+// Tiles along m that share their columns' slices in L2.
+constexpr int kGroup = 16;
 
 // fp32 operands come as three planes of bf16, each the next 8 bits of a number, which
 // add up to it exactly.  Of the nine products of planes the six largest count (what is
-// left out is below 2^-21 of a product, 2^-24 in the mean), the small ones first.  Sums
-// in tensor memory are cut off at each step of 16 along k, not rounded: half a unit
-// of the last place a step, always towards zero (measured: 4.8e-7 of the result after
-// 512 elements of k, 4.4e-6 after 4096).  For fp32 results they are therefore taken out
-// after kRun slices and added up there.
-constexpr int kRun = 4;
+// left out is below 2^-21 of a product, 2^-24 in the mean), the small ones first.  The
+// instructions' sums may be cut off and not rounded; for fp32 results those of a slice
+// are therefore added up outside of them.
 template <bool F32> constexpr int kProducts = F32 ? 6 : 1;
 __device__ __forceinline__ int plane_a(int q) { return q == 0 ? 2 : q == 2 || q == 3 ? 1 : 0; }
 __device__ __forceinline__ int plane_b(int q) { return q == 1 ? 2 : q == 2 || q == 4 ? 1 : 0; }
@@ -57,7 +43,7 @@ __device__ __forceinline__ int plane_b(int q) { return q == 1 ? 2 : q == 2 || q 
 enum Mode { kForward, kDx, kDw };
 
 struct Gemm {
-    CUtensorMap a[2], b[2];
+    Matrix16 a[2], b[2];
     int tiles_m, tiles_n, tiles; // tiles: of all outputs
     int slices;                  // of one pair of operands
     int splits, per_split;       // parts of the slices, each an item of work; slices of one
@@ -66,9 +52,8 @@ struct Gemm {
     void *out[2]; // h; dx; dw_gate, dw_up
     Kept gate, up;
     int accumulate;
-    int first_out;      // kDw: the output of the first tiles
-    float *parts; // more than one split: sums, [tile][split][256 rows][256 columns]
-    unsigned *stalled;
+    int first_out; // kDw: the output of the first tiles
+    float *parts;  // more than one split: sums, [tile][split][rows of a tile][256 columns]
 };
 
 struct TilePlace {
@@ -78,465 +63,121 @@ struct TilePlace {
 
 // Tiles in groups along m, n by n, so that those at work at one time share
 // slices in L2.
-template <int MODE> __device__ __forceinline__ TilePlace tile_place(const Gemm &g, int t)
+template <int MODE, int TALL> __device__ __forceinline__ TilePlace tile_place(const Gemm &g, int t)
 {
     TilePlace p;
     const int per = g.tiles_m * g.tiles_n;
     p.which = MODE == kDw ? t / per + g.first_out : 0;
     t %= per;
-    constexpr int G = kGroup<MODE>;
-    const int group = t / (G * g.tiles_n), left = t - group * G * g.tiles_n;
-    const int height = min(G, g.tiles_m - group * G);
-    p.m0 = (long long)(group * G + left % height) * kSide;
-    p.n0 = (long long)(left / height) * (MODE == kForward ? kHalf : kSide);
+    const long long wide = (long long)kGroup * g.tiles_n;
+    const int group = (int)(t / wide), left = (int)(t - group * wide);
+    const int height = min(kGroup, g.tiles_m - group * kGroup);
+    p.m0 = (long long)(group * kGroup + left % height) * TALL;
+    p.n0 = (long long)(left / height) * (MODE == kForward ? kHalf : kWide);
     return p;
 }
 
-// An item of work: a tile and a stretch of its slices.
-struct Item {
-    int tile, split, lo, hi;
-};
+// ---------------------------------------------------------------- operands
 
-template <int MODE> __device__ __forceinline__ Item item_of(const Gemm &g, int i)
+// 16 bytes of a matrix's plane from (row, col) on to shared memory, col a multiple of 8;
+// what is outside of the plane is zero and not read.
+__device__ __forceinline__ void copy16(uint32_t to, const Matrix16 &x, int plane, long long row,
+                                       long long col)
 {
-    const int all = MODE == kDx ? 2 * g.slices : g.slices;
-    Item t;
-    t.split = i / g.tiles;
-    t.tile = i - t.split * g.tiles;
-    t.lo = t.split * g.per_split;
-    t.hi = min(t.lo + g.per_split, all);
-    return t;
+    const long long left = row < x.rows ? min(8LL, x.cols - col) : 0;
+    const uint32_t bytes = left > 0 ? (uint32_t)left * 2 : 0;
+    const uint16_t *const p = static_cast<const uint16_t *>(x.p);
+    const uint16_t *const from = bytes ? p + (plane * x.rows + row) * x.ld + col : p;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_here()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Slices whose sums stay in tensor memory.
-template <bool F32> __device__ __forceinline__ int run_of(const Item &t) { return F32 ? kRun : t.hi - t.lo; }
-
-// 16 columns from `col` on of a warp's 32 rows (from r0 on; a lane has a row) to an
-// output of m x n.  whole: every 16 columns are on a 32-byte boundary.  A lane then
-// writes its own 32 or 64 bytes (whole sectors, of which 16 bytes would write halves);
-// else they go through shared memory, so that a store has two rows' neighbouring
-// elements and not 32 rows' (which takes a cycle a row: 333 x 513 x 1001 fp16, dx: 50 us).
-constexpr int kStageRow = 17; // floats: rows begin in different banks
-template <typename O>
-__device__ __forceinline__ void put_columns(float *stage, O *out, long long m, long long n,
-                                            long long r0, long long col, bool whole,
-                                            bool accumulate, float (&v)[16])
+// An operand's slice lies in shared memory as lines of 16-byte chunks: along k a line is
+// 64 elements of k of a row, along the rows it is SIZE rows of one k.  A chunk's
+// number is turned by its line's, so that eight lines' chunks are in different banks.
+template <bool ROWS, int SIZE> __device__ __forceinline__ uint32_t chunk_at(int line, int chunk)
 {
-    const int lane = threadIdx.x % 32;
-    if (whole && col + 16 <= n) {
-        O *const p = out + (r0 + lane) * n + col;
-        if (r0 + lane >= m)
-            return;
-        if (accumulate) {
-            float old[16];
-            load8<O, true>(p, 8, *reinterpret_cast<float(*)[8]>(&old[0]));
-            load8<O, true>(p + 8, 8, *reinterpret_cast<float(*)[8]>(&old[8]));
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v[j] += old[j];
-        }
-        uint32_t w[kPackWords<O> * 2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t half[kPackWords<O>];
-            to_words<O>(v + 8 * i, half);
-#pragma unroll
-            for (int j = 0; j < kPackWords<O>; ++j)
-                w[i * kPackWords<O> + j] = half[j];
-        }
-#pragma unroll
-        for (int i = 0; i < kPackWords<O> * 2; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             reinterpret_cast<uint32_t *>(p) + i),
-                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
-                         "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
-                         : "memory");
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        stage[lane * kStageRow + j] = v[j];
-    __syncwarp();
-    const long long c = col + lane % 16;
-    O *p = out + (r0 + lane / 16) * n + c;
-#pragma unroll 8
-    for (int i = lane / 16; i < 32; i += 2, p += 2 * n)
-        if (r0 + i < m && c < n) {
-            const float f = stage[i * kStageRow + lane % 16];
-            *p = from_f32<O>(accumulate ? to_f32(*p) + f : f);
-        }
-    __syncwarp();
+    return (uint32_t)(line * (ROWS ? SIZE * 2 : kSlice * 2) + ((chunk ^ (line & 7)) << 4));
 }
 
-template <int N>
-__device__ __forceinline__ void floats(const uint32_t (&r)[N], int i, float (&v)[16])
+// COUNT rows (from r0 on; all SIZE of them are the operand's, these from `first` on) of
+// a slice from k0 on.
+template <bool ROWS, int SIZE, int COUNT>
+__device__ __forceinline__ void copy_operand(uint32_t to, const Matrix16 &x, int plane, long long r0,
+                                             int first, long long k0)
 {
+    static_assert(COUNT * 8 % kGemmThreads == 0, "all threads copy as much");
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        v[j] = __uint_as_float(r[i + j]);
-}
-
-// ---------------------------------------------------------------- writers
-
-// Writer w has the lanes (rows) 32 (w % 4) .. of tensor memory and one half of the
-// columns (in kForward, of gate's and of up's).  kForward's halves of a row meet in
-// shared memory where a block of 128 codes needs its largest magnitude.
-
-struct Shared {
-    uint64_t full[kStages], empty[kStages], summed[2], written[2];
-    uint32_t tmem, stop;
-    uint32_t top[2][2][kHalf]; // gate, up; half; row
-    float stage[kWriters][32 * kStageRow];
-};
-
-// Largest magnitude's bits of 64 columns of this lane's row.
-__device__ __forceinline__ uint32_t row_top(uint32_t at)
-{
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-        uint32_t r[32];
-        tmem_load(at + c, r);
-        tmem_loaded();
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            top = max(top, r[j] & 0x7fffffffu);
-    }
-    return top;
-}
-
-// One of gate and up, 16 columns from col on.
-template <typename T>
-__device__ __forceinline__ void keep_columns(const Kept &to, float *stage, uint32_t top,
-                                             const Gemm &g, long long r0, long long col, bool whole,
-                                             float (&v)[16])
-{
-    const long long r = r0 + threadIdx.x % 32;
-    if (to.exps) {
-        if (r >= g.m)
-            return;
-        const Codes8 a = encode8(v, top), b = encode8(v + 8, top);
-        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(to.data) + r * blocks_of(g.n) * kBlock +
-                                   col) = make_uint4(a.w[0], a.w[1], b.w[0], b.w[1]);
-    } else if (to.data) {
-        put_columns(stage, static_cast<T *>(to.data), g.m, g.n, r0, col, whole, false, v);
-    }
-}
-
-// Gate and up of a warp's rows from r0 on, 64 columns from n0 + 64 half on, to where
-// they go.
-template <typename T, int ACT>
-__device__ __forceinline__ void write_forward(const Gemm &g, Shared &s, float *stage, int half,
-                                              int quarter, uint32_t at, long long r0, long long n0,
-                                              bool whole)
-{
-    uint32_t top[2] = {0, 0}; // bits of the blocks' largest magnitudes
-    if (g.gate.exps || g.up.exps) {
-        const int row = quarter * 32 + threadIdx.x % 32;
-        const long long r = r0 + threadIdx.x % 32;
-        s.top[0][half][row] = row_top(at + half * 64);
-        s.top[1][half][row] = row_top(at + kHalf + half * 64);
-        named_barrier(2 + quarter, 64);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            top[i] = max(s.top[i][0][row], s.top[i][1][row]);
-            int8_t *const exps = i == 0 ? g.gate.exps : g.up.exps;
-            if (r < g.m && half == 0 && exps)
-                exps[r * blocks_of(g.n) + n0 / kBlock] = exponent_byte(block_exponent(top[i]));
-        }
-        named_barrier(2 + quarter, 64); // (read before the next ones are written)
-    }
-#pragma unroll 1
-    for (int c = half * 64; c < half * 64 + 64; c += 16) {
-        uint32_t rg[16], ru[16];
-        tmem_load(at + c, rg);
-        tmem_load(at + kHalf + c, ru);
-        tmem_loaded();
-        float vg[16], vu[16];
-        floats(rg, 0, vg);
-        floats(ru, 0, vu);
-        keep_columns<T>(g.gate, stage, top[0], g, r0, n0 + c, whole, vg);
-        keep_columns<T>(g.up, stage, top[1], g, r0, n0 + c, whole, vu);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            vg[j] = act_value<ACT, sizeof(T) == 4>(vg[j]) * vu[j];
-        put_columns(stage, static_cast<T *>(g.out[0]), g.m, g.n, r0, n0 + c, whole, false, vg);
-    }
-}
-
-template <typename O>
-__device__ __forceinline__ void write_plain(const Gemm &g, float *stage, O *out, int half,
-                                            uint32_t at, long long r0, long long n0, bool whole)
-{
-#pragma unroll 1
-    for (int c = half * kHalf; c < half * kHalf + kHalf && n0 + c < g.n; c += 32) {
-        uint32_t v[32];
-        tmem_load(at + c, v);
-        tmem_loaded();
-#pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-            float f[16];
-            floats(v, i, f);
-            put_columns(stage, out, g.m, g.n, r0, n0 + c + i, whole, g.accumulate != 0, f);
-        }
-    }
-}
-
-// to (+)= the sums at `from`, a warp's 128 columns from `first` on.
-__device__ __forceinline__ void take_sums(uint32_t from, uint32_t to, int first, bool add)
-{
-#pragma unroll 1
-    for (int c = first; c < first + kHalf; c += 32) {
-        uint32_t v[32];
-        tmem_load(from + c, v);
-        if (add) {
-            uint32_t w[32];
-            tmem_load(to + c, w);
-            tmem_loaded();
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+    for (int j = 0; j < COUNT * 8 / kGemmThreads; ++j) {
+        const int i = j * kGemmThreads + threadIdx.x;
+        if (ROWS) {
+            const int k = i / (COUNT / 8), c = i % (COUNT / 8);
+            copy16(to + chunk_at<true, SIZE>(k, first / 8 + c), x, plane, k0 + k, r0 + c * 8);
         } else {
-            tmem_loaded();
+            const int r = i / 8, c = i % 8;
+            copy16(to + chunk_at<false, SIZE>(first + r, c), x, plane, r0 + r, k0 + c * 8);
         }
-        tmem_store(to + c, v);
     }
-    tmem_stored();
 }
 
-// A warp's sums of an item (128 columns from `first` on; `there`: the lane's row is one of
-// the output's) to memory, for finish_kernel.
-__device__ __forceinline__ void write_part(const Gemm &g, const Item &t, uint32_t at, int row,
-                                           int first, bool there)
+// Four 8 x 8 matrices, a lane giving the address of a line of one.
+template <bool TURN> __device__ __forceinline__ void read4(uint32_t at, uint32_t (&r)[4])
 {
-    float *const to = g.parts + (((long long)t.tile * g.splits + t.split) * kSide + row) * kSide;
-#pragma unroll 1
-    for (int c = first; c < first + kHalf; c += 32) {
-        uint32_t v[32];
-        tmem_load(at + c, v);
-        tmem_loaded();
-#pragma unroll
-        for (int j = 0; there && j < 32; j += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + j),
-                         "r"(v[j]), "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3]), "r"(v[j + 4]),
-                         "r"(v[j + 5]), "r"(v[j + 6]), "r"(v[j + 7])
-                         : "memory");
-    }
+    if (TURN)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(at)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(at)
+                     : "memory");
 }
 
-// ---------------------------------------------------------------- the kernel
-
-// T: the type of the call's elements; O: of the outputs.
-template <typename T, typename O, int MODE>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
+// 16 rows from m on and 16 elements of k of the first operand.
+template <bool ROWS, int SIZE>
+__device__ __forceinline__ void read_a(uint32_t at, int m, int k, uint32_t (&r)[4])
 {
-    constexpr bool F32 = sizeof(T) == 4;
-    constexpr bool A_ROWS = MODE == kDw, B_ROWS = MODE != kForward;
-    constexpr uint32_t kKind =
-        mma_kind(!std::is_same<T, __half>::value, A_ROWS, B_ROWS, kSide, kSide);
-    extern __shared__ unsigned char raw[];
-    // swizzled boxes begin on 1024-byte boundaries
-    unsigned char *const stages = raw + (1024 - smem_u32(raw) % 1024) % 1024;
-    Shared &s = *reinterpret_cast<Shared *>(stages + kStages * kStageBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_rank();
-    const int pairs = gridDim.x / 2, pair = blockIdx.x / 2, items = g.tiles * g.splits;
-
-    if (warp == 0 && lane == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.summed[i], 1);
-            mbar_init(&s.written[i], 2 * kWriters); // of both blocks
-        }
-        s.stop = 0;
-        mbar_fence_init();
-        prefetch_map(&g.a[0]);
-        prefetch_map(&g.b[0]);
-    }
-    __syncwarp();
-    if (warp == 1)
-        tmem_alloc(&s.tmem);
-    tc_fence_before();
-    cluster_barrier();
-    tc_fence_after();
-    const uint32_t tmem = s.tmem;
-    volatile uint32_t *const stop = &s.stop;
-    dependents_wait();
-    dependents_launch();
-
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t step = 0;
-            bool ok = true;
-            // one slice of one product of planes
-            const auto load = [&](const TilePlace &p, int k, int pa, int pb) {
-                const int m = (int)p.m0 + (int)rank * kHalf, n = (int)p.n0 + (int)rank * kHalf;
-                const int i = step % kStages;
-                // the first round finds the stages empty
-                if (!wait_limited(&s.empty[i], (step / kStages & 1) ^ 1, stop, g.stalled))
-                    return false;
-                if (rank == 0)
-                    mbar_arrive_expect_tx(&s.full[i], 2 * kStageBytes);
-                const uint32_t bar = cluster_address(&s.full[i], 0);
-                unsigned char *const a = stages + i * kStageBytes, *const b = a + kOperandBytes;
-                if (MODE == kForward) {
-                    load_box(a, &g.a[0], k * kSlice, m, pa, bar);
-                    load_box(b, &g.b[rank], k * kSlice, (int)p.n0, pb, bar);
-                } else {
-                    const int from = MODE == kDx && k >= g.slices ? 1 : 0;
-                    const int at = (k - from * g.slices) * kSlice;
-                    if (MODE == kDx) {
-                        load_box(a, &g.a[from], at, m, pa, bar);
-                    } else {
-                        load_box(a, &g.a[p.which], m, at, pa, bar);
-                        load_box(a + kBoxBytes, &g.a[p.which], m + kSlice, at, pa, bar);
-                    }
-                    load_box(b, &g.b[from], n, at, pb, bar);
-                    load_box(b + kBoxBytes, &g.b[from], n + kSlice, at, pb, bar);
-                }
-                ++step;
-                return true;
-            };
-            for (int t = pair; ok && t < items; t += pairs) {
-                const Item it = item_of<MODE>(g, t);
-                const TilePlace p = tile_place<MODE>(g, it.tile);
-                const int run = run_of<F32>(it);
-                for (int lo = it.lo; ok && lo < it.hi; lo += run)
-                    for (int q = 0; ok && q < kProducts<F32>; ++q)
-                        for (int k = lo; ok && k < min(lo + run, it.hi); ++k)
-                            ok = load(p, k, F32 ? plane_a(q) : 0, F32 ? plane_b(q) : 0);
-            }
-            // the other block's arrivals on this one's barriers come before it ends
-            for (int i = 0; ok && i < kStages; ++i, ++step)
-                ok = wait_limited(&s.empty[step % kStages], (step / kStages & 1) ^ 1, stop,
-                                  g.stalled);
-            if (!ok) { // what is on its way lands before the block ends
-                const uint64_t t0 = global_ns();
-                while (global_ns() - t0 < 20000000)
-                    __nanosleep(1000);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            uint32_t step = 0, made = 0;
-            bool ok = true;
-            for (int t = pair; ok && t < items; t += pairs) {
-                const Item it = item_of<MODE>(g, t);
-                const int run = run_of<F32>(it);
-                for (int lo = it.lo; ok && lo < it.hi; lo += run, ++made) {
-                    // fp32: the second half of tensor memory holds the sums of runs
-                    const uint32_t into = F32 ? 0 : made % 2, round = F32 ? made : made / 2;
-                    const uint32_t at = tmem + into * kSide;
-                    if (!(ok = wait_limited(&s.written[into], (round & 1) ^ 1, stop, g.stalled)))
-                        break;
-                    tc_fence_after();
-                    const int count = kProducts<F32> * (min(lo + run, it.hi) - lo);
-                    for (int k = 0; k < count; ++k, ++step) {
-                        const int i = step % kStages;
-                        if (!(ok = wait_limited(&s.full[i], step / kStages & 1, stop, g.stalled)))
-                            break;
-                        tc_fence_after();
-                        const unsigned char *const pa = stages + i * kStageBytes,
-                                            *const pb = pa + kOperandBytes;
-                        const uint64_t a =
-                            A_ROWS ? operand_along_rows(pa, kBoxBytes) : operand_along_k(pa);
-                        const uint64_t b =
-                            B_ROWS ? operand_along_rows(pb, kBoxBytes) : operand_along_k(pb);
-#pragma unroll
-                        for (int j = 0; j < kSlice / 16; ++j)
-                            mma_pair(at, a + j * (A_ROWS ? kStepAlongRows : kStepAlongK),
-                                     b + j * (B_ROWS ? kStepAlongRows : kStepAlongK), kKind,
-                                     k > 0 || j > 0);
-                        mma_commit_pair(&s.empty[i]);
-                    }
-                    if (ok)
-                        mma_commit_pair(&s.summed[into]);
-                }
-            }
-        }
-    } else {
-        const int quarter = warp % 4, half = (warp - 2) / 4;
-        const uint32_t lanes = (uint32_t)quarter * 32 << 16;
-        uint32_t made = 0;
-        bool ok = true;
-        const auto wait_sums = [&](uint32_t into, uint32_t round) {
-            // (all writers go on or none: they meet at barriers)
-            const bool yes = named_all(1, 32 * kWriters,
-                                       wait_limited(&s.summed[into], round & 1, stop, g.stalled));
-            __syncwarp();
-            tc_fence_after();
-            return yes;
-        };
-        const auto release = [&](uint32_t into) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                arrive_at(cluster_address(&s.written[into], 0));
-        };
-        for (int t = pair; ok && t < items; t += pairs) {
-            const Item it = item_of<MODE>(g, t);
-            const int run = run_of<F32>(it);
-            uint32_t into = 0;
-            for (int lo = it.lo; ok && lo < it.hi; lo += run, ++made) {
-                into = F32 ? 0 : made % 2;
-                ok = wait_sums(into, F32 ? made : made / 2);
-                if (F32 && ok) {
-                    take_sums(tmem + lanes, tmem + lanes + kSide, half * kHalf, lo > it.lo);
-                    release(0);
-                }
-            }
-            if (!ok)
-                break;
-            const uint32_t at = tmem + lanes + (F32 ? kSide : into * kSide);
-            const TilePlace p = tile_place<MODE>(g, it.tile);
-            const int row = quarter * 32 + lane;
-            const long long r0 = p.m0 + rank * kHalf + quarter * 32;
-            float *const stage = s.stage[warp - 2];
-            if (g.splits > 1) {
-                write_part(g, it, at, rank * kHalf + row, half * kHalf, r0 + lane < g.m);
-            } else {
-                O *const out = static_cast<O *>(g.out[p.which]);
-                const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 32);
-                if (MODE == kForward) {
-                    if (F32) { // a half has columns whose sums the other has stored
-                        tc_fence_before();
-                        named_barrier(2 + quarter, 64);
-                        tc_fence_after();
-                    }
-                    by_act(g.act, [&](auto act) {
-                        write_forward<T, decltype(act)::value>(
-                            g, s, stage, half, quarter, at, r0, p.n0,
-                            whole && (g.gate.exps || aligned_to(g.gate.data, 32)) &&
-                                (g.up.exps || aligned_to(g.up.data, 32)));
-                    });
-                } else {
-                    write_plain<O>(g, stage, out, half, at, r0, p.n0, whole);
-                }
-            }
-            if (!F32)
-                release(into);
-        }
-    }
-    __syncwarp();
-    tc_fence_before();
-    cluster_barrier();
-    tc_fence_after();
-    if (warp == 1)
-        tmem_free(tmem);
+    const int l = threadIdx.x % 32, j = l / 8;
+    if (ROWS)
+        read4<true>(at + chunk_at<true, SIZE>(k + l % 8 + j / 2 * 8, m / 8 + j % 2), r);
+    else
+        read4<false>(at + chunk_at<false, SIZE>(m + l % 16, k / 8 + l / 16), r);
+}
+// 16 columns from n on of the second: r[0], r[1] the first 8, r[2], r[3] the others.
+template <bool ROWS, int SIZE>
+__device__ __forceinline__ void read_b(uint32_t at, int n, int k, uint32_t (&r)[4])
+{
+    const int l = threadIdx.x % 32, j = l / 8;
+    if (ROWS)
+        read4<true>(at + chunk_at<true, SIZE>(k + l % 8 + j % 2 * 8, n / 8 + j / 2), r);
+    else
+        read4<false>(at + chunk_at<false, SIZE>(n + l % 8 + j / 2 * 8, k / 8 + j % 2), r);
 }
 
-constexpr int kGemmSmem = kStages * kStageBytes + 1024 + (int)sizeof(Shared);
+template <bool HALF>
+__device__ __forceinline__ void multiply(float (&acc)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1)
+{
+    if (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-// ---------------------------------------------------------------- splits
-
-// The sums of a tile's splits added, in their order, and on to where they go: a warp has
-// a row of a tile, a lane 4 of its first 128 columns and the same 4 of its last.  (A
-// launch of its own, with all of the GPU: the last of a tile's splits to end took 10 us
-// for it.)
-constexpr int kFinishThreads = 256;
+// ---------------------------------------------------------------- results
 
 template <typename O>
 __device__ __forceinline__ void put4(O *p, long long there, bool whole, const float v[4])
@@ -579,163 +220,221 @@ __device__ __forceinline__ void keep4(const Kept &to, long long r, long long n0,
     }
 }
 
+// A row of a tile (r < m) to where it goes: a lane has 4 of its first 128 columns and the
+// same 4 of its last.
+template <typename T, typename O, int MODE, int ACT>
+__device__ __forceinline__ void put_row(const Gemm &g, const TilePlace &p, long long r,
+                                        float (&v)[2][4])
+{
+    const int c = threadIdx.x % 32 * 4;
+    O *const out = static_cast<O *>(g.out[p.which]);
+    const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 4 * sizeof(O));
+    if constexpr (MODE == kForward) {
+        const bool kept = whole && (g.gate.exps || aligned_to(g.gate.data, 4 * sizeof(T))) &&
+                          (g.up.exps || aligned_to(g.up.data, 4 * sizeof(T)));
+        keep4<T>(g.gate, r, p.n0, g.n, kept, v[0]);
+        keep4<T>(g.up, r, p.n0, g.n, kept, v[1]);
+        float h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            h[j] = act_value<ACT, sizeof(T) == 4>(v[0][j]) * v[1][j];
+        put4(out + r * g.n + p.n0 + c, g.n - p.n0 - c, whole, h);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long col = p.n0 + h * kHalf + c;
+            O *const to = out + r * g.n + col;
+            if (g.accumulate)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < g.n)
+                        v[h][j] += to_f32(to[j]);
+            put4(to, g.n - col, whole, v[h]);
+        }
+    }
+}
+
+// f(the activation) where there is one, once.
+template <int MODE, typename F> __device__ __forceinline__ void by_mode(const Gemm &g, F f)
+{
+    if constexpr (MODE == kForward)
+        by_act(g.act, f);
+    else
+        f(std::integral_constant<int, RRA_ACT_RELU>()); // (not used)
+}
+
+// ---------------------------------------------------------------- the kernel
+
+constexpr int kRowFloats = kWide + 4; // of a block's results in shared memory
+
+// T: the type of the call's elements; O: of the outputs.
+template <typename T, typename O, int MODE>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
+{
+    constexpr bool F32 = sizeof(T) == 4, HALF = std::is_same<T, __half>::value;
+    constexpr bool A_ROWS = MODE == kDw, B_ROWS = MODE != kForward;
+    constexpr int TALL = kTall<F32>, MT = TALL / 32, kAhead = kStages - 1;
+    static_assert(TALL * kRowFloats * 4 <= kStages * kStageBytes<F32>, "results fit");
+    extern __shared__ __align__(1024) unsigned char raw[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int wm = warp / 4 * (TALL / 2), wn = warp % 4 * 64; // the warp's results
+    const int split = blockIdx.x / g.tiles, tile = blockIdx.x - split * g.tiles;
+    const TilePlace p = tile_place<MODE, TALL>(g, tile);
+    const int lo = split * g.per_split,
+              hi = min(lo + g.per_split, MODE == kDx ? 2 * g.slices : g.slices);
+    const int steps = (hi - lo) * kProducts<F32>;
+
+    const auto copy = [&](int step) {
+        if (step < steps) {
+            const int q = step % kProducts<F32>, k = lo + step / kProducts<F32>;
+            const int pa = F32 ? plane_a(q) : 0, pb = F32 ? plane_b(q) : 0;
+            const uint32_t a = smem_u32(raw) + step % kStages * kStageBytes<F32>,
+                           b = a + TALL * kSlice * 2;
+            const int from = MODE == kDx && k >= g.slices ? 1 : 0;
+            const long long k0 = (long long)(k - from * g.slices) * kSlice;
+            copy_operand<A_ROWS, TALL, TALL>(a, g.a[MODE == kDw ? p.which : from], pa, p.m0, 0, k0);
+            if (MODE == kForward) {
+                copy_operand<false, kWide, kHalf>(b, g.b[0], pb, p.n0, 0, k0);
+                copy_operand<false, kWide, kHalf>(b, g.b[1], pb, p.n0, kHalf, k0);
+            } else {
+                copy_operand<B_ROWS, kWide, kWide>(b, g.b[from], pb, p.n0, 0, k0);
+            }
+        }
+        copies_sent(); // (an empty one keeps the count)
+    };
+
+    float acc[MT][8][4] = {}, sum[F32 ? MT : 1][8][4] = {};
+    for (int step = 0; step < kAhead; ++step)
+        copy(step);
+    for (int step = 0; step < steps; ++step) {
+        copies_here<kAhead - 1>();
+        __syncthreads(); // all threads' copies of this slice; the last one's stage is free
+        copy(step + kAhead);
+        const uint32_t a = smem_u32(raw) + step % kStages * kStageBytes<F32>,
+                       b = a + TALL * kSlice * 2;
+#pragma unroll
+        for (int k = 0; k < kSlice; k += 16) {
+            uint32_t fa[MT][4], fb[4][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                read_a<A_ROWS, TALL>(a, wm + 16 * i, k, fa[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                read_b<B_ROWS, kWide>(b, wn + 16 * j, k, fb[j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    multiply<HALF>(acc[i][j], fa[i], fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
+        }
+        if (F32 && step % kProducts<F32> == kProducts<F32> - 1)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum[F32 ? i : 0][j][e] += acc[i][j][e];
+                        acc[i][j][e] = 0.0f;
+                    }
+    }
+    copies_here<0>();
+    __syncthreads();
+
+    // through shared memory, for rows as they are written
+    float *const rows = reinterpret_cast<float *>(raw);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float *const v = F32 ? sum[F32 ? i : 0][j] : acc[i][j];
+                *reinterpret_cast<float2 *>(rows + (wm + 16 * i + 8 * e + lane / 4) * kRowFloats +
+                                            wn + 8 * j + lane % 4 * 2) =
+                    make_float2(v[2 * e], v[2 * e + 1]);
+            }
+    __syncthreads();
+    by_mode<MODE>(g, [&](auto act) {
+        for (int row = warp; row < TALL && p.m0 + row < g.m; row += kGemmWarps) {
+            float v[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 q =
+                    *reinterpret_cast<const float4 *>(rows + row * kRowFloats + h * kHalf + lane * 4);
+                v[h][0] = q.x, v[h][1] = q.y, v[h][2] = q.z, v[h][3] = q.w;
+                if (g.splits > 1) // for finish_kernel
+                    *reinterpret_cast<float4 *>(
+                        g.parts + (((long long)tile * g.splits + split) * TALL + row) * kWide +
+                        h * kHalf + lane * 4) = q;
+            }
+            if (g.splits == 1)
+                put_row<T, O, MODE, decltype(act)::value>(g, p, p.m0 + row, v);
+        }
+    });
+}
+
+// ---------------------------------------------------------------- splits
+
+// The sums of a tile's splits added, in their order, and on to where they go: a warp has
+// a row of a tile.  (A launch of its own, with all of the GPU.)
+constexpr int kFinishThreads = 256;
+
 template <typename T, typename O, int MODE>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Gemm g)
 {
     constexpr int kWarps = kFinishThreads / 32, kAhead = 4; // splits on their way
+    constexpr int TALL = kTall<sizeof(T) == 4>;
     const int c = threadIdx.x % 32 * 4;
     dependents_wait();
     dependents_launch();
-    for (long long i = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
-         i < (long long)g.tiles * kSide; i += (long long)gridDim.x * kWarps) {
-        const int tile = (int)(i / kSide), row = (int)(i % kSide);
-        const TilePlace p = tile_place<MODE>(g, tile);
-        const long long r = p.m0 + row;
-        if (r >= g.m)
-            continue;
-        const float *const from = g.parts + ((long long)tile * g.splits * kSide + row) * kSide + c;
-        float v[2][4] = {};
-        for (int k0 = 0; k0 < g.splits; k0 += kAhead) {
-            float4 q[kAhead][2];
+    by_mode<MODE>(g, [&](auto act) {
+        for (long long i = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
+             i < (long long)g.tiles * TALL; i += (long long)gridDim.x * kWarps) {
+            const int tile = (int)(i / TALL), row = (int)(i % TALL);
+            const TilePlace p = tile_place<MODE, TALL>(g, tile);
+            if (p.m0 + row >= g.m)
+                continue;
+            const float *const from =
+                g.parts + ((long long)tile * g.splits * TALL + row) * kWide + c;
+            float v[2][4] = {};
+            for (int k0 = 0; k0 < g.splits; k0 += kAhead) {
+                float4 q[kAhead][2];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
+                for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    q[k][h] = k0 + k < g.splits
-                                  ? __ldcs(reinterpret_cast<const float4 *>(
-                                        from + (long long)(k0 + k) * kSide * kSide + h * kHalf))
-                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int h = 0; h < 2; ++h)
+                        q[k][h] = k0 + k < g.splits
+                                      ? __ldcs(reinterpret_cast<const float4 *>(
+                                            from + (long long)(k0 + k) * TALL * kWide + h * kHalf))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
+                for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[h][0] += q[k][h].x, v[h][1] += q[k][h].y;
-                    v[h][2] += q[k][h].z, v[h][3] += q[k][h].w;
-                }
-        }
-        O *const out = static_cast<O *>(g.out[p.which]);
-        const bool whole = pack_fits(out, (size_t)g.n * sizeof(O), 4 * sizeof(O));
-        if constexpr (MODE == kForward) {
-            const bool kept = whole && (g.gate.exps || aligned_to(g.gate.data, 4 * sizeof(T))) &&
-                              (g.up.exps || aligned_to(g.up.data, 4 * sizeof(T)));
-            keep4<T>(g.gate, r, p.n0, g.n, kept, v[0]);
-            keep4<T>(g.up, r, p.n0, g.n, kept, v[1]);
-            float h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                h[j] = act_of<sizeof(T) == 4>(g.act, v[0][j]) * v[1][j];
-            put4(out + r * g.n + p.n0 + c, g.n - p.n0 - c, whole, h);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const long long col = p.n0 + h * kHalf + c;
-                O *const to = out + r * g.n + col;
-                if (g.accumulate)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (col + j < g.n)
-                            v[h][j] += to_f32(to[j]);
-                put4(to, g.n - col, whole, v[h]);
+                    for (int h = 0; h < 2; ++h) {
+                        v[h][0] += q[k][h].x, v[h][1] += q[k][h].y;
+                        v[h][2] += q[k][h].z, v[h][3] += q[k][h].w;
+                    }
             }
+            put_row<T, O, MODE, decltype(act)::value>(g, p, p.m0 + row, v);
         }
-    }
+    });
 }
 
 // ---------------------------------------------------------------- host
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder()
-{
-    static const EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
-// Boxes of 64 x box_rows elements of the planes of a matrix of 16-bit numbers; what is
-// outside of a plane is read as zero.
-bool make_map(CUtensorMap *m, bool bf16, const Matrix16 &x, int box_rows)
-{
-    const EncodeFn fn = encoder();
-    if (!fn)
-        return false;
-    const long long plane = x.planes > 1 ? x.rows * x.ld : x.ld;
-    const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)x.planes},
-                     strides[2] = {(cuuint64_t)x.ld * 2, (cuuint64_t)plane * 2};
-    const cuuint32_t box[3] = {kSlice, (cuuint32_t)box_rows, 1}, steps[3] = {1, 1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-              const_cast<void *>(x.p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Pairs of blocks that the device runs at a time (the kernels' launches are alike).
-int resident_pairs()
-{
-    static std::mutex mu;
-    static int cached[64] = {};
-    const void *const fn = reinterpret_cast<const void *>(gemm_kernel<__half, __half, kForward>);
-    const int most = std::max(1, num_sms() / 2);
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64)
-        return most;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!cached[dev]) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * most);
-        cfg.blockDim = dim3(kGemmThreads);
-        cfg.dynamicSmemBytes = kGemmSmem;
-        cudaLaunchAttribute at[1] = {};
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (op_allow(fn, kGemmSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            n = most;
-        }
-        cached[dev] = std::min(n, most);
-    }
-    return cached[dev];
-}
-
-template <typename T, typename O, int MODE> cudaError_t launch_gemm(Gemm &g, cudaStream_t st)
+// (Launched without an early start: it begins when what is ahead of it has ended.)
+template <typename T, typename O, int MODE> cudaError_t launch_gemm(const Gemm &g, cudaStream_t st)
 {
     const auto fn = gemm_kernel<T, O, MODE>;
-    cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), kGemmSmem);
+    constexpr int smem = kStages * kStageBytes<sizeof(T) == 4>;
+    cudaError_t e = op_allow(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
-    if ((e = stalled_word(&g.stalled)) != cudaSuccess)
+    fn<<<(unsigned)(g.tiles * g.splits), kGemmThreads, smem, st>>>(g);
+    if ((e = cudaGetLastError()) != cudaSuccess || g.splits == 1)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * std::min(resident_pairs(), g.tiles * g.splits));
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = kGemmSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    if ((e = cudaLaunchKernelEx(&cfg, fn, g)) != cudaSuccess || g.splits == 1)
-        return e;
-    const long long rows = (long long)g.tiles * kSide, warps = kFinishThreads / 32;
+    const long long rows = (long long)g.tiles * kTall<sizeof(T) == 4>, warps = kFinishThreads / 32;
     return launch_chained(finish_kernel<T, O, MODE>,
                           dim3((unsigned)std::min((rows + warps - 1) / warps, num_sms() * 8LL)),
                           kFinishThreads, st, g);
@@ -749,28 +448,29 @@ struct Plan {
     size_t bytes; // of parts
 };
 
-// Few tiles with many slices are split along k.  The time of a launch in steps, as
-// measured: a slice takes 0.28 us a pair, an item 3 us to write out, adding up the splits
-// 4 us and 0.2 more for each.
+// Few tiles with many slices are split along k.  The time of a launch in steps: a
+// slice takes 0.8 us a block, an item 3 us to write out, adding up the splits 4 us
+// and 0.2 more for each.
 Plan plan_of(long long m, long long n, int outputs, long long step_n, long long total, bool f32)
 {
     Plan p = {};
-    const long long tm = (m + kSide - 1) / kSide, tn = (n + step_n - 1) / step_n;
-    if (tm * tn * outputs > 0x3fffffff || total > 0x3fffffff)
+    const int tall = f32 ? kTall<true> : kTall<false>;
+    const long long tm = (m + tall - 1) / tall, tn = (n + step_n - 1) / step_n;
+    if (tm > 0x3fffffff || tn > 0x3fffffff || tm * tn * outputs > 0x3fffffff || total > 0x0fffffff)
         return p;
     p.ok = true;
     p.tiles_m = (int)tm;
     p.tiles_n = (int)tn;
     p.tiles = (int)(tm * tn) * outputs;
-    const int pairs = resident_pairs();
-    const double slice = 0.28 * (f32 ? kProducts<true> : 1);
+    const int sms = num_sms();
+    const double slice = f32 ? 0.4 * kProducts<true> : 0.8;
     double best = 0;
-    for (int s = 1; s <= 64 && (s == 1 || p.tiles * s <= 2 * pairs); ++s) {
+    for (int s = 1; s <= 64 && (s == 1 || p.tiles * s <= 2 * sms); ++s) {
         const int per = (int)((total + s - 1) / s);
         // (a split has some slices, and none is empty)
-        if (s > 1 && (per * (f32 ? kProducts<true> : 1) < 4 || (long long)per * (s - 1) >= total))
+        if (s > 1 && (per < 2 || (long long)per * (s - 1) >= total))
             continue;
-        const double t = (double)((p.tiles * s + pairs - 1) / pairs) * (per * slice + 3) +
+        const double t = (double)((p.tiles * s + sms - 1) / sms) * (per * slice + 3) +
                          (s > 1 ? 4 + 0.2 * s : 0);
         if (s == 1 || t < best) {
             best = t;
@@ -779,7 +479,7 @@ Plan plan_of(long long m, long long n, int outputs, long long step_n, long long 
         }
     }
     if (p.splits > 1)
-        p.bytes = (size_t)p.tiles * p.splits * kSide * kSide * sizeof(float);
+        p.bytes = (size_t)p.tiles * p.splits * tall * kWide * sizeof(float);
     return p;
 }
 
@@ -791,11 +491,11 @@ Plan plan_forward(const FfArgs &a, bool f32)
 }
 Plan plan_dx(const FfGradArgs &a, bool f32)
 {
-    return plan_of(a.rows, a.dim, 1, kSide, 2 * slices_of(a.ff), f32);
+    return plan_of(a.rows, a.dim, 1, kWide, 2 * slices_of(a.ff), f32);
 }
 Plan plan_dw(const FfGradArgs &a, bool f32)
 {
-    return plan_of(a.ff, a.dim, a.dwg && a.dwu ? 2 : 1, kSide, slices_of(a.rows), f32);
+    return plan_of(a.ff, a.dim, a.dwg && a.dwu ? 2 : 1, kWide, slices_of(a.rows), f32);
 }
 
 // g's tiles by the plan; parts: where they are in the stream's scratch.
@@ -814,31 +514,9 @@ bool use_plan(Gemm &g, const Plan &p, long long slices, unsigned char *scratch, 
 
 } // namespace
 
-// Set by a kernel whose wait has run out of time, in host memory: one word for the
-// process, read (and cleared) by the next call.
-cudaError_t stalled_word(unsigned **word)
-{
-    static std::mutex mu;
-    static unsigned *p = nullptr;
-    std::lock_guard<std::mutex> lk(mu);
-    if (!p) {
-        const AllocationAllowed allowed;
-        void *q = nullptr;
-        const cudaError_t e = cudaHostAlloc(&q, 64, cudaHostAllocPortable | cudaHostAllocMapped);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return e;
-        }
-        p = static_cast<unsigned *>(q);
-        *p = 0;
-    }
-    *word = p;
-    return cudaSuccess;
-}
-
 bool gemm_takes(const Matrix16 &x)
 {
-    return aligned_to(x.p, 16) && x.ld % 8 == 0 && x.ld <= (1LL << 38);
+    return aligned_to(x.p, 16) && x.ld % 8 == 0;
 }
 
 size_t gemm_parts(const FfArgs &a, bool f32) { return plan_forward(a, f32).bytes; }
@@ -853,7 +531,6 @@ template <typename T>
 cudaError_t gemm_forward(const FfArgs &a, const Matrix16 (&in)[3], unsigned char *scratch,
                          size_t parts_at, cudaStream_t st)
 {
-    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.rows;
     g.n = a.ff;
@@ -861,10 +538,11 @@ cudaError_t gemm_forward(const FfArgs &a, const Matrix16 (&in)[3], unsigned char
     g.out[0] = a.h;
     g.gate = a.gate;
     g.up = a.up;
-    if (!use_plan(g, plan_forward(a, sizeof(T) == 4), slices_of(a.dim), scratch, parts_at) ||
-        !make_map(&g.a[0], bf16, in[0], kHalf) || !make_map(&g.b[0], bf16, in[1], kHalf) ||
-        !make_map(&g.b[1], bf16, in[2], kHalf))
+    if (!use_plan(g, plan_forward(a, sizeof(T) == 4), slices_of(a.dim), scratch, parts_at))
         return cudaErrorInvalidValue;
+    g.a[0] = in[0];
+    g.b[0] = in[1];
+    g.b[1] = in[2];
     return launch_gemm<T, T, kForward>(g, st);
 }
 
@@ -872,15 +550,16 @@ template <typename T>
 cudaError_t gemm_dx(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
                     size_t parts_at, cudaStream_t st)
 {
-    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.rows;
     g.n = a.dim;
     g.out[0] = a.dx;
-    if (!use_plan(g, plan_dx(a, sizeof(T) == 4), slices_of(a.ff), scratch, parts_at) ||
-        !make_map(&g.a[0], bf16, in[0], kHalf) || !make_map(&g.a[1], bf16, in[1], kHalf) ||
-        !make_map(&g.b[0], bf16, in[2], kSlice) || !make_map(&g.b[1], bf16, in[3], kSlice))
+    if (!use_plan(g, plan_dx(a, sizeof(T) == 4), slices_of(a.ff), scratch, parts_at))
         return cudaErrorInvalidValue;
+    g.a[0] = in[0];
+    g.a[1] = in[1];
+    g.b[0] = in[2];
+    g.b[1] = in[3];
     return launch_gemm<T, T, kDx>(g, st);
 }
 
@@ -888,7 +567,6 @@ template <typename T, typename O>
 cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char *scratch,
                     size_t parts_at, cudaStream_t st)
 {
-    constexpr bool bf16 = !std::is_same<T, __half>::value;
     Gemm g = {};
     g.m = a.ff;
     g.n = a.dim;
@@ -896,10 +574,11 @@ cudaError_t gemm_dw(const FfGradArgs &a, const Matrix16 (&in)[5], unsigned char 
     g.out[1] = a.dwu;
     g.accumulate = a.accumulate;
     g.first_out = a.dwg ? 0 : 1;
-    if (!use_plan(g, plan_dw(a, sizeof(T) == 4), slices_of(a.rows), scratch, parts_at) ||
-        !make_map(&g.a[0], bf16, in[0], kSlice) || !make_map(&g.a[1], bf16, in[1], kSlice) ||
-        !make_map(&g.b[0], bf16, in[4], kSlice))
+    if (!use_plan(g, plan_dw(a, sizeof(T) == 4), slices_of(a.rows), scratch, parts_at))
         return cudaErrorInvalidValue;
+    g.a[0] = in[0];
+    g.a[1] = in[1];
+    g.b[0] = in[4];
     return launch_gemm<T, O, kDw>(g, st);
 }
 
