@@ -510,3 +510,93 @@ def test_ff_calls_behind_one_another_and_behind_their_inputs_writers():
             seen.append(h.clone())
         for k, s in enumerate(seen):
             assert torch.equal(s, want[k % 2])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,ff", [(40, 72, 300), (300, 520, 1032)])
+def test_ff_grad_carries_nan_where_it_belongs(rows, dim, ff, t):
+    """A block of codes that is not finite: its row of dx, its columns of the weights'
+    gradients, and nothing else."""
+    dh, x, w, kept = grad_inputs(rows, dim, ff, t, "bits8")
+    kept[0].exps[3, 1] = -128
+    kept[0].codes[3, 128:256] = 0
+    dgate, dup, h = (torch.empty_like(dh) for _ in range(3))
+    dx, dw = torch.empty_like(x), [torch.empty_like(v) for v in w]
+    rra.gated_ff_grad(dh, x, *w, *kept, dgate, dup, dx=dx, dw_gate=dw[0], dw_up=dw[1], h=h)
+    for v in (dgate, dup, h):
+        bad = torch.zeros_like(v, dtype=torch.bool)
+        bad[3, 128:256] = True
+        assert torch.equal(torch.isnan(v), bad)
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[3] = True
+    assert torch.equal(torch.isnan(dx).all(1), bad) and torch.equal(torch.isnan(dx).any(1), bad)
+    for v in dw:
+        bad = torch.zeros(ff, dtype=torch.bool, device="cuda")
+        bad[128:256] = True
+        assert torch.equal(torch.isnan(v).all(1), bad) and torch.equal(torch.isnan(v).any(1), bad)
+
+
+def test_ff_first_call_of_a_process_in_a_capture():
+    """Calls that need no scratch may be captured without having been made before."""
+    import subprocess
+    import sys
+    code = """
+import torch, ring_allreduce_compressed_gb300 as rra
+x = torch.randn(300, 64, device="cuda").bfloat16()
+w = [torch.randn(128, 64, device="cuda").bfloat16() for _ in range(2)]
+h, few = torch.zeros(300, 128, device="cuda").bfloat16(), torch.zeros(3, 128, device="cuda").bfloat16()
+s, m, r = rra.Saved.empty(300, 64), *(torch.empty(300, device="cuda") for _ in range(2))
+y = torch.empty_like(x)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    rra.gated_ff(x, *w, h)
+    rra.gated_ff(x[:3], *w, few)
+    rra.layer_norm_save(x, None, None, y, s, m, r)
+    rra.layer_norm_restore(s, y)
+g.replay()
+torch.cuda.synchronize()
+want = torch.nn.functional.silu(x.float() @ w[0].float().t()) * (x.float() @ w[1].float().t())
+for got, ref in ((h, want), (few, want[:3])):
+    assert float((got.float() - ref).norm() / ref.norm()) < 1e-2
+assert float((y.float() - x.float()).norm() / x.float().norm()) < 2e-2
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_ff_in_two_threads_at_once():
+    """Two threads with a stream each, scratch that grows among the calls."""
+    import threading
+    jobs = []
+    for k, t in enumerate(("bf16", "f32")):
+        sizes = [(100 + 50 * k, 99, 301), (200, 515, 129), (300, 1030, 257)]
+        jobs.append([(randn((r, d), 1, 1.0, t), weights(d, f, t)) for r, d, f in sizes])
+    want = [[torch.empty(x.shape[0], w[0].shape[0], dtype=x.dtype, device="cuda") for x, w in j]
+            for j in jobs]
+    for j, ws in zip(jobs, want):
+        for (x, w), o in zip(j, ws):
+            rra.gated_ff(x, *w, o)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(j, ws):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    for (x, w), o in zip(j, ws):
+                        h = torch.empty_like(o)
+                        rra.gated_ff(x, *w, h)
+                        assert torch.equal(h, o)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
