@@ -128,7 +128,7 @@ template <typename T> cudaError_t act_grad(const FfGradArgs &a, cudaStream_t st)
     });
 }
 
-// ---------------------------------------------------------------- operands for tensor maps
+// ---------------------------------------------------------------- operands for the products
 
 // A matrix whose rows do not begin on 16-byte boundaries, copied to rows that do; one
 // of fp32 numbers cut into three planes of bf16, 8 bits of each number in the first,
@@ -189,7 +189,7 @@ template <typename T> __global__ void __launch_bounds__(kActThreads) operand_ker
     }
 }
 
-// Operands as tensor maps can read them: where they are, or in the stream's scratch,
+// Operands as the products can read them: where they are, or in the stream's scratch,
 // where the products' own parts are, too.
 template <typename T, int N> class Operands {
 public:

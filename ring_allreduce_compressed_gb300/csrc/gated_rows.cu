@@ -236,16 +236,11 @@ cudaError_t rows_call(const FfArgs &a, float *wide, cudaStream_t st)
 
 } // namespace
 
-// The large kernel takes over where it is faster: at dim 2048, ff 8192 bf16, 17 us here with
-// 16 rows and 20 with 17, 18 there with any (x fills L1 here); but for operands that it
-// would have to copy first (1000 x 3001: 12 us here and 24 there with 64 rows).
-template <typename T> bool few_rows(const FfArgs &a)
-{
-    bool maps = sizeof(T) == 2;
-    for (const void *p : {a.x, a.wg, a.wu})
-        maps = maps && gemm_takes({p, a.rows, a.dim, a.dim, 1});
-    return a.rows <= (maps || sizeof(T) == 4 ? 16 : 64);
-}
+// The large kernel takes over where this one is no faster (2048 x 8192 fp16: 20 us here
+// with 17 rows, 28 with 48, 36 with 64, 35-37 there with 17 to 64; 4096 x 16384 bf16: 64,
+// 85, 120 here, 115 there; 512 x 1024: 7 here with 64, 12 there with 65).  fp32 has no
+// variant for more than 16 rows (4096 x 16384: 380 us with 16, 694 there with 17).
+template <typename T> bool few_rows(const FfArgs &a) { return a.rows <= (sizeof(T) == 2 ? 64 : 16); }
 
 template <typename T> rra_status rows_forward(const FfArgs &a, cudaStream_t st)
 {
