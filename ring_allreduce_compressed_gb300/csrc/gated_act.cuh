@@ -6,7 +6,7 @@
 //   gelu       a = g P(g)                 a' = P + g p(g)
 //   gelu_tanh  a = g s(2z), z = sqrt(2/pi) (g + 0.044715 g^3): the form with tanh,
 //              since 1 + tanh z = 2 s(2z), without its cancellation below zero
-//              a' = s (1 + 2 g (1 - s) z')
+//              a' = s + 2 g s (1 - s) z'
 //   relu       a = max(g, 0)              a' = 1 for g > 0, else 0
 #pragma once
 
@@ -63,9 +63,10 @@ template <int ACT, bool EXACT> __device__ __forceinline__ float act_both(float g
         return g * p;
     } else if constexpr (ACT == RRA_ACT_GELU_TANH) {
         const float s = gelu_logistic<EXACT>(g);
-        // (the square of a finite g may be infinite where 1 - s is 0)
+        // g^3 of a finite g may be infinite where s (1 - s) is 0: the square is bounded, and
+        // what is 0 is multiplied in ahead of z'
         const float dz = kGeluSlope * fmaf(3.0f * kGeluCubic, fminf(g * g, 1e30f), 1.0f);
-        *slope = s * fmaf(g * (1.0f - s), dz, 1.0f);
+        *slope = fmaf(g * (s * (1.0f - s)), dz, s);
         return g * s;
     } else {
         *slope = g > 0.0f ? 1.0f : 0.0f;
