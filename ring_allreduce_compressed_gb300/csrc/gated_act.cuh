@@ -19,12 +19,16 @@
 namespace rra {
 
 // EXACT: for fp32 results.  16-bit ones are as near with the fast exponential and
-// quotient, whose errors (2^-21) are a 1000th of a half step of theirs.
+// quotient: the exponential misses by 2 + 1.2 |g| units of its last place, the quotient
+// by 2, together below 2^-16 of s as far as s is an fp32 number, and below 2^-18 where
+// g s is one of fp16: a hundredth of the results' own half step.  Both sides of the
+// quotient are quarters, exactly: it is 0 for denominators above 2^126, and those up to
+// 2^128 (g down to -88.7) have results that bf16 holds.
 template <bool EXACT> __device__ __forceinline__ float logistic(float g)
 {
     if (EXACT)
         return 1.0f / (1.0f + expf(-g));
-    return __fdividef(1.0f, 1.0f + __expf(-g));
+    return __fdividef(0.25f, fmaf(0.25f, __expf(-g), 0.25f));
 }
 
 constexpr float kGeluSlope = 1.5957691216057308f; // 2 sqrt(2 / pi)

@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import ring_allreduce_compressed_gb300 as rra
-from saved_util import saved_of, values
-from test_gpu_operators import DT
+from saved_util import act, saved_of, values
+from test_gpu_operators import DT, UT
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,44 @@ def test_slopes_far_out_are_0_or_1(name, keep, t):
     # columns of negative gates alone: no gradient, and none of it NaN
     assert (dw[0][1::2] == 0).all() and (dw[1][1::2] == 0).all()
     assert (dw[0][::2] == rows).all()
+
+
+# silu's argument, and sums of two numbers of 8 bits whose gelu_tanh has such an argument
+EDGE = {"silu": [(-87.0, 0.0), (-87.5, 0.0), (-88.0, 0.0), (-88.5, 0.0)],
+        "gelu_tanh": [(-9.75, 0.0), (-10.0, -0.015625), (-10.0, -0.03125), (-10.0, -0.046875)]}
+
+
+@pytest.mark.parametrize("rows", [4, 300])
+@pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
+def test_quotients_of_large_denominators(name, rows):
+    """1 + e^-z between 2^126 and 2^128: the logistic function is below the normal numbers of
+    fp32, and the activation is one of bf16 (some 2^-121).
+
+    e^-z misses by 2 + 1.2 |z| units of its last place, 2^-23 each, z by 4 roundings, which count
+    |z| times, the quotient by 2 units and by half of fp32's least number of 2^-128: in all
+    less than (2 + 1.2 * 89) * 2^-23 + 4 * 89 * 2^-24 + 2^-20 < 2^-14 of the result."""
+    pairs = EDGE[name]
+    x = torch.tensor([[a, b, 1.0] for a, b in pairs], device="cuda").bfloat16()
+    x = x.repeat(rows // len(pairs), 1)
+    wg = torch.tensor([[1.0, 1.0, 0.0]] * 5, device="cuda").bfloat16()
+    wu = torch.tensor([[0.0, 0.0, 1.0]] * 5, device="cuda").bfloat16()
+    h = torch.empty(rows, 5, dtype=torch.bfloat16, device="cuda")
+    rra.gated_ff(x, wg, wu, h, act=name)
+    want = act(name, x.double() @ wg.double().t())[0]
+    assert (want < -2.0 ** -125).all()
+    assert ((h.double() - want).abs() <= (UT[torch.bfloat16] + 2.0 ** -14) * want.abs()).all()
+
+
+def test_slopes_of_large_denominators():
+    """The same for silu's derivative, from gates kept whole and in 8 bits."""
+    gate = torch.tensor([[-87.0, -87.5, -88.0, -88.5]], device="cuda").bfloat16().repeat(3, 50)
+    dh, up = torch.ones_like(gate), torch.ones_like(gate)
+    x, w = torch.ones_like(gate[:, :8]), torch.ones(200, 8, device="cuda").bfloat16()
+    for kept in ((gate, up), tuple(saved_of(v.double()) for v in (gate, up))):
+        dgate, dup = torch.empty_like(dh), torch.empty_like(dh)
+        rra.gated_ff_grad(dh, x, w, w, *kept, dgate, dup)
+        g = values(kept[0]) if isinstance(kept[0], rra.Saved) else gate.double()
+        a, slope, _ = act("silu", g)
+        for got, want in ((dgate, slope), (dup, a)):
+            err = (UT[torch.bfloat16] + 2.0 ** -14) * want.abs()
+            assert ((got.double() - want).abs() <= err).all()
