@@ -796,11 +796,15 @@ typedef enum {
  * Arrays of 16-byte alignment with dim a multiple of 16 bytes run fastest; others
  * of 16-bit types, and fp32 ones of more than 16 rows, are laid out anew in
  * scratch memory first (2 or 6 bytes an element of x, w_gate and w_up).
- * Products run on tensor cores, whose fp32 sums are cut off and not rounded at
- * every 16 elements of k: by less than 2^-24 k / 16 of the sum of magnitudes.
- * fp32 operands are multiplied as three parts of 8 bits each, and sums of more
- * than 64 elements of k put together by rounded additions: an infinity among
- * them may give NaN.
+ * Products run on tensor cores.  Each instruction adds 16 products to an fp32 sum and
+ * cuts what it adds 25 bits below the largest one's leading bit, and the sum to 24 bits
+ * (as measured), where additions would round.  Sums of k products of 16-bit operands
+ * are within 2^-24 k (k in whole sixteens) of the sum of the products' magnitudes; on
+ * operands of one sign, where all cuts add up, 2^-27 k was measured.  fp32 operands are
+ * multiplied as three parts of 8 bits each, without the three smallest of the nine
+ * products (less than 2^-21 of the whole one), and sums of more than 64 elements of k
+ * put together by rounded additions: within 2^-18 + 2^-29 k of that sum.  An infinity
+ * among them may give NaN.
  * Errors: RRA_ERR_INVALID (NULL, bad enums, dim or ff 0, rows, dim or ff above
  * 2^30, an array of more than 64 TB, an output that overlaps an input or another
  * output), RRA_ERR_NOMEM, RRA_ERR_CUDA.
@@ -827,6 +831,9 @@ rra_status rra_gated_ff(const void *x, const void *w_gate, const void *w_up, siz
  *                 added to what they hold, in fp32.
  * x is not read when both weights' gradients are NULL, the weights not when dx is.
  * Arrays are laid out anew as in rra_gated_ff, dgate and dup among them.
+ * Sums are as far off as rra_gated_ff's, with k = 2 ff for dx and k = rows for the
+ * weights' gradients, whose fp32 sums of 16-bit operands run over all rows: of many rows
+ * (2^-27 * 65,536 = 2^-11), calls on parts of them that accumulate are nearer.
  * Errors: as rra_gated_ff.
  */
 rra_status rra_gated_ff_grad(const void *dh, const void *x, const void *w_gate, const void *w_up,
