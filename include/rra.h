@@ -604,10 +604,10 @@ rra_status rra_debug_withhold(rra_comm *comm, int rank, int step);
  *    rounded to its type once, to nearest even.  Equal calls give equal bits.
  *  - Infinities and NaN are carried through as the formulas have it.
  *  - rra_grad_norm, rra_grad_clip, rra_embedding_grad, rra_layer_norm_grad,
- *    rra_layer_norm_saved_grad, rra_gated_ff and rra_gated_ff_grad use scratch memory that the library keeps per device
- *    and stream (cudaStreamPerThread: per thread) and allocates with
- *    cudaMalloc when a call needs more than it holds (it at least doubles when
- *    it grows).  What it replaces, then or when a destroyed stream's handle
+ *    rra_layer_norm_saved_grad, rra_gated_ff and rra_gated_ff_grad use scratch
+ *    memory that the library keeps per device and stream (cudaStreamPerThread:
+ *    per thread) and allocates with cudaMalloc when a call needs more than it
+ *    holds (it at least doubles when it grows).  What it replaces, then or when a destroyed stream's handle
  *    comes back, it frees with cudaFree, which waits for the device, unless a
  *    captured graph may hold it: that is kept until the process ends.  A call
  *    that would have to allocate while its stream is being captured returns

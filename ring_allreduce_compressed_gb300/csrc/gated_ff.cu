@@ -27,8 +27,8 @@ constexpr int kActThreads = 256;
 
 // Packs of 8 elements of a row; SAVED: gate and up in 8 bits.  Every element is read
 // before it is written, so outputs may take inputs' places.  Bound by memory: 8192 x 16384
-// bf16 from 8 bits take 180 us (1.08 GB, 6.0 TB/s).  WHOLE: every pack is on a 16-byte
-// boundary.
+// bf16 from 8 bits take 187 us without h (1.08 GB, 5.8 TB/s) and 214 with it (1.34 GB,
+// 6.3 TB/s).  WHOLE: every pack is on a 16-byte boundary.
 template <typename T, bool SAVED, bool WHOLE, int ACT>
 __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const FfGradArgs a, int lanes)
 {

@@ -15,7 +15,6 @@
 #include "op_common.cuh"
 #include "ragged.cuh"
 #include "saved.cuh"
-#include "stream_slot.h"
 
 namespace rra {
 namespace {

@@ -5,14 +5,13 @@
 // Bound by the weights, which are read once: every warp reads 16 rows of them (8 of
 // gate, the same 8 of up) straight into registers, 16 bytes a lane, and multiplies
 // them with all rows of x, which stay in L1.  4096 x 16384 bf16: 41 us with one row
-// (6.5 TB/s), 49 with 16; fp32 82 us with one (6.5 TB/s), 130 with 8.  Few rows fill no
-// tile of the large kernel, and each of its copies takes 128 bytes of 128 rows.
+// (6.5 TB/s), 49 with 16; fp32 82 us with one (6.5 TB/s), 130 with 8.  The large kernel's
+// tiles have 128 rows (fp32: 64), which few rows leave empty.
 //
 // 16 bits: one warp-wide product takes 16 weight rows x 16 elements of k x 8 rows of x.
 // Its k may be any 16 as long as both sides agree: a lane's 8 neighbouring elements
-// count as those that it holds in two products, so nothing is rearranged.  (These
-// products run on the older tensor path, at a part of the full rate, of which
-// reading needs less than a tenth.)  fp32: paired fp32 operations, the same layout.
+// count as those that it holds in two products, so nothing is rearranged.  (The
+// large kernel's instruction; with one row its pipe is busy 9 % of the time.)  fp32: paired fp32 operations, the same layout.
 #include "gated_ff.h"
 
 #include "gated_act.cuh"
@@ -236,10 +235,11 @@ cudaError_t rows_call(const FfArgs &a, float *wide, cudaStream_t st)
 
 } // namespace
 
-// The large kernel takes over where this one is no faster (2048 x 8192 fp16: 20 us here
-// with 17 rows, 28 with 48, 36 with 64, 35-37 there with 17 to 64; 4096 x 16384 bf16: 64,
-// 85, 120 here, 115 there; 512 x 1024: 7 here with 64, 12 there with 65).  fp32 has no
-// variant for more than 16 rows (4096 x 16384: 380 us with 16, 694 there with 17).
+// The large kernel takes over where this one is hardly faster, or already 4 % slower
+// (2048 x 8192 fp16: 20 us here with 17 rows, 28 with 48, 36 with 64, 35-37 there with 17
+// to 64; 4096 x 16384 bf16: 64, 85, 120 here, 115 there; 512 x 1024: 7 here with 64, 12
+// there with 65).  fp32 has no variant for more than 16 rows (4096 x 16384: 380 us
+// with 16, 694 there with 17).
 template <typename T> bool few_rows(const FfArgs &a) { return a.rows <= (sizeof(T) == 2 ? 64 : 16); }
 
 template <typename T> rra_status rows_forward(const FfArgs &a, cudaStream_t st)

@@ -12,8 +12,9 @@
 //
 // Bound by memory: one pass over what is read and written, 8 bits of the saved
 // row among it.  Measured at 16384 x 4096 bf16: save 60 us (338 MB, 5.6 TB/s), restore 37 us
-// (202 MB, 5.5 TB/s), gradient 75 us (338 MB, 4.5 TB/s: issue slots 56 % and 12 warps an SM,
-// 5 of the 75 for adding the partial rows); 3001 x 1001 fp32: restore 7.4 us, gradient 15.6.
+// (202 MB, 5.5 TB/s), gradient 75 us (338 MB, 4.5 TB/s: latency, with 12 warps an SM, one row
+// ahead and issue slots busy 56 %; 5 of the 75 for adding the partial rows); 3001 x 1001 fp32:
+// restore 7.4 us, gradient 15.6.
 #include "op_common.cuh"
 #include "ragged.cuh"
 #include "row_group.cuh"
@@ -234,7 +235,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < K; ++k)
             special = special || special_block(top[k]);
-        // (one question a row: asked for every pack, its ways apart cost more than the codes)
+        // (one question a row: asked for every pack, its ways apart cost more than the codes.
+        // Packs behind the row are zero, and so special: rows that leave some of a warp's
+        // packs empty take the general code, as rows of zeros do.  About 200 MB of bf16: 76 us
+        // with rows of 1536, 66 with 1024)
         const bool plain = !__any_sync(kFull, special);
         int8_t *const codes = a.codes + (r * packs + u0) * kPack;
         int8_t *const exps = a.exps + r * nb + u0 / kBlockPacks;
@@ -298,7 +302,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSaveThreads ? 2 : 1)
     }
 }
 
-// Rows that no block holds: passes over each, the later ones from L2.
+// Rows that no block holds: passes over each, the later ones from L2, element by element
+// (1024 x 65536 bf16: 190 us).
 constexpr int kLongThreads = 1024;
 
 template <typename T, typename W>
@@ -847,7 +852,8 @@ __device__ __forceinline__ void normal8(const SavedGrad &a, long long r, long lo
         xh[j] = (xh[j] - mu) * rs;
 }
 
-// Rows that no block holds: dx by two passes over a row, the second from L2.
+// Rows that no block holds: dx by two passes over a row, the second from L2 (with the
+// weights' sums, 1024 x 65536 bf16: 237 us).
 template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) saved_dx_kernel(const SavedGrad a)
 {
