@@ -3,7 +3,8 @@ of one sign, where whatever an instruction cuts off adds up: the bounds that the
 
 An instruction adds 16 products to an fp32 sum.  It cuts every addend 25 bits below the
 leading bit of the largest, less than 2^-25 of it each, and the result to 24 bits, less than
-2^-23: 16 * 2^-25 + 2^-23 < 2^-20 of the sum of magnitudes at every 16 elements of k.  Sums
+2^-23: 16 * 2^-25 + 2^-23 < 2^-20 of the sum of magnitudes at every 16 elements of k.  (The
+leading bit goes by the operands' exponents, so subnormal ones count as the least normal number.)  Sums
 of splits and warps are added with roundings of 2^-24, one for 128 elements or more, which
 the bound has room for.  fp32: four such instructions of the largest parts of a slice of
 64 elements, on that slice's part of the sum: 4 * 5 * 2^-23; those of the smaller parts come
@@ -13,7 +14,7 @@ import pytest
 import torch
 
 import ring_allreduce_compressed_gb300 as rra
-from test_gpu_operators import DT, U, gen
+from test_gpu_operators import DT, U, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +62,26 @@ def test_small_addends_behind_a_large_one(j, t):
     got = weights_grad(dh, x).double()
     want = 2.0 ** 24 + 16 * 128 * (2 - 2.0 ** -6) * 2.0 ** -j
     assert ((got - want).abs() <= bound(rows, t) * want).all()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 40, 1000])
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("both", [False, True])
+def test_sums_of_subnormal_numbers(both, t, rows):
+    """One operand, or both, down to the type's least number."""
+    least = torch.finfo(DT[t]).tiny
+    def tiny(shape, seed):  # noqa: E306
+        e = torch.rand(shape, generator=gen(seed + 9), device="cuda", dtype=torch.float64)
+        v = torch.randn(shape, generator=gen(seed), device="cuda", dtype=torch.float64)
+        return (v * least * 2.0 ** torch.floor(16 * e - 10)).to(DT[t])
+    dh = tiny((rows, 200), 1)
+    # (products of two subnormal numbers of bf16 are no fp32 numbers)
+    x = tiny((rows, 520), 2) if both and t == "f16" else randn((rows, 520), 2, 1.0, t)
+    got, want = weights_grad(dh, x).double(), dh.double().t() @ x.double()
+    size = dh.double().abs().clamp(min=least).t() @ x.double().abs().clamp(min=least)
+    assert ((got - want).abs() <= bound(rows, t) * size + 2.0 ** -149).all()
+    if rows == 1 and t == "f16":
+        assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("dim", [7, 64, 1000, 8192])
